@@ -37,6 +37,9 @@
  *     [2, 252] (not checked), which keeps every scaled weight an exact bf16 value.  The weight
  *     bytes are passed in the library's tiled layout, made once by moe_mxfp4_tile from the
  *     row-major one; the scales stay row-major.
+ *     int8 weights carry one fp32 scale per output channel: s_gate, s_up [E][d_ff], s_down
+ *     [E][d_model]; the weight's value is code * scale.  The bytes are passed in the same tiled
+ *     layout as fp8's, made once by moe_fp8_tile.
  *   - Return value: MOE_OK or an error code; moe_status_string() names it.  Arguments are checked
  *     on the host only (null pointers, sizes, 16-byte alignment, workspace size).  Device data is
  *     not validated: non-finite logits or out-of-range expert ids are undefined behaviour.
@@ -75,11 +78,15 @@ enum moe_dtype {
   MOE_DTYPE_MXFP4 = 2, /* expert weights only: bf16 activations, no shared expert, streaming tiles
                           only (config MOE_CONFIG_MFMA and has_shared give MOE_ERR_UNSUPPORTED).
                           e_gate, e_up and e_down must be 4-byte aligned */
-  MOE_DTYPE_MXFP4_A8 = 3 /* MXFP4 expert weights with MXFP8 activations: the layer quantises x (and
+  MOE_DTYPE_MXFP4_A8 = 3, /* MXFP4 expert weights with MXFP8 activations: the layer quantises x (and
                             the SwiGLU output h) per token and 32 channels to E4M3 with one E8M0
                             scale each (the smallest scale 2^E with amax <= 448 * 2^E), and both
                             GEMMs run on the scaled f8f6f4 MFMA.  No shared expert; e_* 4-byte
                             aligned; MOE_CONFIG_MFMA is supported (256 x 256 LDS-staged tiles) */
+  MOE_DTYPE_INT8 = 4 /* int8 expert weights with one fp32 scale per output channel, int8 activations
+                        with one per token (moe_quant_act_i8): the layer quantises x, and the SwiGLU
+                        output h (fp32) over all of its d_ff columns; sums are int32, exact.  d_model,
+                        d_ff and d_ff_shared <= 32768; the scale arrays 16-byte aligned */
 };
 
 /* Tile configuration for the expert GEMMs.  MOE_CONFIG_AUTO lets the device pick per expert and per
@@ -140,19 +147,19 @@ typedef struct moe_weights {
   const void* w_gate; /* [E][f][d] bf16 or e4m3 */
   const void* w_up;   /* [E][f][d] */
   const void* w_down; /* [E][d][f] */
-  const float* s_gate; /* fp8 only: [E][f/128][d/128]; NULL for bf16 */
+  const float* s_gate; /* fp8: [E][f/128][d/128]; int8: [E][f]; NULL for bf16 */
   const float* s_up;
-  const float* s_down; /* [E][d/128][f/128] */
+  const float* s_down; /* fp8: [E][d/128][f/128]; int8: [E][d] */
   const void* sh_gate; /* shared expert (has_shared), [f_sh][d], same dtype */
   const void* sh_up;
   const void* sh_down; /* [d][f_sh] */
-  const float* s_sh_gate; /* fp8 only */
+  const float* s_sh_gate; /* fp8 and int8 ([f_sh], [f_sh], [d]) */
   const float* s_sh_up;
   const float* s_sh_down;
   const uint8_t* e_gate; /* mxfp4 only: E8M0 scales [E][f][d/32]; NULL otherwise */
   const uint8_t* e_up;
   const uint8_t* e_down; /* [E][d][f/32] */
-  int32_t layout;        /* enum moe_layout of w_* and sh_*: MOE_LAYOUT_TILED for fp8 and mxfp4,
+  int32_t layout;        /* enum moe_layout of w_* and sh_*: MOE_LAYOUT_TILED for fp8, int8 and mxfp4,
                             MOE_LAYOUT_ROW_MAJOR for bf16 */
 } moe_weights;
 
@@ -181,7 +188,7 @@ int moe_route(const float* logits, int T, int E, int k, int32_t* topk_ids, float
  * increasing s inside each expert (stable); slot_dst[s] = row.  If x_perm is not NULL, also gathers
  * x_perm[row] = x[perm_src[row] / k]: act_dtype MOE_DTYPE_BF16 copies d bf16 values per row;
  * MOE_DTYPE_FP8_E4M3 copies d e4m3 bytes per row and, if x_perm_scale is not NULL, the d/128 fp32
- * scales per row from x_scale.
+ * scales per row from x_scale; MOE_DTYPE_INT8 d int8 bytes and the row's one scale.
  *   topk_ids [T][k] int32 in [0, E).  ws: moe_permute_workspace_bytes(T, E, k) bytes. */
 int moe_permute(const int32_t* topk_ids, int T, int E, int k, const void* x, const float* x_scale,
                 int d, int act_dtype, int32_t* counts, int32_t* offsets, int32_t* perm_src,
@@ -208,7 +215,8 @@ int moe_quant_act_mx(const void* x, int T, int d, uint8_t* xq, uint8_t* xe, hipS
  * lands in the same rows of y_perm ([rows][d] bf16, rows = offsets[E]).  bf16 weights: x_perm is
  * bf16 and x_perm_scale NULL (also for mxfp4 weights; MOE_DTYPE_MXFP4_A8 quantises those bf16 rows
  * to MXFP8 itself).  fp8 weights: x_perm is e4m3 with x_perm_scale [rows][d/128]; the
- * SwiGLU output is requantised to e4m3 per row and 128 channels before the down GEMM.  Tile
+ * SwiGLU output is requantised to e4m3 per row and 128 channels before the down GEMM.  int8
+ * weights: x_perm is int8 with x_perm_scale [rows]; h is requantised per row.  Tile
  * shapes are chosen on the device from counts (p->config may force one family).  The shared expert
  * fields of p and w are ignored here.
  *   ws: moe_grouped_ffn_workspace_bytes(p) bytes (rows = T*k of p).  For bf16 weights it includes
@@ -281,6 +289,70 @@ int moe_layer_traced(const moe_problem* p, const float* logits, const void* x,
 int moe_layer_noalloc(const moe_problem* p, const float* logits, const void* x,
                       const moe_weights* w, void* out, const moe_routing* keep,
                       hipStream_t stream);
+
+/* int8 activation quantisation (MOE_DTYPE_INT8): per token, s = fp32(amax / 127) (s = 1 when amax is 0
+ * or the quotient underflows to 0), q = round(x / s), ties to even, in [-127, 127].  A row holding an
+ * infinity or NaN gets s = NaN and zero codes, so whatever is computed from it is NaN.  Also for
+ * weights at load time: rows [N][K] -> per-channel codes and scales.
+ *   x [T][d] bf16 -> xq [T][d] int8, xs [T] fp32.  d % 16 == 0, d <= 32768; x, xq 16-byte aligned. */
+int moe_quant_act_i8(const void* x, int T, int d, int8_t* xq, float* xs, hipStream_t stream);
+
+/* Dense product of int8 rows: y[m][n] = bf16(xs[m] * ws[n] * sum_k xq[m][k] * wq[n][k]), the sum in
+ * int32 (exact), the scaling in fp32, one rounding.
+ *   xq [M][K], xs [M], wq [N][K] in the tiled layout (moe_fp8_tile), ws [N], y [M][N] bf16.
+ *   N % 16 == 0, K % 128 == 0, K <= 32768, M * K and N * K < 2^32, else MOE_ERR_UNSUPPORTED; every
+ *   pointer but xs 16-byte aligned.  M = 0 is a no-op. */
+int moe_gemm_i8(const int8_t* xq, const float* xs, int M, const int8_t* wq, const float* ws, int N,
+                int K, void* y, hipStream_t stream);
+
+/* RMS norm in front of the layer: h = bf16(x + residual) (h = x when residual is NULL),
+ * y = h / sqrt(mean(h^2) + eps) * weight, in fp32 (the sum of squares in fp64).
+ *   x, residual [T][d] bf16, weight [d] bf16, eps >= 0.
+ *   h_out [T][d] bf16 or NULL: the new residual stream; it may be x or residual itself.
+ *   y [T][d] bf16 (may be NULL when there is an 8-bit output).
+ *   act_dtype names the weight format whose activations q and q_scale receive, quantised from the
+ *   fp32 y in one rounding: MOE_DTYPE_BF16 none (q, q_scale ignored); MOE_DTYPE_FP8_E4M3 e4m3 with fp32
+ *   scales [T][d/128] (d % 128 == 0); MOE_DTYPE_MXFP4_A8 e4m3 with E8M0 scales [T][d/32] (d % 32 == 0);
+ *   MOE_DTYPE_INT8 int8 with fp32 scales [T] (d % 16 == 0) -- each by the rules of moe_quant_act,
+ *   moe_quant_act_mx and moe_quant_act_i8.
+ * d % 8 == 0 and d <= 32768, else MOE_ERR_UNSUPPORTED; pointers 16-byte aligned.  A row whose sum of
+ * squares is not finite (an infinity or NaN in it, or |h| above about 2^60) gives NaN in all of its y,
+ * NaN codes (e4m3) or a NaN scale (int8); other rows are not affected. */
+int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int T, int d,
+                int act_dtype, void* h_out, void* y, void* q, void* q_scale, hipStream_t stream);
+
+/* Gradient of moe_rmsnorm's y: with n = h / sqrt(mean(h^2) + eps) and g = dy * weight,
+ *   dx = (g - n * mean(g * n)) / sqrt(mean(h^2) + eps) (+ dh), rounded once to bf16: the gradient of
+ *   x and of residual alike; dweight[c] = sum_t dy[t][c] * n[t][c], fp32, in a fixed order.
+ *   dy [T][d] bf16; dh [T][d] bf16 or NULL: what arrives at h_out; h [T][d]: the h_out (or x) of the
+ *   forward call.  dx [T][d] bf16 (may be dy or dh itself); dweight [d] or NULL (T = 0: zeros).
+ *   ws: moe_rmsnorm_grad_workspace_bytes(T, d) bytes, needed only for dweight.
+ *   d % 8 == 0, d <= 16384, else MOE_ERR_UNSUPPORTED (and 0 bytes). */
+int moe_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* weight, float eps,
+                     int T, int d, void* dx, float* dweight, void* ws, size_t ws_bytes,
+                     hipStream_t stream);
+size_t moe_rmsnorm_grad_workspace_bytes(int T, int d);
+
+/* Gradient of moe_route's weights: dlogits[t][e] = sum over the slots j with topk_ids[t][j] = e of
+ * w_j * (dw_j - sum_i w_i * dw_i), 0 for an expert that was not selected (the selection itself has no
+ * gradient).  topk_ids, topk_w, dtopk_w [T][k]; dlogits [T][E] fp32, written whole. */
+int moe_route_grad(const int32_t* topk_ids, const float* topk_w, const float* dtopk_w, int T, int E,
+                   int k, float* dlogits, hipStream_t stream);
+
+/* Gradient of moe_combine: dy_perm[slot_dst[t*k+j]] = bf16(topk_w[t][j] * dout[t]) and
+ * dtopk_w[t][j] = <dout[t], y_perm[slot_dst[t*k+j]]> in fp32.  (The gradient of shared_y is dout.)
+ * Either output may be NULL, not both; topk_w is needed for dy_perm, y_perm for dtopk_w.
+ *   dout [T][d], y_perm [T*k][d], dy_perm [T*k][d] bf16; dy_perm must not overlap y_perm.
+ *   d % 128 == 0, d <= 32768. */
+int moe_combine_grad(const void* dout, const void* y_perm, const int32_t* slot_dst,
+                     const float* topk_w, int T, int k, int d, void* dy_perm, float* dtopk_w,
+                     hipStream_t stream);
+
+/* Gradient of moe_permute's row gather: dx[t] = bf16(sum_{j<k} dx_perm[slot_dst[t*k+j]] (+ dx_add[t])),
+ * the sum in fp32 in increasing j, dx_add (what reaches x by the shared expert or the router) last.
+ *   dx_perm [T*k][d] bf16, dx_add [T][d] bf16 or NULL, dx [T][d] bf16.  d % 128 == 0. */
+int moe_permute_grad(const void* dx_perm, const int32_t* slot_dst, const void* dx_add, int T, int k,
+                     int d, void* dx, hipStream_t stream);
 
 /* Static name of a status code. */
 const char* moe_status_string(int status);

@@ -61,6 +61,12 @@ bool is_mxfp4(const moe_problem* p) {
   return p->wdtype == MOE_DTYPE_MXFP4 || p->wdtype == MOE_DTYPE_MXFP4_A8;
 }
 
+bool is_int8(const moe_problem* p) { return p->wdtype == MOE_DTYPE_INT8; }
+
+// Longest row of the row kernels (norm, int8 rows): a row stays in one workgroup's registers.
+constexpr int kMaxRowLen = 32768;
+constexpr int kMaxRowLenGrad = 16384;  // (the norm's gradient keeps two rows and its share of dw)
+
 int check_problem(const moe_problem* p) {
   if (!p) return MOE_ERR_INVALID_ARG;
   int st = check_route_shape(p->T, p->num_experts, p->top_k);
@@ -68,7 +74,11 @@ int check_problem(const moe_problem* p) {
   if (p->d_model <= 0 || p->d_ff <= 0) return MOE_ERR_INVALID_ARG;
   if (p->d_model % 128 || p->d_ff % 128) return MOE_ERR_UNSUPPORTED;
   if (p->wdtype != MOE_DTYPE_BF16 && p->wdtype != MOE_DTYPE_FP8_E4M3 &&
-      p->wdtype != MOE_DTYPE_MXFP4 && p->wdtype != MOE_DTYPE_MXFP4_A8)
+      p->wdtype != MOE_DTYPE_MXFP4 && p->wdtype != MOE_DTYPE_MXFP4_A8 && !is_int8(p))
+    return MOE_ERR_UNSUPPORTED;
+  // (int8 rows of x and h are quantised whole)
+  if (is_int8(p) && std::max(std::max(p->d_model, p->d_ff), p->has_shared ? p->d_ff_shared : 0) >
+                        kMaxRowLen)
     return MOE_ERR_UNSUPPORTED;
   if (is_mxfp4(p) && p->has_shared) return MOE_ERR_UNSUPPORTED;
   // (MFMA tiles exist for mxfp4 weights with mxfp8 activations only)
@@ -96,7 +106,7 @@ int check_problem(const moe_problem* p) {
 
 int check_weights(const moe_problem* p, const moe_weights* w, bool with_shared) {
   if (!w) return MOE_ERR_INVALID_ARG;
-  // fp8 and mxfp4 weight bytes must be in the tiled layout (same size as the row-major one, so
+  // fp8, int8 and mxfp4 weight bytes must be in the tiled layout (same size as the row-major one, so
   // the tag is the only thing that tells them apart); bf16 weights are row-major
   const int32_t want = p->wdtype == MOE_DTYPE_BF16 ? MOE_LAYOUT_ROW_MAJOR : MOE_LAYOUT_TILED;
   if (w->layout != want) return MOE_ERR_INVALID_ARG;
@@ -105,6 +115,14 @@ int check_weights(const moe_problem* p, const moe_weights* w, bool with_shared) 
     if (!q || !aligned16(q)) return MOE_ERR_INVALID_ARG;
   if (p->wdtype == MOE_DTYPE_FP8_E4M3) {
     if (!w->s_gate || !w->s_up || !w->s_down) return MOE_ERR_INVALID_ARG;
+  }
+  if (is_int8(p)) {  // (channel scales are read four at a time)
+    const float* s[] = {w->s_gate, w->s_up, w->s_down};
+    for (const void* q : s)
+      if (!q || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+    const float* sh[] = {w->s_sh_gate, w->s_sh_up, w->s_sh_down};
+    for (const void* q : sh)
+      if (with_shared && p->has_shared && (!q || !aligned16(q))) return MOE_ERR_INVALID_ARG;
   }
   if (is_mxfp4(p)) {
     // (the tiles stage the scale rows with 4-byte loads)
@@ -138,13 +156,17 @@ struct FfnWs {
   void* h_sh;
   float* hs_sh;
   void* y_sh;
+  uint8_t* hq;    // int8: the quantised rows of h and h_sh (h and h_sh are then fp32)
+  uint8_t* hq_sh;
 };
 
 // grouped_ffn: the grouped-FFN entry point (which quantises x_perm itself for MXFP8 activations)
 void carve_ffn(Carver& c, const moe_problem* p, bool with_shared, bool grouped_ffn, FfnWs& f) {
   const size_t n = (size_t)p->T * p->top_k;
   const bool a8 = p->wdtype == MOE_DTYPE_MXFP4_A8;
-  const size_t hb = (p->wdtype == MOE_DTYPE_FP8_E4M3 || a8) ? 1 : 2;  // bytes per h value
+  const bool i8 = is_int8(p);
+  // bytes per h value
+  const size_t hb = i8 ? 4 : (p->wdtype == MOE_DTYPE_FP8_E4M3 || a8) ? 1 : 2;
   f.segs = c.take<Seg>((size_t)2 * kNumFam * kSegCap);
   f.meta = c.take<int32_t>(2 * kNumFam * kMetaStride);
   f.split_part = nullptr;  // (only bf16 weights run MFMA tiles, which may split in K)
@@ -152,6 +174,11 @@ void carve_ffn(Carver& c, const moe_problem* p, bool with_shared, bool grouped_f
     f.split_part = c.take<float>((size_t)kSplitMaxPieces * kSplitSlotFloats);
   f.h = c.take<uint8_t>(n * p->d_ff * hb);
   f.hs = p->wdtype == MOE_DTYPE_FP8_E4M3 ? c.take<float>(n * (p->d_ff / 128)) : nullptr;
+  f.hq = f.hq_sh = nullptr;
+  if (i8) {
+    f.hq = c.take<uint8_t>(n * p->d_ff);
+    f.hs = c.take<float>(n);
+  }
   f.he = a8 ? c.take<uint8_t>(n * (p->d_ff / 32)) : nullptr;
   f.xq = f.xe = nullptr;
   if (a8 && grouped_ffn) {
@@ -163,6 +190,10 @@ void carve_ffn(Carver& c, const moe_problem* p, bool with_shared, bool grouped_f
   if (with_shared && p->has_shared) {
     f.h_sh = c.take<uint8_t>((size_t)p->T * p->d_ff_shared * hb);
     f.hs_sh = hb == 1 ? c.take<float>((size_t)p->T * (p->d_ff_shared / 128)) : nullptr;
+    if (i8) {
+      f.hq_sh = c.take<uint8_t>((size_t)p->T * p->d_ff_shared);
+      f.hs_sh = c.take<float>(p->T);
+    }
     f.y_sh = c.take<uint16_t>((size_t)p->T * p->d_model);
   }
 }
@@ -175,7 +206,7 @@ void carve_ffn(Carver& c, const moe_problem* p, bool with_shared, bool grouped_f
 // split needs fewer than kSplitMaxRounds rounds of MFMA tiles, and the MFMA rows are at least the
 // rows of every expert above the streaming threshold, so when those alone fill kSplitMaxRounds
 // rounds at full tile height no split can happen.
-// The streaming thresholds of the policies the device may apply to a bf16 problem (the table row
+// The streaming thresholds of the policies the device may apply to a bf16 or int8 problem (the table row
 // of its T bucket in automatic mode, else the forced one), and whether all of them use the few-tile
 // rule: the host's launch decisions must hold for whichever one the live histogram picks.
 struct PolicyBounds {
@@ -226,6 +257,7 @@ hipError_t launch_gemms(const SelectOut& o, const moe_problem* p, int gemm, int6
     const int64_t experts = std::min<int64_t>(p->num_experts, total_rows);
     if (5 * experts * nt < kFewTileRounds5 * (int64_t)cus) mfma = false;
   }
+  if (is_int8(p)) return moe::launch_gemms_i8(o, gemm, cus, max_rows, stream, mfma, s);
   const int64_t light = p->config == MOE_CONFIG_MFMA ? 0 : (int64_t)pb.thr_max[gemm] * p->num_experts;
   const int64_t min_tiles = (std::max<int64_t>(0, total_rows - light) + kMfmaBM - 1) / kMfmaBM * nt;
   const bool maybe_split =
@@ -233,6 +265,15 @@ hipError_t launch_gemms(const SelectOut& o, const moe_problem* p, int gemm, int6
   const int max_k = gemm == kGemmGateUp ? p->d_model
                                          : std::max(p->d_ff, p->has_shared ? p->d_ff_shared : 0);
   return moe::launch_gemms_bf16(o, gemm, cus, max_rows, max_k, stream, mfma, maybe_split, s, false);
+}
+
+// int8 experts: the rows of h (and of the shared expert's) quantised between the two GEMMs.
+hipError_t launch_quant_h(const FfnWs& f, const moe_problem* p, int64_t rows, bool with_shared,
+                          hipStream_t s) {
+  hipError_t e = moe::launch_quant_i8(f.h, true, (int)rows, p->d_ff, f.hq, f.hs, s);
+  if (e == hipSuccess && with_shared && p->has_shared)
+    e = moe::launch_quant_i8(f.h_sh, true, p->T, p->d_ff_shared, f.hq_sh, f.hs_sh, s);
+  return e;
 }
 }  // namespace
 
@@ -302,10 +343,12 @@ int moe_permute(const int32_t* topk_ids, int T, int E, int k, const void* x, con
   if (x_perm) {
     if (!x || d <= 0) return MOE_ERR_INVALID_ARG;
     if (d % 128) return MOE_ERR_UNSUPPORTED;
-    if (act_dtype != MOE_DTYPE_BF16 && act_dtype != MOE_DTYPE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;
+    if (act_dtype != MOE_DTYPE_BF16 && act_dtype != MOE_DTYPE_FP8_E4M3 &&
+        act_dtype != MOE_DTYPE_INT8)
+      return MOE_ERR_UNSUPPORTED;
     if ((int64_t)T * k * (d / 128) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;  // scale index
     if (!aligned16(x) || !aligned16(x_perm)) return MOE_ERR_INVALID_ARG;
-    if (act_dtype == MOE_DTYPE_FP8_E4M3 && x_perm_scale && !x_scale) return MOE_ERR_INVALID_ARG;
+    if (act_dtype != MOE_DTYPE_BF16 && x_perm_scale && !x_scale) return MOE_ERR_INVALID_ARG;
   }
   if (T > 0 && !topk_ids) return MOE_ERR_INVALID_ARG;
   const size_t need = moe_permute_workspace_bytes(T, E, k);
@@ -318,9 +361,10 @@ int moe_permute(const int32_t* topk_ids, int T, int E, int k, const void* x, con
                                 rank, hist, stream);
   if (e != hipSuccess) return MOE_ERR_HIP;
   if (x_perm && n > 0) {
-    const int fp8 = act_dtype == MOE_DTYPE_FP8_E4M3;
-    e = launch_gather(x, fp8 ? x_scale : nullptr, perm_src, n, k, fp8 ? d : 2 * d, d / 128, x_perm,
-                      fp8 ? x_perm_scale : nullptr, stream);
+    const bool b8 = act_dtype != MOE_DTYPE_BF16;  // one byte per value; int8: one scale per row
+    e = launch_gather(x, b8 ? x_scale : nullptr, perm_src, n, k, b8 ? d : 2 * d,
+                      act_dtype == MOE_DTYPE_INT8 ? 1 : d / 128, x_perm, b8 ? x_perm_scale : nullptr,
+                      stream);
   }
   return hip_status(e);
 }
@@ -363,7 +407,7 @@ int moe_grouped_ffn(const moe_problem* p, const void* x_perm, const float* x_per
   const int fp8 = p->wdtype == MOE_DTYPE_FP8_E4M3;
   if (!x_perm || !counts || !offsets || !y_perm) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x_perm) || !aligned16(y_perm)) return MOE_ERR_INVALID_ARG;
-  if (fp8 && !x_perm_scale) return MOE_ERR_INVALID_ARG;
+  if ((fp8 || is_int8(p)) && !x_perm_scale) return MOE_ERR_INVALID_ARG;
   const size_t need = moe_grouped_ffn_workspace_bytes(p);
   if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
   Carver c{static_cast<uint8_t*>(ws)};
@@ -386,11 +430,13 @@ int moe_grouped_ffn(const moe_problem* p, const void* x_perm, const float* x_per
   a.fp8 = fp8;
   a.w4 = is_mxfp4(p);
   a.mx8 = p->wdtype == MOE_DTYPE_MXFP4_A8;
+  a.i8 = is_int8(p);
+  a.hq = f.hq;
   a.e_gate = w->e_gate; a.e_up = w->e_up; a.e_down = w->e_down;
   a.x = a.mx8 ? static_cast<const void*>(f.xq) : x_perm;
   a.xe = f.xq ? f.xe : nullptr;
   a.he = f.he;
-  a.xs = fp8 ? x_perm_scale : nullptr;
+  a.xs = fp8 || a.i8 ? x_perm_scale : nullptr;
   a.tok = nullptr;
   a.w_gate = w->w_gate; a.w_up = w->w_up; a.w_down = w->w_down;
   a.s_gate = w->s_gate; a.s_up = w->s_up; a.s_down = w->s_down;
@@ -402,6 +448,7 @@ int moe_grouped_ffn(const moe_problem* p, const void* x_perm, const float* x_per
   if (a.mx8) e = launch_quant_act_mx(x_perm, (int)n, p->d_model, f.xq, f.xe, stream);
   if (e == hipSuccess) e = launch_select(a, o, stream);  // caller-given counts: any expert may hold all rows
   if (e == hipSuccess) e = launch_gemms(o, p, kGemmGateUp, n, n, cus, stream);
+  if (e == hipSuccess && a.i8) e = launch_quant_h(f, p, n, false, stream);
   if (e == hipSuccess) e = launch_gemms(o, p, kGemmDown, n, n, cus, stream);
   return hip_status(e);
 }
@@ -415,6 +462,111 @@ int moe_combine(const void* y_perm, const int32_t* slot_dst, const float* topk_w
   if (!aligned16(y_perm) || !aligned16(out) || (shared_y && !aligned16(shared_y)))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_combine(y_perm, slot_dst, topk_w, T, k, d, shared_y, out, stream));
+}
+
+int moe_quant_act_i8(const void* x, int T, int d, int8_t* xq, float* xs, hipStream_t stream) {
+  if (T < 0 || d <= 0) return MOE_ERR_INVALID_ARG;
+  if (d % 16 || d > kMaxRowLen) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !xq || !xs || !aligned16(x) || !aligned16(xq)) return MOE_ERR_INVALID_ARG;
+  return hip_status(
+      launch_quant_i8(x, false, T, d, reinterpret_cast<uint8_t*>(xq), xs, stream));
+}
+
+int moe_gemm_i8(const int8_t* xq, const float* xs, int M, const int8_t* wq, const float* ws, int N,
+                int K, void* y, hipStream_t stream) {
+  if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (N % 16 || K % 128 || K > kMaxRowLen) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)M * K >= kMaxOffsetBytes || (int64_t)N * K >= kMaxOffsetBytes)
+    return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!xq || !xs || !wq || !ws || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned16(wq) || !aligned16(ws) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  const int cus = device_cus();
+  if (cus == 0) return MOE_ERR_HIP;
+  return hip_status(launch_gemm_i8(xq, xs, M, wq, ws, N, K, y, cus, stream));
+}
+
+int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int T, int d,
+                int act_dtype, void* h_out, void* y, void* q, void* q_scale, hipStream_t stream) {
+  if (T < 0 || d <= 0 || !(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  int fmt, step;
+  switch (act_dtype) {
+    case MOE_DTYPE_BF16: fmt = 0; step = 8; break;
+    case MOE_DTYPE_FP8_E4M3: fmt = 1; step = 128; break;
+    case MOE_DTYPE_MXFP4_A8: fmt = 2; step = 32; break;
+    case MOE_DTYPE_INT8: fmt = 3; step = 16; break;
+    default: return MOE_ERR_UNSUPPORTED;
+  }
+  if (d % step || d > kMaxRowLen) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !weight) return MOE_ERR_INVALID_ARG;
+  if (fmt == 0 ? !y : (!q || !q_scale)) return MOE_ERR_INVALID_ARG;
+  const void* al[] = {x, residual, weight, h_out, y, q};
+  for (const void* p : al)
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_rmsnorm(x, residual, weight, eps, T, d, fmt, h_out, y, q, q_scale, stream));
+}
+
+size_t moe_rmsnorm_grad_workspace_bytes(int T, int d) {
+  if (T < 0 || d <= 0 || d % 8 || d > kMaxRowLenGrad) return 0;
+  Carver c{nullptr};
+  c.take<float>((size_t)rmsnorm_grad_parts(T) * d);
+  return c.used;
+}
+
+int moe_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* weight, float eps,
+                     int T, int d, void* dx, float* dweight, void* ws, size_t ws_bytes,
+                     hipStream_t stream) {
+  if (T < 0 || d <= 0 || !(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (d % 8 || d > kMaxRowLenGrad) return MOE_ERR_UNSUPPORTED;
+  if (T == 0 && !dweight) return MOE_OK;
+  if (T > 0 && (!dy || !h || !weight || !dx)) return MOE_ERR_INVALID_ARG;
+  const void* al[] = {dy, dh, h, weight, dx, dweight};
+  for (const void* p : al)
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (dweight && T > 0) {
+    if (!ws || ws_bytes < moe_rmsnorm_grad_workspace_bytes(T, d)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  }
+  return hip_status(launch_rmsnorm_grad(dy, dh, h, weight, eps, T, d, dx, dweight,
+                                        static_cast<float*>(ws), stream));
+}
+
+int moe_route_grad(const int32_t* topk_ids, const float* topk_w, const float* dtopk_w, int T, int E,
+                   int k, float* dlogits, hipStream_t stream) {
+  int st = check_route_shape(T, E, k);
+  if (st) return st;
+  if (T == 0) return MOE_OK;
+  if (!topk_ids || !topk_w || !dtopk_w || !dlogits) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_route_grad(topk_ids, topk_w, dtopk_w, T, E, k, dlogits, stream));
+}
+
+int moe_combine_grad(const void* dout, const void* y_perm, const int32_t* slot_dst,
+                     const float* topk_w, int T, int k, int d, void* dy_perm, float* dtopk_w,
+                     hipStream_t stream) {
+  if (T < 0 || k <= 0 || d <= 0) return MOE_ERR_INVALID_ARG;
+  if (k > kMaxTopK || d % 128 || d > kMaxRowLen) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)T * k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!dy_perm && !dtopk_w) return MOE_ERR_INVALID_ARG;
+  if (!dout || !slot_dst || (dy_perm && !topk_w) || (dtopk_w && !y_perm)) return MOE_ERR_INVALID_ARG;
+  const void* al[] = {dout, y_perm, dy_perm};
+  for (const void* p : al)
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_combine_grad(dout, y_perm, slot_dst, topk_w, T, k, d, dy_perm, dtopk_w,
+                                        stream));
+}
+
+int moe_permute_grad(const void* dx_perm, const int32_t* slot_dst, const void* dx_add, int T, int k,
+                     int d, void* dx, hipStream_t stream) {
+  if (T < 0 || k <= 0 || d <= 0) return MOE_ERR_INVALID_ARG;
+  if (k > kMaxTopK || d % 128) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)T * k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!dx_perm || !slot_dst || !dx) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dx_perm) || !aligned16(dx) || !aligned16(dx_add)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_combine(dx_perm, slot_dst, nullptr, T, k, d, dx_add, dx, stream));
 }
 
 // Workspace of the whole layer (see carve_layer for the order).
@@ -447,9 +599,10 @@ void carve_layer(Carver& c, const moe_problem* p, LayerWs& L) {
   L.xq = nullptr;
   L.xs = nullptr;
   L.xe = nullptr;
-  if (p->wdtype == MOE_DTYPE_FP8_E4M3 || p->wdtype == MOE_DTYPE_MXFP4_A8)
+  if (p->wdtype == MOE_DTYPE_FP8_E4M3 || p->wdtype == MOE_DTYPE_MXFP4_A8 || is_int8(p))
     L.xq = c.take<uint8_t>((size_t)p->T * p->d_model);
   if (p->wdtype == MOE_DTYPE_FP8_E4M3) L.xs = c.take<float>((size_t)p->T * (p->d_model / 128));
+  if (is_int8(p)) L.xs = c.take<float>(p->T);
   if (p->wdtype == MOE_DTYPE_MXFP4_A8) L.xe = c.take<uint8_t>((size_t)p->T * (p->d_model / 32));
   carve_ffn(c, p, true, false, L.ffn);
   L.y = c.take<uint16_t>(n * p->d_model);
@@ -513,8 +666,11 @@ int layer_impl(const moe_problem* p, const float* logits, const void* x, const m
   a.fp8 = fp8;
   a.w4 = is_mxfp4(p);
   a.mx8 = p->wdtype == MOE_DTYPE_MXFP4_A8;
+  a.i8 = is_int8(p);
+  a.hq = L.ffn.hq;
+  a.h_shq = L.ffn.hq_sh;
   a.e_gate = w->e_gate; a.e_up = w->e_up; a.e_down = w->e_down;
-  a.x = (fp8 || a.mx8) ? static_cast<const void*>(L.xq) : x;
+  a.x = (fp8 || a.mx8 || a.i8) ? static_cast<const void*>(L.xq) : x;
   a.xs = L.xs;
   a.xe = L.xe;
   a.he = L.ffn.he;
@@ -595,6 +751,7 @@ int layer_impl(const moe_problem* p, const float* logits, const void* x, const m
     if (e == hipSuccess) e = mark(2);
     if (e == hipSuccess && fp8) e = launch_quant_act(x, T, d, L.xq, L.xs, stream);
     if (e == hipSuccess && a.mx8) e = launch_quant_act_mx(x, T, d, L.xq, L.xe, stream);
+    if (e == hipSuccess && a.i8) e = launch_quant_i8(x, false, T, d, L.xq, L.xs, stream);
     if (e == hipSuccess) e = mark(3);
     if (e == hipSuccess) e = mark(4);
   } else {
@@ -606,6 +763,7 @@ int layer_impl(const moe_problem* p, const float* logits, const void* x, const m
     if (e == hipSuccess) e = mark(2);
     if (e == hipSuccess && fp8) e = launch_quant_act(x, T, d, L.xq, L.xs, stream);
     if (e == hipSuccess && a.mx8) e = launch_quant_act_mx(x, T, d, L.xq, L.xe, stream);
+    if (e == hipSuccess && a.i8) e = launch_quant_i8(x, false, T, d, L.xq, L.xs, stream);
     if (e == hipSuccess) e = mark(3);
     if (e == hipSuccess) e = launch_select(a, o, stream);
     if (e == hipSuccess) e = mark(4);
@@ -614,6 +772,7 @@ int layer_impl(const moe_problem* p, const float* logits, const void* x, const m
   if (e == hipSuccess && !decode1)
     e = launch_gemms(o, p, kGemmGateUp, T, (int64_t)T * p->top_k, cus, stream);
   if (e == hipSuccess) e = mark(5);
+  if (e == hipSuccess && a.i8) e = launch_quant_h(L.ffn, p, (int64_t)T * k, true, stream);
   if (e == hipSuccess) e = launch_gemms(o, p, kGemmDown, T, (int64_t)T * p->top_k, cus, stream);
   if (e == hipSuccess) e = mark(6);
   if (e == hipSuccess)

@@ -12,6 +12,9 @@ namespace moe {
 
 constexpr int kCombineMaxThreads = 256;
 
+// WEIGHTED = false: every weight is 1 (the gradient of the sort: a token's row gathers what arrived
+// at its k copies).
+template <bool WEIGHTED>
 __global__ __launch_bounds__(kCombineMaxThreads) void combine_kernel(const uint16_t* __restrict__ y,
                                                       const int32_t* __restrict__ slot_dst,
                                                       const float* __restrict__ w, int k, int d,
@@ -27,7 +30,7 @@ __global__ __launch_bounds__(kCombineMaxThreads) void combine_kernel(const uint1
   for (int j = 0; j < kMaxTopK; ++j) {
     if (j < k) {
       row[j] = slot_dst[(size_t)t * k + j];
-      wj[j] = w[(size_t)t * k + j];
+      wj[j] = WEIGHTED ? w[(size_t)t * k + j] : 1.0f;
     }
   }
   uint4 v[kMaxTopK];
@@ -76,9 +79,10 @@ hipError_t launch_combine(const void* y, const int32_t* slot_dst, const float* w
   const int lanes = d / 8;  // threads per token row
   const int bt = lanes % 256 == 0 ? 256 : lanes % 128 == 0 ? 128 : lanes % 64 == 0 ? 64 : 256;
   const int nbx = (lanes + bt - 1) / bt;
-  combine_kernel<<<(unsigned)((int64_t)T * nbx), bt, 0, s>>>(static_cast<const uint16_t*>(y),
-                                      slot_dst, w, k, d, nbx, static_cast<const uint16_t*>(shared_y),
-                                      static_cast<uint16_t*>(out));
+  auto* kernel = w ? &combine_kernel<true> : &combine_kernel<false>;
+  kernel<<<(unsigned)((int64_t)T * nbx), bt, 0, s>>>(static_cast<const uint16_t*>(y), slot_dst, w, k,
+                                                     d, nbx, static_cast<const uint16_t*>(shared_y),
+                                                     static_cast<uint16_t*>(out));
   return hipGetLastError();
 }
 

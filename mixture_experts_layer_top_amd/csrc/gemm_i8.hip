@@ -1,0 +1,455 @@
+// Matrix products of int8 rows and int8 weights with one fp32 scale per row (token) and per weight
+// row (output channel): the experts' grouped gate/up and down GEMMs, and one dense product.
+//
+//   acc[row][n] = sum_k qx[row][k] * qw[n][k]          (int32, exact: K <= 32768 keeps it below 2^30)
+//   v[row][n] = float(acc) * sx[row] * sw[n]
+//   gate/up: h = SiLU(v_gate) * v_up in fp32 (quantised per row before the down GEMM, norm.hip: a
+//            row's scale needs all of its d_ff columns, so it cannot be taken inside a tile)
+//   down, dense: y = bf16(v)
+//
+// The scales are constant along K, so the K loops are MFMAs and loads only, and integer sums do not
+// depend on their order: results are the same bits whatever the tile family.  Two families, as for
+// bf16:
+//  * stream (light experts, small dense products): a workgroup's 4 wavefronts split K over 16 weight
+//    rows (K >= kStreamSplitK) or 32, up to 64 token rows per pass; weights go straight from HBM
+//    into MFMA registers, 1 KB contiguous per load in the tiled layout (moe_fp8_tile).
+//  * mfma (mfma_tile.h): 256 weight rows by 32 to 256 token rows staged through LDS.
+#include <algorithm>
+
+#include "common.h"
+#include "kernels.h"
+#include "mfma_tile.h"
+#include "stream_dev.h"
+
+namespace moe {
+
+namespace {
+
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+// 16 bytes per lane and operand, loaded alike for both (row l % 32 or l % 16, the lane group's 16
+// bytes of K), so the K order inside the instruction does not matter.  C as the bf16 MFMAs.
+struct ElemI8 {
+  using Frag = i32x4;
+  using Acc = i32x16;
+  static constexpr int kBytes = 1;
+  static constexpr bool kTiledW = true;
+  static constexpr bool kOddSteps = true;  // K % 128 == 0: any number of 128-wide K-steps
+  static __device__ __forceinline__ Frag frag(const uint4& v) { return __builtin_bit_cast(i32x4, v); }
+  static __device__ __forceinline__ Acc mfma(const Frag& a, const Frag& b, const Acc& c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+  }
+};
+
+__device__ __forceinline__ i32x4 mfma16_i8(const uint4& a, const uint4& b, const i32x4& c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                               __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float4 gload_f32x4(const float* p, uint32_t i) {
+  return __builtin_bit_cast(float4, gload16(p, i * 4));
+}
+
+// ------------------------------------------------------------------------------------------------
+// streaming tiles
+// ------------------------------------------------------------------------------------------------
+
+// Rows [m0, m0 + rows) (rows <= 16 * MQ) by the 16 weight rows of each wavefront group from n0.
+template <int MQ, bool GU, int WK>
+__device__ __forceinline__ void stream_tile_i8(const Seg& sg, int m0, int rows, int n0, int* red) {
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, kg = lane >> 4;
+  const int grp = wv / WK, kw = wv % WK;
+  n0 += 16 * grp;
+  const int K = sg.K, N = sg.N, nkb = K / 128;
+  const uint32_t woff = (uint32_t)(n0 >> 4) * (uint32_t)(nkb * 2048) + lane * 16;
+  int src[MQ];
+  uint32_t xoff[MQ];
+#pragma unroll
+  for (int q = 0; q < MQ; ++q) {
+    int r = q * 16 + r16;
+    r = r < rows ? r : rows - 1;  // padded columns re-read a valid row; never stored
+    const int gr = sg.row0 + m0 + r;
+    src[q] = sg.tok ? gload_i32(sg.tok, gr) : gr;
+    xoff[q] = (uint32_t)src[q] * (uint32_t)K + kg * 32;
+  }
+  i32x4 acc0[MQ], acc1[MQ];
+#pragma unroll
+  for (int q = 0; q < MQ; ++q) acc0[q] = acc1[q] = i32x4{0, 0, 0, 0};
+  constexpr int U = 2;  // 128-wide chunks per batch
+  struct Batch { uint4 a0[U][2], a1[U][2], b[U][MQ][2]; };
+  // this wavefront's chunks: kw, kw + WK, ... (the group's wavefronts read adjacent units)
+  const int nc = (nkb - kw + WK - 1) / WK;
+  auto load = [&](Batch& bt, int i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t kb = (uint32_t)min(kw + WK * (i + u), nkb - 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bt.a0[u][h] = gload16_nt(sg.w0, woff + kb * 2048 + h * 1024);
+        if (GU) bt.a1[u][h] = gload16_nt(sg.w1, woff + kb * 2048 + h * 1024);
+#pragma unroll
+        for (int q = 0; q < MQ; ++q) bt.b[u][q][h] = gload16(sg.a, xoff[q] + kb * 128 + h * 16);
+      }
+    }
+  };
+  auto compute = [&](const Batch& bt, int i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u >= nc) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < MQ; ++q) {
+          acc0[q] = mfma16_i8(bt.a0[u][h], bt.b[u][q][h], acc0[q]);
+          if (GU) acc1[q] = mfma16_i8(bt.a1[u][h], bt.b[u][q][h], acc1[q]);
+        }
+    }
+  };
+  Batch b0, b1;
+  if (nc > 0) load(b0, 0);
+  for (int i = 0; i < nc; i += 2 * U) {
+    if (i + U < nc) load(b1, i + U);
+    compute(b0, i);
+    if (i + 2 * U < nc) load(b0, i + 2 * U);
+    if (i + U < nc) compute(b1, i + U);
+  }
+  // split-K sums: wavefronts kw > 0 of a group park theirs in LDS, wavefront 0 adds them
+  constexpr int NV = MQ * 4 * (GU ? 2 : 1);
+  __syncthreads();  // red[] may still be read by the previous tile
+  if (kw > 0) {
+    int* dst = red + ((grp * (WK - 1) + kw - 1) * NV) * 64 + lane;
+#pragma unroll
+    for (int q = 0; q < MQ; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        dst[(q * 4 + j) * 64] = acc0[q][j];
+        if (GU) dst[(MQ * 4 + q * 4 + j) * 64] = acc1[q][j];
+      }
+  }
+  __syncthreads();
+  if (kw != 0) return;
+#pragma unroll
+  for (int w = 0; w < WK - 1; ++w) {
+    const int* sp = red + ((grp * (WK - 1) + w) * NV) * 64 + lane;
+#pragma unroll
+    for (int q = 0; q < MQ; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc0[q][j] += sp[(q * 4 + j) * 64];
+        if (GU) acc1[q][j] += sp[(MQ * 4 + q * 4 + j) * 64];
+      }
+  }
+  // lane holds weight rows n0 + 4 kg + j of token column r16 of each group q
+  const float4 s0 = gload_f32x4(sg.s0, n0 + 4 * kg);
+  const float4 s1 = GU ? gload_f32x4(sg.s1, n0 + 4 * kg) : s0;
+  const float c0[4] = {s0.x, s0.y, s0.z, s0.w}, c1[4] = {s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+  for (int q = 0; q < MQ; ++q) {
+    const int r = q * 16 + r16;
+    if (r >= rows) continue;
+    const float sx = gload_f32(sg.as, src[q]);
+    const size_t at = (size_t)(sg.row0 + m0 + r) * N + n0 + 4 * kg;
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = float(acc0[q][j]) * sx * c0[j];
+      if (GU) v[j] = swiglu(v[j], float(acc1[q][j]) * sx * c1[j]);
+    }
+    if (GU)
+      gstore16(sg.out, at * 4, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                          __float_as_uint(v[2]), __float_as_uint(v[3])));
+    else
+      gstore8(sg.out, at * 2, uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+  }
+}
+
+template <int MQMAX, bool GU, int WK>
+__device__ __forceinline__ void stream_rows_i8(const Seg& sg, int m0, int rows, int n0, int* red) {
+  for (int sub = 0; sub < rows; sub += 16 * MQMAX) {
+    const int r = min(16 * MQMAX, rows - sub);
+    if (MQMAX == 1 || r <= 16) stream_tile_i8<1, GU, WK>(sg, m0 + sub, r, n0, red);
+    else if (MQMAX == 2 || r <= 32) stream_tile_i8<MQMAX >= 2 ? 2 : 1, GU, WK>(sg, m0 + sub, r, n0, red);
+    else stream_tile_i8<MQMAX, GU, WK>(sg, m0 + sub, r, n0, red);
+  }
+}
+
+// Persistent, as the bf16 streaming kernel.
+template <bool GU, int MQMAX>
+__global__ __launch_bounds__(256) void gemm_stream_i8(const Seg* __restrict__ segs,
+                                                      int32_t* __restrict__ meta) {
+  __shared__ int slot;
+  __shared__ int seg_base[kSegCap];
+  __shared__ int red[3 * MQMAX * 4 * 2 * 64];
+  const int nseg = meta[0], ntiles = meta[1];
+  if ((int)blockIdx.x >= ntiles) return;
+  for (int i = threadIdx.x; i < nseg; i += 256) seg_base[i] = segs[i].tile_base;
+  __syncthreads();
+  int t = blockIdx.x;
+  for (;;) {
+    const Seg& sg = segs[__builtin_amdgcn_readfirstlane(find_seg_lds(seg_base, nseg, t))];
+    const int local = t - sg.tile_base;
+    const int mt = local % sg.mtiles, nt = local / sg.mtiles;
+    const int m0 = mt * kStreamMaxRows;
+    const int rows = min(kStreamMaxRows, sg.rows - m0);
+    if (sg.tn == 16) stream_rows_i8<MQMAX, GU, 4>(sg, m0, rows, nt * 16, red);
+    else stream_rows_i8<MQMAX, GU, 2>(sg, m0, rows, nt * 32, red);
+    t = gridDim.x + __builtin_amdgcn_readfirstlane(pop_tile(&meta[kMetaQueue], &slot));
+    if (t >= ntiles) break;
+  }
+}
+
+// The dense product's streaming form: one segment, 16 columns per workgroup.
+template <int MQ>
+__global__ __launch_bounds__(256) void gemm_stream_i8_dense(Seg sg) {
+  __shared__ int red[3 * MQ * 4 * 64];
+  const int m0 = (blockIdx.x % sg.mtiles) * (16 * MQ);
+  stream_tile_i8<MQ, false, 4>(sg, m0, min(16 * MQ, sg.rows - m0), (blockIdx.x / sg.mtiles) * 16, red);
+}
+
+// ------------------------------------------------------------------------------------------------
+// LDS-staged MFMA tiles
+// ------------------------------------------------------------------------------------------------
+
+// What the epilogue needs of a claimed tile.
+struct I8Cur {
+  int m0, rows, n0, nk, N, row0;
+  void* out;
+  const float* as;
+  const float* s0;
+  const float* s1;
+  const int32_t* tok;
+};
+
+// Epilogue through LDS (as the bf16 tiles'): the tile goes into the idle ring as [token row][column],
+// fp32 h (gate/up, 128 columns) or bf16 y (256 columns), 512 bytes of output per row and 16 of
+// padding, then out in 16-byte chunks of whole rows.  TB: token blocks of a short tile (8: full).
+template <bool GU, int TB>
+__device__ __forceinline__ void i8_store(const i32x16 (&acc)[4][4], const I8Cur& c) {
+  constexpr bool kFull = TB == 8;
+  constexpr int RS = 512 + 16;
+  static_assert(256 * RS <= kRingBytes, "an output tile fits the ring");
+  const uint32_t tid = tid_here();
+  const int lane = tid & 63, wv = tid >> 6;
+  const int l32 = lane & 31, khalf = lane >> 5;
+  const int wm = kFull ? wv & 1 : 0, wn = kFull ? wv >> 1 : wv;
+  constexpr int NB = kFull ? 4 : TB;           // token blocks of this wavefront
+  constexpr int NA = GU ? (kFull ? 2 : 1) : (kFull ? 4 : 2);  // its 32-column output blocks
+  const int cw = wn * 32 * NA;                 // its first output column
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int t = (kFull ? wm * 128 : 0) + b * 32 + l32;
+    const int gr = c.row0 + c.m0 + min(t, c.rows - 1);
+    const float sx = gload_f32(c.as, c.tok ? gload_i32(c.tok, gr) : gr);
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      // (one block's scale loads at a time: all of them together would not fit beside the
+      // accumulators)
+      if (kFull) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // lane holds C[8 q + 4 khalf + s][l32] of each 32x32 block (rows = weights)
+        const int col = cw + a * 32 + 8 * q + 4 * khalf;
+        const int n = min(c.n0 + col, c.N - 4);  // (columns past N are not stored)
+        const float4 s0 = gload_f32x4(c.s0, n);
+        const float w0[4] = {s0.x, s0.y, s0.z, s0.w};
+        float v[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v[s] = float(acc[a][b][q * 4 + s]) * sx * w0[s];
+        if (GU) {
+          const float4 s1 = gload_f32x4(c.s1, n);
+          const float w1[4] = {s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            v[s] = swiglu(v[s], float(acc[a + NA][b][q * 4 + s]) * sx * w1[s]);
+          *reinterpret_cast<float4*>(g_ring + t * RS + col * 4) = float4{v[0], v[1], v[2], v[3]};
+        } else {
+          *reinterpret_cast<uint2*>(g_ring + t * RS + col * 2) =
+              uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        }
+      }
+    }
+  }
+  __syncthreads();
+  constexpr int H = kFull ? 256 : TB * 32;
+  constexpr int VB = GU ? 4 : 2;  // bytes per value
+  const int ch = tid & 31;
+  const int col = c.n0 + ch * (16 / VB);
+  const int nr = c.rows < H ? c.rows : H;
+  if (col < c.N) {  // (down: the last tile of a row may be part full, in multiples of 16 columns)
+    for (int t = tid >> 5; t < nr; t += 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(g_ring + t * RS + ch * 16);
+      gstore16(c.out, ((size_t)(c.row0 + c.m0 + t) * c.N + col) * VB, v);
+    }
+  }
+}
+
+template <bool GU>
+__device__ __forceinline__ void i8_run(MfmaTile<GU, ElemI8>& tile, int h, const I8Cur& c) {
+  if (h == BM) {
+    tile.run_full(c.nk);
+    i8_store<GU, 8>(tile.acc, c);
+  } else if (h == 128) {
+    tile.template run_short<4>(c.nk);
+    i8_store<GU, 4>(tile.acc, c);
+  } else if (h == 64) {
+    tile.template run_short<2>(c.nk);
+    i8_store<GU, 2>(tile.acc, c);
+  } else {
+    tile.template run_short<1>(c.nk);
+    i8_store<GU, 1>(tile.acc, c);
+  }
+}
+
+template <bool GU>
+__device__ __forceinline__ I8Cur i8_cur(const Seg& sg, int m0, int rows, int nt) {
+  I8Cur c;
+  c.m0 = m0;
+  c.rows = rows;
+  c.n0 = nt * (GU ? kMfmaBNGateUp : kMfmaBNDown);
+  c.nk = sg.K / 128;
+  c.N = sg.N;
+  c.row0 = sg.row0;
+  c.out = sg.out;
+  c.as = sg.as;
+  c.s0 = sg.s0;
+  c.s1 = sg.s1;
+  c.tok = sg.tok;
+  return c;
+}
+
+// Persistent: one workgroup per CU takes tiles from the per-XCD queues in the list's order (the
+// selection kernel's, as for bf16).
+template <bool GU>
+__global__ __launch_bounds__(256, 1) void gemm_mfma_i8(const Seg* __restrict__ segs,
+                                                       int32_t* __restrict__ meta) {
+  __shared__ int slot;
+  __shared__ int seg_base[kSegCap];
+  const int ntiles = meta[1];
+  if (ntiles == 0) return;
+  const int nseg = meta[0], ntiles0 = meta[kMetaClass0], order = meta[kMetaOrder];
+  int pref, b0, b1;
+  two_class_split((int)gridDim.x, ntiles0, ntiles - ntiles0, pref, b0, b1);
+  b0 = __builtin_amdgcn_readfirstlane(b0);
+  b1 = __builtin_amdgcn_readfirstlane(b1);
+  const int chunk = __builtin_amdgcn_readfirstlane(max(1, (int)gridDim.x / kXcds) *
+                                                   (order == kOrderMix ? 2 : 1));
+  for (int i = threadIdx.x; i < nseg; i += blockDim.x) seg_base[i] = segs[i].tile_base;
+  __syncthreads();
+  MfmaTile<GU, ElemI8> tile;
+  int q = 0;
+  for (;;) {
+    // (opaque moves: the reciprocals of the queue's divisions are computed here, not held across
+    // the K loops)
+    const int nt_ = opaque_s(ntiles), nt0_ = opaque_s(ntiles0), ch_ = opaque_s(chunk);
+    int t;
+    if (order == kOrderTwoClass) {
+      t = pop_tile_two_class(meta + kMetaQueue, meta + kMetaQueue1, nt0_, nt_ - nt0_, opaque_s(b0),
+                             opaque_s(b1), pref, &slot, q);
+      if (t < 0) return;
+    } else {
+      const int pos = pop_tile_xcd(meta + kMetaQueue, nt_, ch_, &slot, q);
+      if (pos < 0) return;
+      t = order == kOrderLongestFirst ? pos : interleave_tile(pos, nt0_, nt_);
+    }
+    const Seg& sg = segs[__builtin_amdgcn_readfirstlane(find_seg_lds(seg_base, nseg, t))];
+    const int local = t - sg.tile_base;
+    const int m0 = local % sg.mtiles * BM;
+    const I8Cur c = i8_cur<GU>(sg, m0, min(BM, sg.rows - m0), local / sg.mtiles);
+    tile.setup(sg, c.m0, c.rows, c.n0, 0);
+    const int h = __builtin_amdgcn_readfirstlane(tile.bm);
+    tile.prologue(c.nk);
+    i8_run<GU>(tile, h, c);  // (the pop's barriers keep the next tile's loads behind its stores)
+  }
+}
+
+// The dense product: one segment, MH token rows per tile; XCD x takes an equal run of consecutive
+// tiles (m-tiles of one weight tile adjacent).
+template <int MH>
+__global__ __launch_bounds__(256, 1) void gemm_mfma_i8_dense(Seg sg) {
+  sg.tok = nullptr;
+  sg.row0 = 0;
+  MfmaTile<false, ElemI8> tile;
+  const int ntiles = sg.mtiles * sg.ntiles, per = (ntiles + kXcds - 1) / kXcds;
+  const int x = blockIdx.x % kXcds;
+  for (int i = blockIdx.x / kXcds; i < per; i += gridDim.x / kXcds) {
+    const int mt_ = opaque_s(sg.mtiles);
+    const int t = x * per + i;
+    if (t >= ntiles) return;
+    const int m0 = t % mt_ * MH;
+    const I8Cur c = i8_cur<false>(sg, m0, min(MH, sg.rows - m0), t / mt_);
+    tile.template setup<MH>(sg, c.m0, c.rows, c.n0, 0);
+    if constexpr (MH == BM) {
+      tile.prologue_full(c.nk);
+      tile.run_full(c.nk);
+      i8_store<false, 8>(tile.acc, c);
+    } else {
+      tile.template prologue_short<MH / 32>(c.nk);
+      tile.template run_short<MH / 32>(c.nk);
+      i8_store<false, MH / 32>(tile.acc, c);
+    }
+    __syncthreads();  // (the ring's rows are stored before the next tile's loads overwrite them)
+  }
+}
+
+template <bool GU>
+void launch_stream_i8(const Seg* ss, int32_t* ms, int num_cus, int64_t max_rows, hipStream_t s) {
+  const int g = 4 * num_cus;
+  if (max_rows <= 16) gemm_stream_i8<GU, 1><<<g, 256, 0, s>>>(ss, ms);
+  else if (max_rows <= 32) gemm_stream_i8<GU, 2><<<g, 256, 0, s>>>(ss, ms);
+  else gemm_stream_i8<GU, 4><<<g, 256, 0, s>>>(ss, ms);
+}
+
+}  // namespace
+
+hipError_t launch_gemms_i8(const SelectOut& o, int g, int num_cus, int64_t max_rows, bool stream,
+                           bool mfma, hipStream_t s) {
+  const Seg* ss = o.segs + (size_t)(g * kNumFam + kFamStream) * kSegCap;
+  int32_t* ms = o.meta + (g * kNumFam + kFamStream) * kMetaStride;
+  const Seg* sm = o.segs + (size_t)(g * kNumFam + kFamMfma) * kSegCap;
+  int32_t* mm = o.meta + (g * kNumFam + kFamMfma) * kMetaStride;
+  if (g == kGemmGateUp) {
+    if (stream) launch_stream_i8<true>(ss, ms, num_cus, max_rows, s);
+    if (mfma) gemm_mfma_i8<true><<<num_cus, 256, 0, s>>>(sm, mm);
+  } else {
+    if (stream) launch_stream_i8<false>(ss, ms, num_cus, max_rows, s);
+    if (mfma) gemm_mfma_i8<false><<<num_cus, 256, 0, s>>>(sm, mm);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_i8(const void* xq, const float* xs, int M, const void* wq, const float* ws,
+                          int N, int K, void* y, int num_cus, hipStream_t s) {
+  if (M == 0) return hipSuccess;
+  Seg sg = {};
+  sg.a = xq;
+  sg.as = xs;
+  sg.w0 = wq;
+  sg.s0 = ws;
+  sg.out = y;
+  sg.rows = M;
+  sg.N = N;
+  sg.K = K;
+  if (M <= 64) {
+    const int mq = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    sg.mtiles = 1;
+    sg.ntiles = N / 16;
+    if (mq == 1) gemm_stream_i8_dense<1><<<sg.ntiles, 256, 0, s>>>(sg);
+    else if (mq == 2) gemm_stream_i8_dense<2><<<sg.ntiles, 256, 0, s>>>(sg);
+    else gemm_stream_i8_dense<4><<<sg.ntiles, 256, 0, s>>>(sg);
+    return hipGetLastError();
+  }
+  // the tallest tile that still gives every CU one
+  sg.ntiles = (N + kMfmaBNDown - 1) / kMfmaBNDown;
+  int mh = 256;
+  while (mh > 32 && (int64_t)((M + mh - 1) / mh) * sg.ntiles < num_cus) mh /= 2;
+  sg.mtiles = (M + mh - 1) / mh;
+  const int g = std::max(kXcds, num_cus / kXcds * kXcds);
+  if (mh == 256) gemm_mfma_i8_dense<256><<<g, 256, 0, s>>>(sg);
+  else if (mh == 128) gemm_mfma_i8_dense<128><<<g, 256, 0, s>>>(sg);
+  else if (mh == 64) gemm_mfma_i8_dense<64><<<g, 256, 0, s>>>(sg);
+  else gemm_mfma_i8_dense<32><<<g, 256, 0, s>>>(sg);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -53,15 +53,16 @@ constexpr int kStream8BNDown = 64;
 struct Seg {
   const void* a;        // activation base ([.][K], bf16 or e4m3)
   const int32_t* tok;   // row -> activation row (null: row0 + r)
-  const float* as;      // fp8: activation scales [.][K/128]
+  const float* as;      // fp8: activation scales [.][K/128]; int8: [.]
   const void* w0;       // gate (gate/up GEMM) or down weights, [N][K]
   const void* w1;       // up weights (gate/up GEMM), [N][K]
-  const float* s0;      // fp8 block scales of w0, [N/128][K/128]
-  const float* s1;      // fp8 block scales of w1
+  const float* s0;      // fp8 block scales of w0, [N/128][K/128]; int8 channel scales [N]
+  const float* s1;      // the same of w1
   const uint8_t* e0;    // mxfp4: E8M0 scales of w0, [N][K/32] (w0 then holds [N][K/2] bytes)
   const uint8_t* e1;    // mxfp4: E8M0 scales of w1
   const uint8_t* ae;    // mxfp8 activations: E8M0 scales [.][K/32] of the rows of `a`
-  void* out;            // output base [.][N] (bf16, or e4m3 for the fp8 and mxfp8 gate/up GEMMs)
+  void* out;            // output base [.][N] (bf16; e4m3 for the fp8 and mxfp8 gate/up GEMMs, fp32
+                        // for the int8 one)
   float* outs;          // fp8 gate/up: output scales [.][N/128]
   uint8_t* oute;        // mxfp8 gate/up: output E8M0 scales [.][N/32]
   int32_t row0, rows, N, K;
@@ -104,6 +105,8 @@ struct SelectArgs {
   const int32_t* offsets;  // [E + 1]
   int E, T, k, d, f, f_sh, has_shared, config, fp8;
   int w4;                  // mxfp4 expert weights (streaming tiles)
+  int i8;                  // int8 weights and rows, one scale per row and per output channel
+  const void* hq; const void* h_shq;  // int8: the quantised rows of h and h_sh (the down GEMM's)
   int mx8;                 // with mxfp8 activations (x and h quantised per 32; else bf16)
   const uint8_t* e_gate; const uint8_t* e_up; const uint8_t* e_down;  // their E8M0 scales
   const uint8_t* xe;       // mx8: E8M0 scales of the gate/up activations [.][d/32]
@@ -209,8 +212,36 @@ hipError_t launch_decode1_bf16(const Decode1Args& a, const SelectOut& o, int num
 // The whole single-token layer (routing, gate/up, down, combine) in one launch (MOE_CONFIG_FUSED;
 // bf16, no shared expert, d and f <= kStreamXlMaxK).
 hipError_t launch_decode1_fused(const Decode1Args& a, int num_cus, hipStream_t s);
+// (w null: every weight 1)
 hipError_t launch_combine(const void* y, const int32_t* slot_dst, const float* w, int T, int k,
                           int d, const void* shared_y, void* out, hipStream_t s);
 hipError_t launch_quant_act(const void* x, int T, int d, uint8_t* xq, float* xs, hipStream_t s);
+
+// int8 weights and rows: one grouped GEMM (each kernel launched only when its list may hold tiles),
+// one dense product [M][K] x [N][K] -> bf16 [M][N] (tiled weights, N % 16 == 0, K % 128 == 0), and
+// the rows' quantisation (bf16, or fp32 when f32; d % 8 == 0, d <= 32768).
+hipError_t launch_gemms_i8(const SelectOut& o, int gemm, int num_cus, int64_t max_rows, bool stream,
+                           bool mfma, hipStream_t s);
+hipError_t launch_gemm_i8(const void* xq, const float* xs, int M, const void* wq, const float* ws,
+                          int N, int K, void* y, int num_cus, hipStream_t s);
+hipError_t launch_quant_i8(const void* x, bool f32, int T, int d, uint8_t* q, float* qs,
+                           hipStream_t s);
+
+// RMS norm (fmt: 0 bf16 only, 1 e4m3 per 128, 2 e4m3 with E8M0 per 32, 3 int8 rows) and its gradient
+// (part: rmsnorm_grad_parts(T) rows of d partial sums, unused when dw is null).
+hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float eps, int T, int d,
+                          int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s);
+constexpr int kNormGradBlocks = 512;
+int rmsnorm_grad_parts(int T);
+hipError_t launch_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* w,
+                               float eps, int T, int d, void* dx, float* dw, float* part,
+                               hipStream_t s);
+
+// Gradients of combine and route (permute's is launch_combine without weights).
+hipError_t launch_combine_grad(const void* dout, const void* y, const int32_t* slot_dst,
+                               const float* w, int T, int k, int d, void* dy, float* dw,
+                               hipStream_t s);
+hipError_t launch_route_grad(const int32_t* ids, const float* w, const float* dw, int T, int E,
+                             int k, float* dl, hipStream_t s);
 
 }  // namespace moe

@@ -128,6 +128,19 @@ __device__ __forceinline__ int pop_tile_two_class(int32_t* queues0, int32_t* que
   return -1;
 }
 
+// The two-class order's split of an XCD's g = grid / kXcds workgroups: the first r0 start on class 0
+// (pref = 0), in proportion to the classes' estimated CU time; each class's XCD chunk (b0, b1) is
+// the number of workgroups that start on it.
+__device__ __forceinline__ void two_class_split(int grid, int n0, int n1, int& pref, int& b0, int& b1) {
+  const int g = max(1, grid / kXcds);
+  const long long w0 = (long long)kTwoClassW0 * n0, w1 = (long long)kTwoClassW1 * n1;
+  int r0 = n1 == 0 ? g : n0 == 0 ? 0 : (int)((g * w0 + (w0 + w1) / 2) / (w0 + w1));
+  if (n0 > 0 && n1 > 0) r0 = min(max(r0, 1), g - 1);
+  pref = (int)(blockIdx.x / kXcds) < r0 ? 0 : 1;
+  b0 = max(r0, 1);
+  b1 = max(g - r0, 1);
+}
+
 // Queue position -> tile index in the mixed order: the L class-1 tiles spread evenly between the
 // H class-0 ones (class-0 tiles are [0, H) in tile order, class-1 ones [H, H + L)): among the first
 // p positions, floor(p * H / (H + L)) are class 0.  (32-bit products while they fit.)

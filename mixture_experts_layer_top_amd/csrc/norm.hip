@@ -1,0 +1,343 @@
+// RMS norm in front of the layer, with the residual's addition and an 8-bit output, its gradient,
+// and the int8 row quantisation.
+//
+//   h = bf16(x + r) (h = x without a residual), n = h / sqrt(mean(h^2) + eps), y = n * w
+//   outputs: h, bf16(y), and y in the activation format of the experts' weights (from the fp32 y,
+//   one rounding): e4m3 with an fp32 scale per 128 channels, e4m3 with an E8M0 scale per 32, or
+//   int8 with an fp32 scale per row.
+// gradient (g = dy * w, dh the gradient that arrives at h on the residual path):
+//   dx = (g - n * mean(g * n)) / sqrt(mean(h^2) + eps) + dh, for x and for r alike
+//   dw[c] = sum_t dy[t][c] * n[t][c]
+//
+// All of it is bound by HBM: a row is read once into registers, both passes over it (the sum of
+// squares, then the scaling) run from there, and the 8-bit output costs no second read of y.  The
+// sum of squares is held in fp64 across a row: the terms are exact in fp32 and the chip's fp64 rate
+// is far above what the memory asks for.
+#include <type_traits>
+
+#include "fp8_codec.h"
+#include "kernels.h"
+#include "mx_codec.h"
+#include "rows_dev.h"
+
+namespace moe {
+
+namespace {
+
+enum NormFormat { kNormBf16 = 0, kNormFp8 = 1, kNormMx = 2, kNormI8 = 3 };
+
+// 1 / sqrt(sum / d + eps); NaN when the sum of squares is not finite (an infinity or NaN in the
+// row), so that the whole row shows it.
+__device__ __forceinline__ float row_rstd(double sum, double inv_d, float eps) {
+  const float m = float(sum * inv_d) + eps;
+  return m < __uint_as_float(kInfBits) ? 1.0f / sqrtf(m) : __uint_as_float(0x7FC00000u);
+}
+
+template <int FMT, int R, int V>
+__global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
+    const void* x, const void* res, const void* __restrict__ w, float eps, double inv_d, int T,
+    int nvec, void* h_out, void* y, uint8_t* q, void* qs) {
+  __shared__ double red[R / 64];
+  __shared__ uint32_t redm[R / 64];
+  const int row = R == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (R == 64 && row >= T) return;  // (whole wavefronts; no barrier in this form)
+  const int i = R == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const size_t base = (size_t)row * nvec;
+  uint4 hv[V], rv[V];
+#pragma unroll
+  for (int s = 0; s < V; ++s) hv[s] = ld16(x, base + min(i + R * s, nvec - 1));
+  if (res) {
+#pragma unroll
+    for (int s = 0; s < V; ++s) rv[s] = ld16(res, base + min(i + R * s, nvec - 1));
+  }
+  double sum[1] = {0.0};
+#pragma unroll
+  for (int s = 0; s < V; ++s) {
+    const bool in = i + R * s < nvec;
+    float h[8];
+    unpack8(hv[s], h);
+    if (res) {
+      float r[8];
+      unpack8(rv[s], r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] += r[j];
+      hv[s] = pack8(h);
+      unpack8(hv[s], h);
+    }
+    if (in) {
+      if (h_out) st16(h_out, base + i + R * s, hv[s]);
+      float p = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p = fmaf(h[j], h[j], p);
+      sum[0] += (double)p;
+    }
+  }
+  row_reduce<R>(sum, red, SumOp{});
+  const float rstd = row_rstd(sum[0], inv_d, eps);
+  auto yvec = [&](int s, float (&v)[8]) {
+    float wv[8];
+    unpack8(ld16(w, min(i + R * s, nvec - 1)), wv);
+    unpack8(hv[s], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * wv[j];
+  };
+  double inv = 0.0;
+  if (FMT == kNormI8) {
+    uint32_t m[1] = {0u};
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      float v[8];
+      yvec(s, v);
+      if (i + R * s < nvec) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[0] = max(m[0], abs_bits(v[j]));
+      }
+    }
+    row_reduce<R>(m, redm, MaxOp{});
+    const float sc = i8_scale(m[0]);
+    inv = m[0] < kInfBits ? 1.0 / (double)sc : 0.0;
+    if (i == 0) static_cast<float*>(qs)[row] = sc;
+  }
+#pragma unroll
+  for (int s = 0; s < V; ++s) {
+    const int idx = i + R * s;
+    float v[8];
+    yvec(s, v);
+    uint32_t m = 0u;
+    if (FMT == kNormFp8 || FMT == kNormMx) {
+      // (the 16 or 4 lanes of a scale group are in or out together: d % 128 == 0, d % 32 == 0)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+      m = group_max<FMT == kNormFp8 ? 16 : 4>(m);
+    }
+    if (idx >= nvec) continue;
+    if (y) st16(y, base + idx, pack8(v));
+    if (FMT == kNormI8) {
+      const bool bad = inv == 0.0;  // (the row's scale is NaN; codes 0)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = bad ? 0.f : v[j];
+      st8(q, (base + idx) * 8, i8_pack4(v, inv), i8_pack4(v + 4, inv));
+    }
+    if (FMT == kNormFp8 || FMT == kNormMx) {
+      const bool bad = m >= kInfBits;
+      double f;
+      if (FMT == kNormFp8) {
+        float sc = float(double(__uint_as_float(m)) / 448.0);
+        if (sc == 0.0f) sc = 1.0f;
+        if (bad) sc = 1.0f;
+        f = 1.0 / (double)sc;
+        if ((idx & 15) == 0) static_cast<float*>(qs)[base / 16 + idx / 16] = sc;
+      } else {
+        const int X = bad ? 127 : mx_scale_code(__uint_as_float(m));
+        f = (double)mx_inv_scale(X);
+        if ((idx & 3) == 0) gstore_u8(static_cast<uint8_t*>(qs), base / 4 + idx / 4, X);
+      }
+      uint32_t p[2] = {0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        p[j >> 2] |= uint32_t(e4m3_encode(bad ? 0.f : float(double(v[j]) * f))) << (8 * (j & 3));
+      if (bad) p[0] = p[1] = 0x7F7F7F7Fu;  // NaN codes
+      st8(q, (base + idx) * 8, p[0], p[1]);
+    }
+  }
+}
+
+// x [T][d] bf16 or fp32 -> int8 rows and their scales.
+template <bool F32, int R, int V>
+__global__ __launch_bounds__(row_block(R)) void quant_i8_kernel(const void* __restrict__ x, int T,
+                                                                int nvec, uint8_t* __restrict__ q,
+                                                                float* __restrict__ qs) {
+  __shared__ uint32_t redm[R / 64];
+  const int row = R == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (R == 64 && row >= T) return;
+  const int i = R == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const size_t base = (size_t)row * nvec;
+  uint4 a[V], b[F32 ? V : 1];
+#pragma unroll
+  for (int s = 0; s < V; ++s) {
+    const size_t idx = base + min(i + R * s, nvec - 1);
+    a[s] = ld16(x, F32 ? 2 * idx : idx);
+    if (F32) b[F32 ? s : 0] = ld16(x, 2 * idx + 1);
+  }
+  auto vec = [&](int s, float (&v)[8]) {
+    if (F32) {
+      const uint4 c = b[F32 ? s : 0];
+      const uint32_t p[8] = {a[s].x, a[s].y, a[s].z, a[s].w, c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(p[j]);
+    } else {
+      unpack8(a[s], v);
+    }
+  };
+  uint32_t m[1] = {0u};  // (clamped loads repeat a value of the row: the maximum is unchanged)
+#pragma unroll
+  for (int s = 0; s < V; ++s) {
+    float v[8];
+    vec(s, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m[0] = max(m[0], abs_bits(v[j]));
+  }
+  row_reduce<R>(m, redm, MaxOp{});
+  const float sc = i8_scale(m[0]);
+  const bool bad = m[0] >= kInfBits;
+  const double inv = bad ? 0.0 : 1.0 / (double)sc;
+  if (i == 0) qs[row] = sc;
+#pragma unroll
+  for (int s = 0; s < V; ++s) {
+    if (i + R * s >= nvec) continue;
+    float v[8];
+    vec(s, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = bad ? 0.f : v[j];
+    st8(q, (base + i + R * s) * 8, i8_pack4(v, inv), i8_pack4(v + 4, inv));
+  }
+}
+
+// Norm gradient: every workgroup takes rows blockIdx.x, + gridDim.x, ... and keeps its share of dw
+// in registers; part [gridDim.x][d] receives it (summed by dw_reduce_kernel, in a fixed order).
+template <int R, int V>
+__global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
+    const void* dy, const void* dh, const void* h, const void* __restrict__ w, float eps,
+    double inv_d, int T, int nvec, void* dx, float* __restrict__ part) {
+  __shared__ double red[2][2 * R / 64];
+  const int i = threadIdx.x;
+  float dw[V][8];
+#pragma unroll
+  for (int s = 0; s < V; ++s)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[s][j] = 0.f;
+  int turn = 0;
+  for (int row = blockIdx.x; row < T; row += gridDim.x, turn ^= 1) {
+    const size_t base = (size_t)row * nvec;
+    uint4 hv[V], gv[V], av[V];
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      const size_t idx = base + min(i + R * s, nvec - 1);
+      hv[s] = ld16(h, idx);
+      gv[s] = ld16(dy, idx);
+      if (dh) av[s] = ld16(dh, idx);
+    }
+    double sum[2] = {0.0, 0.0};
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      float a[8], g[8], wv[8];
+      unpack8(hv[s], a);
+      unpack8(gv[s], g);
+      unpack8(ld16(w, min(i + R * s, nvec - 1)), wv);
+      float p = 0.f, c = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p = fmaf(a[j], a[j], p);
+        c = fmaf(g[j] * wv[j], a[j], c);
+      }
+      if (i + R * s < nvec) {
+        sum[0] += (double)p;
+        sum[1] += (double)c;
+      }
+    }
+    // (two buffers in turn: a wavefront that is a row ahead writes the other one)
+    row_reduce<R>(sum, red[turn], SumOp{});
+    const float rstd = row_rstd(sum[0], inv_d, eps);
+    const float c = float(sum[1] * inv_d) * rstd * rstd;
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      float a[8], g[8], wv[8], add[8], o[8];
+      unpack8(hv[s], a);
+      unpack8(gv[s], g);
+      unpack8(ld16(w, min(i + R * s, nvec - 1)), wv);
+      if (dh) unpack8(av[s], add);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[s][j] = fmaf(g[j], a[j] * rstd, dw[s][j]);
+        o[j] = rstd * fmaf(-c, a[j], g[j] * wv[j]);
+        if (dh) o[j] += add[j];
+      }
+      if (i + R * s < nvec) st16(dx, base + i + R * s, pack8(o));
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int s = 0; s < V; ++s) {
+    const int idx = i + R * s;
+    if (idx >= nvec) continue;
+    float* p = part + ((size_t)blockIdx.x * nvec + idx) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; j += 4)
+      gstore16(p + j, 0, make_uint4(__float_as_uint(dw[s][j]), __float_as_uint(dw[s][j + 1]),
+                                    __float_as_uint(dw[s][j + 2]), __float_as_uint(dw[s][j + 3])));
+  }
+}
+
+// dw[c] = sum_b part[b][c]: 8 columns per workgroup, 32 threads take every 32nd partial of a
+// column, then their sums in order.
+__global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict__ part, int nb, int d,
+                                                        float* __restrict__ dw) {
+  __shared__ float red[32][9];
+  const int c = threadIdx.x & 7, r = threadIdx.x >> 3, col = blockIdx.x * 8 + c;
+  float s = 0.f;
+  for (int b = r; b < nb; b += 32) s += part[(size_t)b * d + col];
+  red[r][c] = s;
+  __syncthreads();
+  if (r == 0) {
+    for (int b = 1; b < 32; ++b) s += red[b][c];
+    dw[col] = s;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float eps, int T, int d,
+                          int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s) {
+  if (T == 0) return hipSuccess;
+  const int nvec = d / 8;
+  with_row_shape(nvec, [&](auto Rc, auto Vc) {
+    constexpr int R = decltype(Rc)::value, V = decltype(Vc)::value;
+    const unsigned grid = R == 64 ? ((unsigned)T + 3) / 4 : (unsigned)T;
+    auto go = [&](auto F) {
+      rmsnorm_kernel<decltype(F)::value, R, V><<<grid, row_block(R), 0, s>>>(
+          x, res, w, eps, 1.0 / d, T, nvec, h_out, y, static_cast<uint8_t*>(q), qs);
+    };
+    if (fmt == kNormFp8) go(std::integral_constant<int, kNormFp8>{});
+    else if (fmt == kNormMx) go(std::integral_constant<int, kNormMx>{});
+    else if (fmt == kNormI8) go(std::integral_constant<int, kNormI8>{});
+    else go(std::integral_constant<int, kNormBf16>{});
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_i8(const void* x, bool f32, int T, int d, uint8_t* q, float* qs,
+                           hipStream_t s) {
+  if (T == 0) return hipSuccess;
+  const int nvec = d / 8;
+  with_row_shape(nvec, [&](auto Rc, auto Vc) {
+    constexpr int R = decltype(Rc)::value, V = decltype(Vc)::value;
+    const unsigned grid = R == 64 ? ((unsigned)T + 3) / 4 : (unsigned)T;
+    if (f32) quant_i8_kernel<true, R, V><<<grid, row_block(R), 0, s>>>(x, T, nvec, q, qs);
+    else quant_i8_kernel<false, R, V><<<grid, row_block(R), 0, s>>>(x, T, nvec, q, qs);
+  });
+  return hipGetLastError();
+}
+
+// Partial sums of dw: one per workgroup.
+int rmsnorm_grad_parts(int T) { return T < kNormGradBlocks ? T : kNormGradBlocks; }
+
+hipError_t launch_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* w,
+                               float eps, int T, int d, void* dx, float* dw, float* part,
+                               hipStream_t s) {
+  const int nvec = d / 8, nb = rmsnorm_grad_parts(T);
+  if (T > 0) {
+    auto go = [&](auto Rc, auto Vc) {
+      constexpr int R = decltype(Rc)::value, V = decltype(Vc)::value;
+      rmsnorm_grad_kernel<R, V><<<nb, R, 0, s>>>(dy, dh, h, w, eps, 1.0 / d, T, nvec, dx,
+                                                 dw ? part : nullptr);
+    };
+    if (nvec <= 64) go(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 128) go(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 1024) with_steps<256, 1, 4>((nvec + 255) / 256, go);
+    else with_steps<512, 3, 4>((nvec + 511) / 512, go);
+  }
+  if (dw) dw_reduce_kernel<<<nvec, 256, 0, s>>>(part, nb, d, dw);
+  return hipGetLastError();
+}
+
+}  // namespace moe

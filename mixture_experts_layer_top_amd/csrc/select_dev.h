@@ -82,7 +82,7 @@ __device__ __forceinline__ void select_block(const SelectArgs& a, const SelectOu
   const bool shared = e == a.E;
   const int ffe = shared ? a.f_sh : a.f;
   // The policy ("Decoding the Skew", Abstract: the live histogram matched to offline-tuned
-  // configurations): bf16 problems in automatic mode look it up by T and the live effective expert
+  // configurations): bf16 (and int8) problems in automatic mode look it up by T and the live effective expert
   // count; config >= kConfigPolicy0 forces one; forced families (config 0 / 1) and the streaming-only
   // formats use none.
   const bool bf16 = !a.fp8 && !a.w4;
@@ -224,7 +224,7 @@ __device__ __forceinline__ void select_block(const SelectArgs& a, const SelectOu
       }
   }
 
-  const size_t wb = a.fp8 ? 1 : 2;
+  const size_t wb = a.fp8 || a.i8 ? 1 : 2;
   const int kb_d = a.d / 128, kb_f = ffe / 128;
   const int row0 = (e < nexp && !shared) ? (lds_offsets ? lds_offsets[e] : gload_i32(a.offsets, e)) : 0;
 #pragma unroll
@@ -260,7 +260,7 @@ __device__ __forceinline__ void select_block(const SelectArgs& a, const SelectOu
         const size_t eo = (size_t)e * ffe * (a.d / 32);
         sg.e0 = a.e_gate ? a.e_gate + eo : nullptr;
         sg.e1 = a.e_up ? a.e_up + eo : nullptr;
-        const size_t so = (size_t)e * kb_f * kb_d;
+        const size_t so = a.i8 ? (size_t)e * ffe : (size_t)e * kb_f * kb_d;
         sg.w0 = static_cast<const uint8_t*>(a.w_gate) + wo;
         sg.w1 = static_cast<const uint8_t*>(a.w_up) + wo;
         sg.s0 = a.s_gate ? a.s_gate + so : nullptr;
@@ -280,19 +280,19 @@ __device__ __forceinline__ void select_block(const SelectArgs& a, const SelectOu
       sg.ae = a.mx8 && !shared ? a.he : nullptr;
       sg.oute = nullptr;
       if (shared) {
-        sg.a = a.h_sh;
+        sg.a = a.i8 ? a.h_shq : a.h_sh;
         sg.as = a.hs_sh;
         sg.w0 = a.sh_down;
         sg.e0 = nullptr;
         sg.s0 = a.s_sh_down;
         sg.out = a.y_sh;
       } else {
-        sg.a = a.h;
+        sg.a = a.i8 ? a.hq : a.h;
         sg.as = a.hs;
         sg.w0 = static_cast<const uint8_t*>(a.w_down) +
                 (a.w4 ? (size_t)e * a.d * (ffe / 2) : (size_t)e * a.d * ffe * wb);
         sg.e0 = a.e_down ? a.e_down + (size_t)e * a.d * (ffe / 32) : nullptr;
-        sg.s0 = a.s_down ? a.s_down + (size_t)e * kb_d * kb_f : nullptr;
+        sg.s0 = a.s_down ? a.s_down + (a.i8 ? (size_t)e * a.d : (size_t)e * kb_d * kb_f) : nullptr;
         sg.out = a.y;
       }
     }

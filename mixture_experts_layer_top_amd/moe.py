@@ -17,13 +17,13 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MOE_MI355X_LIB", os.path.join(_PKG, "libmoe_mi355x.so"))
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
-DTYPE_BF16, DTYPE_FP8, DTYPE_MXFP4, DTYPE_MXFP4_A8 = 0, 1, 2, 3
+DTYPE_BF16, DTYPE_FP8, DTYPE_MXFP4, DTYPE_MXFP4_A8, DTYPE_INT8 = 0, 1, 2, 3, 4
 CONFIG_AUTO, CONFIG_STREAM, CONFIG_MFMA, CONFIG_FUSED = -1, 0, 1, 2
 FUSED_SYNC_BYTES = 36864    # the fused single-token launch's counters at the workspace's start
 CONFIG_POLICY0, NUM_POLICIES = 16, 8  # config = 16 + i forces selection policy i (bf16)
 LAYOUT_ROW_MAJOR, LAYOUT_TILED = 0, 1
 
-_vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 
 
 class Problem(ctypes.Structure):
@@ -82,6 +82,14 @@ def lib() -> ctypes.CDLL:
             "moe_fp8_tile": (_i, [_vp, _vp, ctypes.c_int64, ctypes.c_int64, _vp]),
             "moe_layer_noalloc": (_i, [ctypes.POINTER(Problem), _vp, _vp, ctypes.POINTER(Weights),
                                        _vp, ctypes.POINTER(Routing), _vp]),
+            "moe_quant_act_i8": (_i, [_vp, _i, _i, _vp, _vp, _vp]),
+            "moe_gemm_i8": (_i, [_vp, _vp, _i, _vp, _vp, _i, _i, _vp, _vp]),
+            "moe_rmsnorm": (_i, [_vp, _vp, _vp, _f, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+            "moe_rmsnorm_grad": (_i, [_vp, _vp, _vp, _vp, _f, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+            "moe_rmsnorm_grad_workspace_bytes": (_sz, [_i, _i]),
+            "moe_route_grad": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
+            "moe_combine_grad": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp]),
+            "moe_permute_grad": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -94,7 +102,9 @@ EXPORTED = ("moe_route", "moe_permute", "moe_permute_workspace_bytes", "moe_quan
             "moe_quant_act_mx",
             "moe_grouped_ffn", "moe_grouped_ffn_workspace_bytes", "moe_combine", "moe_layer",
             "moe_layer_workspace_bytes", "moe_layer_traced", "moe_status_string", "moe_mxfp4_tile",
-            "moe_fp8_tile", "moe_layer_noalloc")
+            "moe_fp8_tile", "moe_layer_noalloc", "moe_quant_act_i8", "moe_gemm_i8", "moe_rmsnorm",
+            "moe_rmsnorm_grad", "moe_rmsnorm_grad_workspace_bytes", "moe_route_grad",
+            "moe_combine_grad", "moe_permute_grad")
 
 NOALLOC_SCRATCH_BYTES = 128 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -148,8 +158,8 @@ class ExpertWeights:
             setattr(w, name, _ptr(getattr(self, key)))
         w.layout = LAYOUT_ROW_MAJOR
         if self.wdtype != DTYPE_BF16:
-            # fp8 / mxfp4 bytes count as tiled only if every weight tensor came from fp8_tile or
-            # mxfp4_tile (the library rejects row-major bytes of these formats)
+            # fp8 / int8 / mxfp4 bytes count as tiled only if every weight tensor came from fp8_tile,
+            # int8_tile or mxfp4_tile (the library rejects row-major bytes of these formats)
             mats = [self.gate, self.up, self.down] + (
                 [self.sh_gate, self.sh_up, self.sh_down] if self.has_shared else [])
             if all(getattr(t, "_moe_tiled", False) for t in mats):
@@ -160,6 +170,8 @@ class ExpertWeights:
     def wdtype(self) -> int:
         if self.e_gate is not None:
             return DTYPE_MXFP4_A8 if self.act_mx8 else DTYPE_MXFP4
+        if self.gate.dtype == torch.int8:
+            return DTYPE_INT8
         return DTYPE_FP8 if self.gate.dtype == torch.uint8 else DTYPE_BF16
 
     @property
@@ -198,7 +210,8 @@ def route(logits: torch.Tensor, k: int):
 def permute(ids: torch.Tensor, E: int, x: torch.Tensor | None = None,
             x_scale: torch.Tensor | None = None):
     """Returns counts, offsets, perm_src, slot_dst (and x_perm, x_perm_scale if x is given).
-    x: bf16 [T, d] as int16 bits, or e4m3 [T, d] uint8 (with x_scale [T, d/128])."""
+    x: bf16 [T, d] as int16 bits, e4m3 [T, d] uint8 (with x_scale [T, d/128]) or int8 [T, d] (with
+    x_scale [T])."""
     T, k = ids.shape
     dev = _dev(ids)
     n = T * k
@@ -212,10 +225,11 @@ def permute(ids: torch.Tensor, E: int, x: torch.Tensor | None = None,
     act = DTYPE_BF16
     if x is not None:
         d = x.shape[1]
-        act = DTYPE_FP8 if x.dtype == torch.uint8 else DTYPE_BF16
+        act = {torch.uint8: DTYPE_FP8, torch.int8: DTYPE_INT8}.get(x.dtype, DTYPE_BF16)
         xp = torch.empty((n, d), dtype=x.dtype, device=dev)
         if x_scale is not None:
-            xps = torch.empty((n, d // 128), dtype=torch.float32, device=dev)
+            shape = (n,) if act == DTYPE_INT8 else (n, d // 128)
+            xps = torch.empty(shape, dtype=torch.float32, device=dev)
     _check(lib().moe_permute(_ptr(ids), T, E, k, _ptr(x), _ptr(x_scale), d, act, _ptr(counts),
                              _ptr(offsets), _ptr(perm_src), _ptr(slot_dst), _ptr(xp), _ptr(xps),
                              _ptr(ws), ws.numel(), _stream()), "moe_permute")
@@ -287,6 +301,173 @@ def combine(y_perm, slot_dst, topk_w, shared_y=None):
     _check(lib().moe_combine(_ptr(y_perm), _ptr(slot_dst), _ptr(topk_w), T, k, d, _ptr(shared_y),
                              _ptr(out), _stream()), "moe_combine")
     return out
+
+
+# ------------------------------------------------------------------------------------------------
+# int8 products, RMS norm, gradients
+#
+# bf16 tensors are torch.bfloat16 or their bits as torch.int16, like the rest of this module's; outputs
+# take the input's choice.  Tensors must be contiguous and on one GPU, which need not be the current
+# one: a call runs on that GPU's current stream.
+# ------------------------------------------------------------------------------------------------
+
+def _arg(t, name, shape, *dtypes):
+    """t itself, checked: a contiguous GPU tensor of this shape and one of these types."""
+    if t.dtype not in dtypes:
+        raise MoEError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise MoEError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise MoEError(f"{name} must be contiguous")
+    _dev(t)
+    return t
+
+
+_BF16 = (torch.bfloat16, torch.int16)
+_I8, _I32, _F32 = (torch.int8,), (torch.int32,), (torch.float32,)
+
+
+def _rows(t, name):
+    if t.dim() != 2:
+        raise MoEError(f"{name} must have two dimensions, not {t.dim()}")
+    return t.shape
+
+
+def _call(name, dev, *args):
+    """One library call on dev's current stream; tensors among args must live on dev."""
+    for a in args:
+        if isinstance(a, torch.Tensor) and a.device != dev:
+            raise MoEError(f"{name}: tensors on {a.device} and {dev}")
+    raw = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        _check(getattr(lib(), name)(*raw, stream), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(getattr(lib(), name)(*raw, stream), name)
+
+
+def quant_act_i8(x: torch.Tensor):
+    """bf16 [T, d] -> int8 codes [T, d] and fp32 scales [T] (per token; or per channel of weights)."""
+    T, d = _rows(x, "x")
+    _arg(x, "x", (T, d), *_BF16)
+    xq = torch.empty((T, d), dtype=torch.int8, device=x.device)
+    xs = torch.empty(T, dtype=torch.float32, device=x.device)
+    _call("moe_quant_act_i8", x.device, x, T, d, xq, xs)
+    return xq, xs
+
+
+def int8_tile(w: torch.Tensor) -> torch.Tensor:
+    """Row-major int8 weights [..., rows, cols] -> the library's tiled layout (moe_fp8_tile: the layout
+    is the same for every one-byte format)."""
+    if w.dtype != torch.int8:
+        raise MoEError(f"w must be torch.int8, not {w.dtype}")
+    _dev(w)
+    return fp8_tile(w)
+
+
+def gemm_i8(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor):
+    """bf16 [M, N] = (xq [M, K] * xs [M]) (w [N, K] * w_scale [N])^T; w from int8_tile."""
+    (M, K), (N, _) = _rows(xq, "xq"), _rows(w, "w")
+    _arg(xq, "xq", (M, K), *_I8)
+    _arg(xs, "xs", (M,), *_F32)
+    _arg(w, "w", (N, K), *_I8)
+    _arg(w_scale, "w_scale", (N,), *_F32)
+    if not getattr(w, "_moe_tiled", False):
+        raise MoEError("w must come from int8_tile")
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+    _call("moe_gemm_i8", xq.device, xq, xs, M, w, w_scale, N, K, y)
+    return y
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+            eps: float = 1e-6, act_dtype: int = DTYPE_BF16, want_y: bool = True):
+    """RMS norm of h = x + residual.  Returns (h, y, q, q_scale): h is x itself without a residual, y is
+    None when not wanted (8-bit outputs only), q and q_scale are the activations that experts of format
+    act_dtype take (DTYPE_FP8: e4m3 uint8 and fp32 [T, d/128]; DTYPE_MXFP4_A8: e4m3 and E8M0 uint8
+    [T, d/32]; DTYPE_INT8: int8 and fp32 [T]; DTYPE_BF16: None)."""
+    T, d = _rows(x, "x")
+    _arg(x, "x", (T, d), *_BF16)
+    _arg(weight, "weight", (d,), *_BF16)
+    dev = x.device
+    h = x
+    if residual is not None:
+        _arg(residual, "residual", (T, d), *_BF16)
+        h = torch.empty_like(x)
+    q = qs = None
+    if act_dtype != DTYPE_BF16:
+        q = torch.empty((T, d), dtype=torch.int8 if act_dtype == DTYPE_INT8 else torch.uint8, device=dev)
+        if act_dtype == DTYPE_INT8:
+            qs = torch.empty(T, dtype=torch.float32, device=dev)
+        elif act_dtype == DTYPE_FP8:
+            qs = torch.empty((T, d // 128), dtype=torch.float32, device=dev)
+        else:
+            qs = torch.empty((T, d // 32), dtype=torch.uint8, device=dev)
+    y = torch.empty_like(x) if want_y or act_dtype == DTYPE_BF16 else None
+    _call("moe_rmsnorm", dev, x, residual, weight, eps, T, d, act_dtype,
+          h if residual is not None else None, y, q, qs)
+    return h, y, q, qs
+
+
+def rmsnorm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                 dh: torch.Tensor | None = None, eps: float = 1e-6, want_dweight: bool = True):
+    """Gradient of rmsnorm's y (and of h on the residual path, dh): (dx [T, d], dweight fp32 [d] or
+    None).  dx is the gradient of x and of residual alike."""
+    T, d = _rows(dy, "dy")
+    _arg(dy, "dy", (T, d), *_BF16)
+    _arg(h, "h", (T, d), *_BF16)
+    _arg(weight, "weight", (d,), *_BF16)
+    if dh is not None:
+        _arg(dh, "dh", (T, d), *_BF16)
+    dx = torch.empty_like(dy)
+    dw = ws = None
+    nws = 0
+    if want_dweight:
+        dw = torch.empty(d, dtype=torch.float32, device=dy.device)
+        nws = lib().moe_rmsnorm_grad_workspace_bytes(T, d)
+        ws = torch.empty(max(1, nws), dtype=torch.uint8, device=dy.device)
+    _call("moe_rmsnorm_grad", dy.device, dy, dh, h, weight, eps, T, d, dx, dw, ws, nws)
+    return dx, dw
+
+
+def route_grad(ids: torch.Tensor, w: torch.Tensor, dw: torch.Tensor, E: int):
+    """Gradient of route: ids, w, dw [T, k] -> dlogits fp32 [T, E]."""
+    T, k = _rows(ids, "ids")
+    _arg(ids, "ids", (T, k), *_I32)
+    _arg(w, "w", (T, k), *_F32)
+    _arg(dw, "dw", (T, k), *_F32)
+    dl = torch.empty((T, E), dtype=torch.float32, device=ids.device)
+    _call("moe_route_grad", ids.device, ids, w, dw, T, E, k, dl)
+    return dl
+
+
+def combine_grad(dout: torch.Tensor, y_perm: torch.Tensor, slot_dst: torch.Tensor, topk_w: torch.Tensor):
+    """Gradient of combine: (dy_perm [T*k, d], dtopk_w fp32 [T, k]); shared_y's is dout."""
+    T, k = _rows(topk_w, "topk_w")
+    d = _rows(dout, "dout")[1]
+    _arg(topk_w, "topk_w", (T, k), *_F32)
+    _arg(dout, "dout", (T, d), *_BF16)
+    _arg(y_perm, "y_perm", (T * k, d), *_BF16)
+    _arg(slot_dst, "slot_dst", (T * k,), *_I32)
+    dy = torch.empty_like(y_perm)
+    dw = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+    _call("moe_combine_grad", dout.device, dout, y_perm, slot_dst, topk_w, T, k, d, dy, dw)
+    return dy, dw
+
+
+def permute_grad(dx_perm: torch.Tensor, slot_dst: torch.Tensor, k: int, add: torch.Tensor | None = None):
+    """Gradient of permute's gather: dx [T, d] = each token's k rows of dx_perm summed (+ add)."""
+    n, d = _rows(dx_perm, "dx_perm")
+    if k < 1 or n % k:
+        raise MoEError(f"dx_perm has {n} rows, not a multiple of k = {k}")
+    T = n // k
+    _arg(dx_perm, "dx_perm", (n, d), *_BF16)
+    _arg(slot_dst, "slot_dst", (n,), *_I32)
+    if add is not None:
+        _arg(add, "add", (T, d), *_BF16)
+    dx = torch.empty((T, d), dtype=dx_perm.dtype, device=dx_perm.device)
+    _call("moe_permute_grad", dx_perm.device, dx_perm, slot_dst, add, T, k, d, dx)
+    return dx
 
 
 class Layer:

@@ -10,4 +10,5 @@ Modules:
   fp8_e4m3   OCP E4M3FN codec written from the format definition.
   mxfp4      OCP MXFP4 (E2M1 elements, E8M0 scales per 32) written from the format definitions.
   moe_oracle the layer, step by step, in float64.
+  rows       RMS norm, int8 rows and products, and the gradients of route, combine and the gather.
 """

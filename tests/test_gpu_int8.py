@@ -1,0 +1,307 @@
+"""GPU: int8 rows and products, alone, as experts and in the whole layer.
+
+Sums are exact integers, so a product's value differs from the exact one by the fp32 scaling (the sum's
+conversion and two products: 2^-22) and bf16's rounding (2^-8), and every tile family gives the same
+bits.  For the experts, codes of h that lie within fp32 error of a half step may go either way; the
+oracle says what those can do to y."""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_top_amd import inputs as I
+from mixture_experts_layer_top_amd import moe as _moe
+from oracle import moe_oracle as O
+from oracle import rows as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    _moe.lib()
+    return _moe
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _bf16(*shape, seed=0, std=1.0):
+    return (torch.randn(*shape, generator=_gen(seed)) * std).to(torch.bfloat16).cuda()
+
+
+def _codes(*shape, seed=0):
+    return torch.randint(-128, 128, shape, generator=_gen(seed), dtype=torch.int16).to(torch.int8).cuda()
+
+
+def _scales(*shape, seed=0, mid=1e-3):
+    return ((torch.rand(*shape, generator=_gen(seed)) + 0.5) * mid).cuda()
+
+
+@pytest.mark.parametrize("T,d", [(1, 16), (1, 7168), (3, 128), (77, 4096), (5, 4112), (9, 8192), (2, 32768)])
+def test_quant_act_i8(moe, T, d):
+    x = _bf16(T, d, seed=T + d)
+    if T > 2:
+        x[1] = 0
+        x[2, 0] = -300.0
+    q, s = moe.quant_act_i8(x)
+    want_q, want_s = R.quant_i8(f64(x))
+    assert np.array_equal(f64(s), want_s)
+    # float64 quotient by the reciprocal: off by 2^-52 of it, so only exact half steps could differ,
+    # and those are exact in both
+    assert np.array_equal(f64(q), want_q)
+
+
+def test_quant_act_i8_non_finite_rows(moe):
+    x = _bf16(4, 256, seed=1)
+    x[1, 3], x[2, 255] = float("inf"), float("nan")
+    q, s = moe.quant_act_i8(x)
+    ref, sr = moe.quant_act_i8(_bf16(4, 256, seed=1))
+    assert s[1:3].isnan().all() and (q[1:3] == 0).all()
+    assert torch.equal(q[[0, 3]], ref[[0, 3]]) and torch.equal(s[[0, 3]], sr[[0, 3]])
+    assert moe.quant_act_i8(x[:0])[0].shape == (0, 256)
+
+
+GEMMS = [(1, 16, 128), (1, 2048, 7168), (16, 48, 256), (17, 256, 384), (33, 272, 128), (64, 512, 4224),
+         (65, 256, 128), (100, 528, 640), (130, 1040, 256), (257, 256, 1152), (300, 4096, 512), (1030, 2064, 384),
+         (2100, 7168, 256)]
+
+
+@pytest.mark.parametrize("M,N,K", GEMMS)
+def test_gemm_i8(moe, M, N, K):
+    xq, w = _codes(M, K, seed=M), _codes(N, K, seed=N + 1)
+    xs, ws = _scales(M, seed=K), _scales(N, seed=K + 1)
+    y = moe.gemm_i8(xq, xs, moe.int8_tile(w), ws)
+    ref = R.gemm_i8(f64(xq), f64(xs), f64(w), f64(ws))
+    assert (np.abs(f64(y) - ref) <= np.abs(ref) * (2.0 ** -8 + 2.0 ** -21)).all()
+
+
+def test_gemm_i8_extremes(moe):
+    """The longest K at the largest codes: the sum reaches 2^29 and stays exact; M = 0; rows behind the
+    last one stay as they were."""
+    K, N = 32768, 32
+    xq = torch.full((3, K), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+    one = torch.ones(N, device="cuda")
+    t = moe.int8_tile(w)
+    for M in (3, 80):
+        x = xq[:1].expand(M, K).contiguous()
+        y = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        xs = torch.ones(M, device="cuda")
+        assert moe.lib().moe_gemm_i8(x.data_ptr(), xs.data_ptr(), M, t.data_ptr(), one.data_ptr(), N, K,
+                                     y.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert (y[:M] == 2.0 ** 29).all() and (y[M:] == 7).all()
+    assert moe.gemm_i8(xq[:0], one[:0], t, one).shape == (0, N)
+    with pytest.raises(moe.MoEError, match="int8_tile"):
+        moe.gemm_i8(xq, one[:3], w, one)
+
+
+def test_gemm_i8_passes_non_finite_rows_on(moe):
+    x = _bf16(70, 256, seed=1)
+    x[5, 7] = float("nan")
+    w, ws = _codes(256, 256, seed=2), _scales(256, seed=3)
+    q, s = moe.quant_act_i8(x)
+    y = moe.gemm_i8(q, s, moe.int8_tile(w), ws)
+    assert y[5].isnan().all() and y[:5].isfinite().all() and y[6:].isfinite().all()
+
+
+# ------------------------------------------------------------------------------------------------
+# experts
+# ------------------------------------------------------------------------------------------------
+
+class Experts:
+    def __init__(self, moe, E, d, f, seed, shared_f=0):
+        def w(n, k, i, lead=()):
+            m = torch.randn(*lead, n, k, generator=_gen(seed + i)).mul_(32).round_().clamp_(-127, 127)
+            return m.to(torch.int8).cuda(), _scales(*lead, n, seed=seed + 50 + i, mid=0.02 / 32)
+
+        self.c, self.s = {}, {}
+        for i, (name, n, k) in enumerate((("gate", f, d), ("up", f, d), ("down", d, f))):
+            self.c[name], self.s["s_" + name] = w(n, k, i, (E,))
+        if shared_f:
+            for i, (name, n, k) in enumerate((("gate", shared_f, d), ("up", shared_f, d), ("down", d, shared_f))):
+                self.c["sh_" + name], self.s["s_sh_" + name] = w(n, k, 10 + i)
+        self.ew = moe.ExpertWeights(**{n: moe.int8_tile(t) for n, t in self.c.items()}, **self.s)
+        self.shared = bool(shared_f)
+
+    def get(self, e):
+        r = {n: f64(self.c[n][e]) for n in ("gate", "up", "down")}
+        r.update({"s_" + n: f64(self.s["s_" + n][e]) for n in ("gate", "up", "down")})
+        return r
+
+    def get_shared(self):
+        r = {n: f64(self.c["sh_" + n]) for n in ("gate", "up", "down")}
+        r.update({"s_" + n: f64(self.s["s_sh_" + n]) for n in ("gate", "up", "down")})
+        return r
+
+
+def _rows(counts, d, seed):
+    counts = torch.tensor(counts, dtype=torch.int32)
+    off = torch.zeros(len(counts) + 1, dtype=torch.int32)
+    off[1:] = counts.cumsum(0)
+    n = int(off[-1])
+    q = torch.randn(n, d, generator=_gen(seed)).mul_(32).round_().clamp_(-127, 127).to(torch.int8)
+    return q.cuda(), _scales(n, seed=seed + 1, mid=1.0 / 32), counts.cuda(), off.cuda()
+
+
+FFN = [  # counts per expert, d, f: one row; empty experts; short and tall tiles; odd K-step counts; tails
+    ([0, 1, 0], 128, 128), ([8] * 4, 256, 512), ([1, 0, 33, 5, 0, 17], 384, 640), ([70, 2, 0, 200], 512, 256),
+    ([300, 1, 64], 640, 384), ([16, 129, 257, 40], 4224, 256), ([3, 0, 2], 256, 4224), ([700], 256, 1152),
+]
+
+
+@pytest.mark.parametrize("counts,d,f", FFN, ids=lambda v: str(v).replace(" ", ""))
+def test_grouped_ffn(moe, counts, d, f):
+    xq, xs, cnt, off = _rows(counts, d, seed=d + f)
+    W = Experts(moe, len(counts), d, f, seed=3)
+    n = xq.shape[0]
+    out = {}
+    for name, cfg in (("auto", moe.CONFIG_AUTO), ("stream", moe.CONFIG_STREAM), ("mfma", moe.CONFIG_MFMA)):
+        out[name] = moe.grouped_ffn(xq, xs, cnt, off, W.ew, n, 1, cfg).view(torch.bfloat16)
+    assert torch.equal(out["stream"], out["mfma"]) and torch.equal(out["auto"], out["mfma"])
+    y = f64(out["auto"])
+    for e, c in enumerate(counts):
+        if c:
+            a = int(off[e])
+            ref, slack = R.expert_i8(f64(xq[a:a + c]), f64(xs[a:a + c]), W.get(e))
+            assert (np.abs(y[a:a + c] - ref) <= slack * (1 + 2.0 ** -7) + np.abs(ref) * (2.0 ** -8 + 2.0 ** -20)).all(), e
+
+
+def test_grouped_ffn_many_tiles(moe):
+    """Several rounds of tiles, full heights with tails, and the two-class order (long K)."""
+    counts = [520, 300, 0, 40, 1, 260, 128, 5]
+    xq, xs, cnt, off = _rows(counts, 4096, seed=1)
+    W = Experts(moe, len(counts), 4096, 8192, seed=5)
+    n = xq.shape[0]
+    a = moe.grouped_ffn(xq, xs, cnt, off, W.ew, n, 1, moe.CONFIG_MFMA)
+    assert torch.equal(a, moe.grouped_ffn(xq, xs, cnt, off, W.ew, n, 1, moe.CONFIG_STREAM))
+    assert torch.equal(a, moe.grouped_ffn(xq, xs, cnt, off, W.ew, n, 1))
+    y = f64(a.view(torch.bfloat16))
+    for e in (1, 4, 7):
+        s = slice(int(off[e]), int(off[e + 1]))
+        ref, slack = R.expert_i8(f64(xq[s]), f64(xs[s]), W.get(e))
+        assert (np.abs(y[s] - ref) <= slack * (1 + 2.0 ** -7) + np.abs(ref) * (2.0 ** -8 + 2.0 ** -20)).all(), e
+
+
+def test_grouped_ffn_leaves_other_rows(moe):
+    """Fewer rows than T * k: rows past offsets[E] are not written, and a NaN row stays alone."""
+    xq, xs, cnt, off = _rows([5, 0, 90], 256, seed=2)
+    W = Experts(moe, 3, 256, 256, seed=9)
+    base = moe.grouped_ffn(xq, xs, cnt, off, W.ew, 95, 1)
+    bad = xs.clone()
+    bad[7] = float("nan")
+    got = moe.grouped_ffn(xq, bad, cnt, off, W.ew, 95, 1)
+    keep = torch.arange(95, device="cuda") != 7
+    assert torch.equal(got[keep], base[keep]) and got[7].view(torch.bfloat16).isnan().all()
+    import ctypes
+    p = moe.problem(100, 256, 256, 3, 1, wdtype=moe.DTYPE_INT8)
+    ws = torch.empty(moe.lib().moe_grouped_ffn_workspace_bytes(ctypes.byref(p)), dtype=torch.uint8, device="cuda")
+    y = torch.full((100, 256), 7, dtype=torch.int16, device="cuda")
+    w = W.ew.struct()
+    assert moe.lib().moe_grouped_ffn(ctypes.byref(p), xq.data_ptr(), xs.data_ptr(), cnt.data_ptr(), off.data_ptr(),
+                                     ctypes.byref(w), y.data_ptr(), ws.data_ptr(), ws.numel(),
+                                     torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(y[:95], base) and (y[95:] == 7).all()
+
+
+LAYERS = [(1, 256, 256, 8, 2, 0), (3, 384, 128, 16, 8, 256), (33, 256, 512, 4, 2, 0), (150, 512, 256, 6, 3, 384),
+          (600, 256, 256, 2, 1, 0)]
+
+
+@pytest.mark.parametrize("T,d,f,E,k,sf", LAYERS)
+def test_layer(moe, T, d, f, E, k, sf):
+    """moe_layer on int8 experts: the steps one by one give the same bits, and the oracle's layer on the
+    quantised rows the same values."""
+    x, logits = _bf16(T, d, seed=T), torch.randn(T, E, generator=_gen(T + 1)).cuda()
+    W = Experts(moe, E, d, f, seed=11, shared_f=sf)
+    out, keep = moe.layer(logits, x.view(torch.int16), W.ew, k, keep_routing=True)
+    xq, xs = moe.quant_act_i8(x)
+    ids, w = moe.route(logits, k)
+    cnt, off, perm, slot, xp, xps = moe.permute(ids, E, xq, xs)
+    assert torch.equal(xp, xq[perm.long() // k]) and torch.equal(xps, xs[perm.long() // k])
+    y = moe.grouped_ffn(xp, xps, cnt, off, W.ew, T, k)
+    ysh = None
+    if sf:  # the shared expert as a one-expert grouped FFN of all tokens
+        one = moe.ExpertWeights(**{n: getattr(W.ew, "sh_" + n).unsqueeze(0) for n in ("gate", "up", "down")},
+                                **{"s_" + n: getattr(W.ew, "s_sh_" + n).unsqueeze(0) for n in ("gate", "up", "down")})
+        for n in ("gate", "up", "down"):
+            getattr(one, n)._moe_tiled = True
+        c = torch.tensor([T], dtype=torch.int32, device="cuda")
+        ysh = moe.grouped_ffn(xq, xs, c, torch.tensor([0, T], dtype=torch.int32, device="cuda"), one, T, 1)
+    assert torch.equal(out, moe.combine(y, slot, w, ysh))
+    ref, slack = np.zeros((T * k, d)), np.zeros((T * k, d))
+    o = off.tolist()
+    for e in range(E):
+        if o[e] < o[e + 1]:
+            s = slice(o[e], o[e + 1])
+            ref[s], slack[s] = R.expert_i8(f64(xp[s]), f64(xps[s]), W.get(e))
+    tol = slack + np.abs(ref) * 2.0 ** -7  # y is held in bf16 between the products and the combine
+    wk, sl = f64(w), slot.cpu().numpy()
+    want = (wk[..., None] * ref[sl].reshape(T, k, d)).sum(1)
+    room = (wk[..., None] * tol[sl].reshape(T, k, d)).sum(1)
+    if sf:
+        r, sk = R.expert_i8(f64(xq), f64(xs), W.get_shared())
+        want, room = want + r, room + sk + np.abs(r) * 2.0 ** -7
+    assert (np.abs(f64(out.view(torch.bfloat16)) - want) <= room * 1.01 + np.abs(want) * 2.0 ** -8).all()
+    noal = moe.layer_noalloc(logits, x.view(torch.int16), W.ew, k) if T * k < 400 else out
+    assert torch.equal(noal, out)
+
+
+def test_norm_sort_experts_together_in_a_graph(moe):
+    """The serving path: norm (bf16 and int8 rows) -> route -> permute -> int8 experts -> combine -> the
+    next norm; eager, on another stream, and captured and replayed on new inputs."""
+    T, d, f, E, k = 40, 512, 256, 8, 2
+    W = Experts(moe, E, d, f, seed=21)
+    nw, router = _bf16(d, seed=1), torch.randn(d, E, generator=_gen(2)).cuda()
+    x, res = _bf16(T, d, seed=3), _bf16(T, d, seed=4)
+
+    def step(x, res):
+        h, y, q, qs = moe.rmsnorm(x, nw, res, 1e-6, moe.DTYPE_INT8)
+        ids, w = moe.route(y.float() @ router, k)
+        cnt, off, _, slot, xp, xps = moe.permute(ids, E, q, qs)
+        o = moe.combine(moe.grouped_ffn(xp, xps, cnt, off, W.ew, T, k), slot, w).view(torch.bfloat16)
+        return moe.rmsnorm(o, nw, h)[:2]
+
+    h0, y0 = (t.clone() for t in step(x, res))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        h1, y1 = step(x, res)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(h0, h1) and torch.equal(y0, y1)
+    sx, sr = x.clone(), res.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gh, gy = step(sx, sr)
+    for seed in (0, 30, 40):
+        if seed:
+            sx.copy_(_bf16(T, d, seed=seed))
+            sr.copy_(_bf16(T, d, seed=seed + 1))
+        g.replay()
+        torch.cuda.synchronize()
+        h, y = step(sx, sr)  # eager work between the replays
+        torch.cuda.synchronize()
+        assert torch.equal(gh, h) and torch.equal(gy, y)
+    # against the oracle: routing from the library's bf16 y, everything behind it in float64
+    hh, yy, q, qs = moe.rmsnorm(sx, nw, sr, 1e-6, moe.DTYPE_INT8)
+    ids, w = moe.route(yy.float() @ router, k)
+    qn, qsn, idn, wn = f64(q), f64(qs), ids.cpu().numpy(), f64(w)
+    o = np.zeros((T, d))
+    room = np.zeros((T, d))
+    for e in range(E):
+        for j in range(k):
+            r = np.nonzero(idn[:, j] == e)[0]
+            if len(r):
+                v, sl = R.expert_i8(qn[r], qsn[r], W.get(e))
+                o[r] += wn[r, j, None] * v
+                room[r] += wn[r, j, None] * (sl + np.abs(v) * 2.0 ** -7)
+    want = f64(hh) + o
+    assert (np.abs(f64(gh) - want) <= 1.01 * room + (np.abs(o) + np.abs(want)) * 2.0 ** -8).all()

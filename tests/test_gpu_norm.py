@@ -1,0 +1,217 @@
+"""GPU: RMS norm with its 8-bit outputs, and its gradient, against float64.
+
+Tolerances count roundings.  u = 2^-24.  The sum of squares: eight fp32 FMAs of positive terms, then
+fp64 (8 u), halved by the root; mean, eps, root, quotient and the two products: 6 u more; so y before
+its output rounding is within 12 u < 2^-20 of the exact value.  bf16 adds 2^-8, e4m3 2^-4 (2^-10 of the
+scale below its normal range), int8 half a scale."""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_top_amd import moe as _moe
+from oracle import fp8_e4m3
+from oracle import rows as R
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+Y = 2.0 ** -20
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    _moe.lib()
+    return _moe
+
+
+def _bf16(*shape, seed=0, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(torch.bfloat16).cuda()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def values(moe, act, q, qs, d):
+    """(codes' values times scales, scales spread over the columns) as float64."""
+    if act == moe.DTYPE_INT8:
+        s = np.repeat(f64(qs)[:, None], d, 1)
+        return f64(q) * s, s
+    code = fp8_e4m3.decode(q.cpu().numpy()).astype(np.float64)
+    if act == moe.DTYPE_FP8:
+        s = np.repeat(f64(qs), 128, 1)
+    else:
+        s = np.repeat(np.exp2(qs.cpu().numpy().astype(np.float64) - 127), 32, 1)
+    return code * s, s
+
+
+ACTS = {"bf16": 0, "fp8": 1, "mxfp8": 3, "int8": 4}
+SHAPES = [(1, 128), (3, 128), (1, 7168), (5, 512), (77, 4096), (130, 640), (2, 4224), (9, 8192), (3, 12288),
+          (2, 32768)]
+
+
+def check_forward(moe, act, x, w, res, h, y, q, qs):
+    d = x.shape[1]
+    want_h = x if res is None else (x.float() + res.float()).to(torch.bfloat16)
+    assert torch.equal(h.view(torch.int16), want_h.view(torch.int16))
+    ref = R.rmsnorm(f64(want_h), f64(w), EPS)
+    if y is not None:
+        assert (np.abs(f64(y) - ref) <= np.abs(ref) * (2.0 ** -8 + Y)).all()
+    if act == moe.DTYPE_BF16:
+        assert q is None and qs is None
+        return
+    v, s = values(moe, act, q, qs, d)
+    group = {moe.DTYPE_FP8: 128, moe.DTYPE_MXFP4_A8: 32, moe.DTYPE_INT8: d}[act]
+    amax = np.repeat(np.abs(ref).reshape(-1, d // group, group).max(-1), group, 1)
+    if act == moe.DTYPE_INT8:
+        assert (np.abs(s - amax / 127) <= amax / 127 * 2 * Y).all()
+        tol = s / 2 + np.abs(ref) * 2 * Y
+    else:
+        if act == moe.DTYPE_FP8:
+            assert (np.abs(s - amax / 448) <= amax / 448 * 2 * Y).all()
+        else:  # the smallest power of two that holds amax
+            assert (amax <= 448 * s * (1 + Y)).all() and (amax > 224 * s * (1 - Y)).all()
+        tol = np.maximum(np.abs(ref) * 2.0 ** -4, s * 2.0 ** -10) + np.abs(ref) * 2 * Y
+    assert (np.abs(v - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("T,d", SHAPES)
+@pytest.mark.parametrize("fmt", ACTS)
+def test_rmsnorm(moe, fmt, T, d):
+    act = ACTS[fmt]
+    x, w = _bf16(T, d, seed=T + d), _bf16(d, seed=d)
+    res = _bf16(T, d, seed=T + d + 1, std=3.0) if (T + d // 128) % 2 else None
+    h, y, q, qs = moe.rmsnorm(x, w, res, EPS, act)
+    check_forward(moe, act, x, w, res, h, y, q, qs)
+    assert h is x if res is None else h is not x
+    if fmt != "bf16":
+        assert moe.rmsnorm(x, w, res, EPS, act, want_y=False)[1] is None
+
+
+@pytest.mark.parametrize("fmt,d", [("bf16", 8), ("bf16", 200), ("bf16", 4104), ("mxfp8", 32), ("mxfp8", 4128),
+                                   ("int8", 16), ("int8", 4112)])
+def test_rmsnorm_odd_rows(moe, fmt, d):
+    """Rows that end inside a wavefront, of the fewest channels each format takes."""
+    x, w, res = _bf16(7, d, seed=d), _bf16(d, seed=1), _bf16(7, d, seed=2)
+    check_forward(moe, ACTS[fmt], x, w, res, *moe.rmsnorm(x, w, res, EPS, ACTS[fmt]))
+
+
+def test_rmsnorm_int16_bits_and_zero_tokens(moe):
+    x, w = _bf16(4, 256, seed=1), _bf16(256, seed=2)
+    h, y, _, _ = moe.rmsnorm(x.view(torch.int16), w.view(torch.int16))
+    assert y.dtype == torch.int16 and torch.equal(y, moe.rmsnorm(x, w)[1].view(torch.int16))
+    h, y, q, qs = moe.rmsnorm(x[:0], w, x[:0], EPS, moe.DTYPE_INT8)
+    assert h.shape == y.shape == q.shape == (0, 256) and qs.shape == (0,)
+    dx, dw = moe.rmsnorm_grad(x[:0], x[:0], w)
+    assert dx.shape == (0, 256) and torch.equal(dw, torch.zeros_like(dw))
+
+
+def test_rmsnorm_in_place_and_neighbours(moe):
+    """h_out may be the residual itself; rows behind the last one stay as they were."""
+    T, d = 5, 4224
+    x, res, w = _bf16(T + 2, d, seed=1), _bf16(T + 2, d, seed=2), _bf16(d, seed=3)
+    want = (x.float() + res.float()).to(torch.bfloat16)
+    for inplace in ("residual", "x"):
+        a, b = x.clone(), res.clone()
+        out = b if inplace == "residual" else a
+        keep = out[T:].clone()
+        y = torch.full_like(x, 7.0)
+        q = torch.full((T + 2, d), 77, dtype=torch.uint8, device="cuda")
+        qs = torch.full((T + 2, d // 128), 7.0, device="cuda")
+        st = torch.cuda.current_stream().cuda_stream
+        assert moe.lib().moe_rmsnorm(a.data_ptr(), b.data_ptr(), w.data_ptr(), EPS, T, d, moe.DTYPE_FP8,
+                                     out.data_ptr(), y.data_ptr(), q.data_ptr(), qs.data_ptr(), st) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(out[:T], want[:T]) and torch.equal(out[T:], keep)
+        assert (y[T:] == 7).all() and (q[T:] == 77).all() and (qs[T:] == 7).all()
+        check_forward(moe, moe.DTYPE_FP8, x[:T], w, res[:T], out[:T], y[:T], q[:T], qs[:T])
+
+
+@pytest.mark.parametrize("fmt", ACTS)
+def test_rmsnorm_zero_and_non_finite_rows(moe, fmt):
+    """A zero row is zero with scale 1; an infinity or NaN makes its own row NaN and no other."""
+    act, T, d = ACTS[fmt], 6, 384
+    x, w = _bf16(T, d, seed=9), _bf16(d, seed=3)
+    clean = moe.rmsnorm(x, w, None, EPS, act)
+    bad = x.clone()
+    bad[1] = 0
+    bad[2, 5], bad[3, 383], bad[4, 0] = float("inf"), float("nan"), float("-inf")
+    h, y, q, qs = moe.rmsnorm(bad, w, None, EPS, act)
+    assert torch.equal(y[[0, 5]], clean[1][[0, 5]])
+    assert (y[1] == 0).all() and y[2:5].isnan().all()
+    if act == moe.DTYPE_BF16:
+        return
+    v, s = values(moe, act, q, qs, d)
+    vc, _ = values(moe, act, clean[2], clean[3], d)
+    assert (v[[0, 5]] == vc[[0, 5]]).all() and (v[1] == 0).all() and (s[1] == 1).all()
+    assert np.isnan(v[2:5]).all()
+
+
+def test_rmsnorm_small_and_large_values(moe):
+    """Rows far below and above one: eps leads, or the squares stay inside fp32."""
+    d = 512
+    x, w = _bf16(4, d, seed=4), _bf16(d, seed=5)
+    for scale in (1e-20, 1e-4, 1e4, 1e17):
+        xs = (x.float() * scale).to(torch.bfloat16)
+        for act in ACTS.values():
+            check_forward(moe, act, xs, w, None, *moe.rmsnorm(xs, w, None, EPS, act))
+
+
+def check_grad(dy, h, w, dh, dx, dw):
+    """dx: bf16's 2^-8, and 2^-20 of each term that is added (mean(g n) by its terms' magnitudes).
+    dw: fp32 sums over T / 512 rows, 16 and 32 partials, each product rounded a few times."""
+    T, d = dy.shape
+    dy64, h64, w64 = f64(dy), f64(h), f64(w)
+    ref, refw = R.rmsnorm_grad(dy64, h64, w64, EPS)
+    r = 1 / np.sqrt((h64 ** 2).mean(-1, keepdims=True) + EPS)
+    g, n = dy64 * w64, h64 * r
+    add = 0 if dh is None else f64(dh)
+    terms = r * (np.abs(g) + np.abs(n) * np.abs(g * n).mean(-1, keepdims=True)) + np.abs(add)
+    ref = ref + add
+    assert (np.abs(f64(dx) - ref) <= np.abs(ref) * 2.0 ** -8 + terms * 2 * Y).all()
+    if dw is not None:
+        depth = -(-T // 512) + 16 + 32 + 14
+        assert (np.abs(f64(dw) - refw) <= depth * 2.0 ** -24 * np.abs(dy64 * n).sum(0)).all()
+
+
+@pytest.mark.parametrize("T,d", [(1, 8), (1, 7168), (3, 128), (5, 520), (77, 1024), (200, 4104), (600, 256),
+                                 (1030, 2048), (33, 8192), (7, 12288), (3, 16384)])
+def test_rmsnorm_grad(moe, T, d):
+    h, dy, w = _bf16(T, d, seed=T, std=2.0), _bf16(T, d, seed=T + 1, std=0.1), _bf16(d, seed=d)
+    for dh in (None, _bf16(T, d, seed=3, std=0.1)):
+        dx, dw = moe.rmsnorm_grad(dy, h, w, dh, EPS)
+        check_grad(dy, h, w, dh, dx, dw)
+        again, dw2 = moe.rmsnorm_grad(dy, h, w, dh, EPS)
+        assert torch.equal(dx, again) and torch.equal(dw, dw2)  # fixed order
+    dx2, none = moe.rmsnorm_grad(dy, h, w, dh, EPS, want_dweight=False)
+    assert none is None and torch.equal(dx, dx2)
+
+
+def test_rmsnorm_grad_in_place(moe):
+    T, d = 6, 4104
+    h, dy, w, dh = _bf16(T, d, seed=1), _bf16(T, d, seed=2), _bf16(d, seed=3), _bf16(T, d, seed=4)
+    want, _ = moe.rmsnorm_grad(dy, h, w, dh, EPS)
+    for which in ("dy", "dh"):
+        a, b = dy.clone(), dh.clone()
+        out = a if which == "dy" else b
+        st = torch.cuda.current_stream().cuda_stream
+        assert moe.lib().moe_rmsnorm_grad(a.data_ptr(), b.data_ptr(), h.data_ptr(), w.data_ptr(), EPS, T, d,
+                                          out.data_ptr(), None, None, 0, st) == 0
+        assert torch.equal(out, want)
+
+
+def test_rmsnorm_grad_against_differences(moe):
+    """The kernel's dx and dw against central differences of the float64 norm, along one direction:
+    the gradients' bf16 and fp32 errors, summed with the direction's magnitudes, bound the gap."""
+    T, d = 3, 256
+    h, dy, w = _bf16(T, d, seed=1), _bf16(T, d, seed=2), _bf16(d, seed=3)
+    dx, dw = moe.rmsnorm_grad(dy, h, w, None, EPS)
+    v, vw = f64(_bf16(T, d, seed=4)), f64(_bf16(d, seed=5))
+    f = lambda a, b: (f64(dy) * R.rmsnorm(a, b, EPS)).sum()  # noqa: E731
+    e = 1e-5
+    num = (f(f64(h) + e * v, f64(w)) - f(f64(h) - e * v, f64(w))) / (2 * e)
+    assert abs(num - (f64(dx) * v).sum()) <= (np.abs(f64(dx) * v)).sum() * 2.0 ** -8 + 1e-6
+    num = (f(f64(h), f64(w) + e * vw) - f(f64(h), f64(w) - e * vw)) / (2 * e)
+    assert abs(num - (f64(dw) * vw).sum()) <= (np.abs(f64(dw) * vw)).sum() * 2.0 ** -18 + 1e-6
