@@ -72,6 +72,14 @@ __device__ __forceinline__ int frag_lane_off(int kk) {
   const int lane = threadIdx.x & 63, l32 = lane & 31;
   return l32 * ROWB64 + (((kk * 2 + (lane >> 5)) ^ ((l32 >> 1) & 7)) << 4);
 }
+// The same for weights in the tiled layout, whose LDS bytes keep it: per 16-row block 2 KB ordered
+// [half][lane group][row][16 bytes], chunk c of a row being half c & 1 of lane group c >> 1.  A read of
+// chunks 2 kk (lanes 0..31) and 2 kk + 1 (lanes 32..63) of 32 rows is four runs of 256 bytes, free of
+// bank conflicts without a swizzle.
+__device__ __forceinline__ int frag_lane_off_tiled(int kk) {
+  const int lane = threadIdx.x & 63;
+  return ((lane >> 4) & 1) * 2048 + (lane >> 5) * 1024 + kk * 256 + (lane & 15) * 16;
+}
 // byte offset of weight block a of a full tile (gate/up: gate blocks 0, 1 then up blocks 2, 3)
 template <bool GU>
 __device__ __forceinline__ constexpr int full_a_blk(int a) {
@@ -132,14 +140,17 @@ struct MfmaTile {
       // weight slot are never issued)
       int wr = GU ? n0 + ((r - bm) & 127) : n0 + (r - bm);
       wr = wr < sg.N ? wr : sg.N - 1;
-      const uint32_t woff =
-          EL::kTiledW
-              // tiled weights: per 16-row block and 128-byte chunk of K, 2 KB ordered
-              // [half][lane group][row][16 bytes]; bytes [16 c, +16) of the chunk are half c & 1 of
-              // lane group c >> 1
-              ? (uint32_t)(wr >> 4) * 16 * rowbytes + (uint32_t)kt0 * (16 * ROWB64) +
-                    (uint32_t)(((c & 1) * 4 + (c >> 1)) * 256 + (wr & 15) * 16)
-              : (uint32_t)wr * rowbytes + c * 16 + (uint32_t)kt0 * ROWB64;
+      uint32_t woff = (uint32_t)wr * rowbytes + c * 16 + (uint32_t)kt0 * ROWB64;
+      if (EL::kTiledW) {
+        // tiled weights: the slot is one contiguous kilobyte, half wvu & 1 of the 16-row block of LDS
+        // rows 32 j + 16 (wvu >> 1) (with a lane's 16 bytes of every row in the swizzled order instead,
+        // each load touched a quarter of 32 lines: the int8 gate/up GEMM of an 8-expert prefill
+        // layer took 1.12 ms against 0.XX)
+        const int br = 32 * j + 16 * (wvu >> 1) - bm;
+        int blk = (GU ? n0 + (br & 127) : n0 + br) >> 4;
+        blk = blk < (sg.N >> 4) ? blk : (sg.N >> 4) - 1;
+        woff = (uint32_t)blk * 16 * rowbytes + (uint32_t)kt0 * (16 * ROWB64) + (wvu & 1) * 1024 + lane * 16;
+      }
       if (j < 8) {
         const int rr = 32 * j + 8 * wvu + (lane >> 3);
         const uint32_t toff =
@@ -158,6 +169,11 @@ struct MfmaTile {
       arow0 = (bm + (GU ? wn * 32 : wn * 64)) * ROWB64;
       brow0 = 0;
     }
+  }
+
+  // A lane's offset in a weight block for k-substep kk.
+  static __device__ __forceinline__ int wfrag_off(int kk) {
+    return EL::kTiledW ? frag_lane_off_tiled(kk) : frag_lane_off(kk);
   }
 
   // Byte advance of the weights for a K-step whose rows advance by ko bytes (tiled: 2 KB units).
@@ -186,7 +202,7 @@ struct MfmaTile {
   template <int S>
   __device__ __forceinline__ void read_frags(int kk, Frag (&f)[8]) const {
     const uint8_t* st = stage64_ptr<S>();
-    const int lo = frag_lane_off(kk), va = arow0 + lo, vb = brow0 + lo;
+    const int va = arow0 + wfrag_off(kk), vb = brow0 + frag_lane_off(kk);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = frag_full(st, va, vb, i);
   }
@@ -220,7 +236,7 @@ struct MfmaTile {
   template <int S, int T, int J0, int N>
   __device__ __forceinline__ void sub_dma(int kk, const Frag (&cur)[8], Frag (&nxt)[8], uint32_t ko) {
     const uint8_t* st = stage64_ptr<S>();
-    const int lo = frag_lane_off(kk), va = arow0 + lo, vb = brow0 + lo;
+    const int va = arow0 + wfrag_off(kk), vb = brow0 + frag_lane_off(kk);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       __builtin_amdgcn_sched_barrier(0);
@@ -253,7 +269,7 @@ struct MfmaTile {
     // MFMAs of substep 3
     const uint32_t ko = (uint32_t)min(kt + 2, nk - 1) * ROWB64;
     const uint8_t* rd = stage64_ptr<S ^ 1>();
-    const int lo = frag_lane_off(0), va = arow0 + lo, vb = brow0 + lo;
+    const int va = arow0 + wfrag_off(0), vb = brow0 + frag_lane_off(0);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       __builtin_amdgcn_sched_barrier(0);
@@ -322,7 +338,7 @@ struct MfmaTile {
 
   template <int TB>
   __device__ __forceinline__ void read_frags_short(const uint8_t* st, int kk, Frag (&f)[2 + TB]) const {
-    const int lo = frag_lane_off(kk), va = arow0 + lo, vb = brow0 + lo;
+    const int va = arow0 + wfrag_off(kk), vb = brow0 + frag_lane_off(kk);
 #pragma unroll
     for (int i = 0; i < 2 + TB; ++i) f[i] = frag_short<TB>(st, va, vb, i);
   }
@@ -387,7 +403,7 @@ struct MfmaTile {
       const uint32_t ko = (uint32_t)min(kt + NS, nk - 1) * ROWB64;
       const int sn = s == NS - 1 ? 0 : s + 1;
       const uint8_t* rd = g_ring + sn * kStage;
-      const int lo = frag_lane_off(0), va = arow0 + lo, vb = brow0 + lo;
+      const int va = arow0 + wfrag_off(0), vb = brow0 + frag_lane_off(0);
 #pragma unroll
       for (int i = 0; i < D; ++i) {
         __builtin_amdgcn_sched_barrier(0);
