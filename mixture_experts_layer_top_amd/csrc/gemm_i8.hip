@@ -236,35 +236,44 @@ __device__ __forceinline__ void i8_store(const i32x16 (&acc)[4][4], const I8Cur&
   constexpr int NB = kFull ? 4 : TB;           // token blocks of this wavefront
   constexpr int NA = GU ? (kFull ? 2 : 1) : (kFull ? 4 : 2);  // its 32-column output blocks
   const int cw = wn * 32 * NA;                 // its first output column
+  const int t0 = (kFull ? wm * 128 : 0) + l32;  // its token rows: t0 + 32 b
+  float sx[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    const int t = (kFull ? wm * 128 : 0) + b * 32 + l32;
-    const int gr = c.row0 + c.m0 + min(t, c.rows - 1);
-    const float sx = gload_f32(c.as, c.tok ? gload_i32(c.tok, gr) : gr);
+    const int gr = c.row0 + c.m0 + min(t0 + 32 * b, c.rows - 1);
+    sx[b] = gload_f32(c.as, c.tok ? gload_i32(c.tok, gr) : gr);
+  }
 #pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      // (one block's scale loads at a time: all of them together would not fit beside the
-      // accumulators)
-      if (kFull) __builtin_amdgcn_sched_barrier(0);
+  for (int a = 0; a < NA; ++a) {
+    // (one block's scales at a time: all of them together would not fit beside the accumulators)
+    __builtin_amdgcn_sched_barrier(0);
+    // lane holds C[8 q + 4 khalf + s][l32] of each 32x32 block (rows = weights)
+    const int col = cw + a * 32 + 4 * khalf;
+    float4 w0[4], w1[GU ? 4 : 1];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = min(c.n0 + col + 8 * q, c.N - 4);  // (columns past N are not stored)
+      w0[q] = gload_f32x4(c.s0, n);
+      if (GU) w1[GU ? q : 0] = gload_f32x4(c.s1, n);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      uint8_t* row = g_ring + (t0 + 32 * b) * RS;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        // lane holds C[8 q + 4 khalf + s][l32] of each 32x32 block (rows = weights)
-        const int col = cw + a * 32 + 8 * q + 4 * khalf;
-        const int n = min(c.n0 + col, c.N - 4);  // (columns past N are not stored)
-        const float4 s0 = gload_f32x4(c.s0, n);
-        const float w0[4] = {s0.x, s0.y, s0.z, s0.w};
+        const float s0[4] = {w0[q].x, w0[q].y, w0[q].z, w0[q].w};
         float v[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) v[s] = float(acc[a][b][q * 4 + s]) * sx * w0[s];
+        for (int s = 0; s < 4; ++s) v[s] = float(acc[a][b][q * 4 + s]) * sx[b] * s0[s];
         if (GU) {
-          const float4 s1 = gload_f32x4(c.s1, n);
-          const float w1[4] = {s1.x, s1.y, s1.z, s1.w};
+          const float4 u = w1[GU ? q : 0];
+          const float s1[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            v[s] = swiglu(v[s], float(acc[a + NA][b][q * 4 + s]) * sx * w1[s]);
-          *reinterpret_cast<float4*>(g_ring + t * RS + col * 4) = float4{v[0], v[1], v[2], v[3]};
+            v[s] = swiglu(v[s], float(acc[a + NA][b][q * 4 + s]) * sx[b] * s1[s]);
+          *reinterpret_cast<float4*>(row + (col + 8 * q) * 4) = float4{v[0], v[1], v[2], v[3]};
         } else {
-          *reinterpret_cast<uint2*>(g_ring + t * RS + col * 2) =
+          *reinterpret_cast<uint2*>(row + (col + 8 * q) * 2) =
               uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
         }
       }
@@ -328,6 +337,8 @@ __global__ __launch_bounds__(256, 1) void gemm_mfma_i8(const Seg* __restrict__ s
   const int ntiles = meta[1];
   if (ntiles == 0) return;
   const int nseg = meta[0], ntiles0 = meta[kMetaClass0], order = meta[kMetaOrder];
+  // positions [0, sbase) are whole tiles, then come 2^lgs pieces of 256 >> lgs token rows of each tile
+  const int sbase = meta[kMetaSplitBase], S = meta[kMetaSplitS], lgs = S == 4 ? 2 : S == 2 ? 1 : 0;
   int pref, b0, b1;
   two_class_split((int)gridDim.x, ntiles0, ntiles - ntiles0, pref, b0, b1);
   b0 = __builtin_amdgcn_readfirstlane(b0);
@@ -342,20 +353,27 @@ __global__ __launch_bounds__(256, 1) void gemm_mfma_i8(const Seg* __restrict__ s
     // (opaque moves: the reciprocals of the queue's divisions are computed here, not held across
     // the K loops)
     const int nt_ = opaque_s(ntiles), nt0_ = opaque_s(ntiles0), ch_ = opaque_s(chunk);
-    int t;
-    if (order == kOrderTwoClass) {
+    int t, piece = 0, hrows = BM;
+    if (order == kOrderTwoClass) {  // (never split)
       t = pop_tile_two_class(meta + kMetaQueue, meta + kMetaQueue1, nt0_, nt_ - nt0_, opaque_s(b0),
                              opaque_s(b1), pref, &slot, q);
       if (t < 0) return;
     } else {
-      const int pos = pop_tile_xcd(meta + kMetaQueue, nt_, ch_, &slot, q);
+      const int sb_ = opaque_s(sbase);
+      int pos = pop_tile_xcd(meta + kMetaQueue, sb_ + ((nt_ - sb_) << lgs), ch_, &slot, q);
       if (pos < 0) return;
+      if (pos >= sb_) {
+        hrows = BM >> lgs;
+        piece = (pos - sb_) & ((1 << lgs) - 1);
+        pos = sb_ + ((pos - sb_) >> lgs);
+      }
       t = order == kOrderLongestFirst ? pos : interleave_tile(pos, nt0_, nt_);
     }
     const Seg& sg = segs[__builtin_amdgcn_readfirstlane(find_seg_lds(seg_base, nseg, t))];
     const int local = t - sg.tile_base;
-    const int m0 = local % sg.mtiles * BM;
-    const I8Cur c = i8_cur<GU>(sg, m0, min(BM, sg.rows - m0), local / sg.mtiles);
+    const int m0 = local % sg.mtiles * BM + piece * hrows;
+    if (m0 >= sg.rows) continue;  // (a piece past the tile's rows)
+    const I8Cur c = i8_cur<GU>(sg, m0, min(hrows, sg.rows - m0), local / sg.mtiles);
     tile.setup(sg, c.m0, c.rows, c.n0, 0);
     const int h = __builtin_amdgcn_readfirstlane(tile.bm);
     tile.prologue(c.nk);
@@ -363,31 +381,53 @@ __global__ __launch_bounds__(256, 1) void gemm_mfma_i8(const Seg* __restrict__ s
   }
 }
 
-// The dense product: one segment, MH token rows per tile; XCD x takes an equal run of consecutive
-// tiles (m-tiles of one weight tile adjacent).
-template <int MH>
-__global__ __launch_bounds__(256, 1) void gemm_mfma_i8_dense(Seg sg) {
+// Tile t of a dense product in an order that keeps 32 consecutive tiles (one round of an XCD's CUs)
+// near a square: runs of kDenseGM m-tiles per weight tile.
+constexpr int kDenseGM = 8;
+__device__ __forceinline__ void dense_tile(int t, int mtiles, int ntiles, int& mt, int& nt) {
+  const int per = kDenseGM * ntiles, g = t / per, r = t - g * per;
+  const int gm = min(kDenseGM, mtiles - g * kDenseGM);
+  nt = r / gm;
+  mt = g * kDenseGM + r - nt * gm;
+}
+
+// The dense product: whole tiles [0, full), a multiple of the grid, then what is left over as pieces
+// of H = 256 >> lgs token rows, so that the last round is shorter instead of half empty (full = 0: the
+// product has less than a round of whole tiles, and all of it is pieces).  XCD x takes an equal run of
+// the whole tiles and of the pieces.
+__global__ __launch_bounds__(256, 1) void gemm_mfma_i8_dense(Seg sg, int full, int pieces, int lgs) {
   sg.tok = nullptr;
   sg.row0 = 0;
   MfmaTile<false, ElemI8> tile;
-  const int ntiles = sg.mtiles * sg.ntiles, per = (ntiles + kXcds - 1) / kXcds;
-  const int x = blockIdx.x % kXcds;
-  for (int i = blockIdx.x / kXcds; i < per; i += gridDim.x / kXcds) {
-    const int mt_ = opaque_s(sg.mtiles);
-    const int t = x * per + i;
-    if (t >= ntiles) return;
-    const int m0 = t % mt_ * MH;
-    const I8Cur c = i8_cur<false>(sg, m0, min(MH, sg.rows - m0), t / mt_);
-    tile.template setup<MH>(sg, c.m0, c.rows, c.n0, 0);
-    if constexpr (MH == BM) {
-      tile.prologue_full(c.nk);
-      tile.run_full(c.nk);
-      i8_store<false, 8>(tile.acc, c);
+  const int x = blockIdx.x % kXcds, step = gridDim.x / kXcds;
+  const int nfull = full / kXcds, n = nfull + (pieces + kXcds - 1) / kXcds;
+  for (int i = blockIdx.x / kXcds; i < n; i += step) {
+    // (opaque: the decode's reciprocals are computed here, not held across the K loop)
+    const int mt_ = opaque_s(sg.mtiles), nt_ = opaque_s(sg.ntiles), lgs_ = opaque_s(lgs);
+    const int H = BM >> lgs_;
+    int mt, nt, m0, rows;
+    if (i < nfull) {
+      dense_tile(x * nfull + i, mt_, nt_, mt, nt);
+      m0 = mt * BM;
+      rows = min(BM, sg.rows - m0);
     } else {
-      tile.template prologue_short<MH / 32>(c.nk);
-      tile.template run_short<MH / 32>(c.nk);
-      i8_store<false, MH / 32>(tile.acc, c);
+      const int q = x * (n - nfull) + i - nfull;
+      if (q >= pieces) return;
+      if (full) {
+        dense_tile(full + (q >> lgs_), mt_, nt_, mt, nt);
+        m0 = mt * BM + (q & ((1 << lgs_) - 1)) * H;
+        if (m0 >= sg.rows) continue;  // (an m-tile of fewer rows)
+      } else {
+        dense_tile(q, (sg.rows + H - 1) >> (8 - lgs_), nt_, mt, nt);
+        m0 = mt * H;
+      }
+      rows = min(H, sg.rows - m0);
     }
+    const I8Cur c = i8_cur<false>(sg, m0, rows, nt);
+    tile.setup(sg, c.m0, c.rows, c.n0, 0);
+    const int h = __builtin_amdgcn_readfirstlane(tile.bm);
+    tile.prologue(c.nk);
+    i8_run<false>(tile, h, c);
     __syncthreads();  // (the ring's rows are stored before the next tile's loads overwrite them)
   }
 }
@@ -439,16 +479,20 @@ hipError_t launch_gemm_i8(const void* xq, const float* xs, int M, const void* wq
     else gemm_stream_i8_dense<4><<<sg.ntiles, 256, 0, s>>>(sg);
     return hipGetLastError();
   }
-  // the tallest tile that still gives every CU one
-  sg.ntiles = (N + kMfmaBNDown - 1) / kMfmaBNDown;
-  int mh = 256;
-  while (mh > 32 && (int64_t)((M + mh - 1) / mh) * sg.ntiles < num_cus) mh /= 2;
-  sg.mtiles = (M + mh - 1) / mh;
   const int g = std::max(kXcds, num_cus / kXcds * kXcds);
-  if (mh == 256) gemm_mfma_i8_dense<256><<<g, 256, 0, s>>>(sg);
-  else if (mh == 128) gemm_mfma_i8_dense<128><<<g, 256, 0, s>>>(sg);
-  else if (mh == 64) gemm_mfma_i8_dense<64><<<g, 256, 0, s>>>(sg);
-  else gemm_mfma_i8_dense<32><<<g, 256, 0, s>>>(sg);
+  sg.ntiles = (N + kMfmaBNDown - 1) / kMfmaBNDown;
+  sg.mtiles = (M + BM - 1) / BM;
+  const int64_t tiles = (int64_t)sg.mtiles * sg.ntiles;
+  const int full = (int)(tiles / g * g);
+  int lgs = 0, pieces;
+  if (full) {
+    while (lgs < 3 && (tiles - full) * (2 << lgs) <= g) ++lgs;
+    pieces = (int)(tiles - full) << lgs;
+  } else {  // the tallest tile that gives every CU one
+    while (lgs < 3 && ((M + (BM >> lgs) - 1) / (BM >> lgs)) * (int64_t)sg.ntiles < g) ++lgs;
+    pieces = (M + (BM >> lgs) - 1) / (BM >> lgs) * sg.ntiles;
+  }
+  gemm_mfma_i8_dense<<<g, 256, 0, s>>>(sg, full, pieces, lgs);
   return hipGetLastError();
 }
 

@@ -96,6 +96,13 @@ struct MfmaTile {
   const char* wbase0;
   const char* wbase1;
   uint32_t off[DMA64];
+  // Tiled weights: a slot is one contiguous kilobyte, half wvu & 1 of a 16-row block.  Slot i's block is
+  // wblk0 + 2 i (gate/up: i mod 4, of the gate or the up rows), past N the last one: uniform, so one lane
+  // offset serves every slot.  (With a lane's 16 bytes of every row in the swizzled order instead, each
+  // load touched a quarter of 32 lines: the gate/up GEMM of an 8-expert prefill layer 1.12 ms against
+  // 0.96.)
+  int wblk0, wlast;
+  uint32_t wbytes, wlane;
   int wvu;
   int bm;  // tile height: 256, 128, 64 or 32 token rows
   int arow0, brow0;  // LDS byte offsets of the wavefront's first weight and token rows
@@ -140,17 +147,7 @@ struct MfmaTile {
       // weight slot are never issued)
       int wr = GU ? n0 + ((r - bm) & 127) : n0 + (r - bm);
       wr = wr < sg.N ? wr : sg.N - 1;
-      uint32_t woff = (uint32_t)wr * rowbytes + c * 16 + (uint32_t)kt0 * ROWB64;
-      if (EL::kTiledW) {
-        // tiled weights: the slot is one contiguous kilobyte, half wvu & 1 of the 16-row block of LDS
-        // rows 32 j + 16 (wvu >> 1) (with a lane's 16 bytes of every row in the swizzled order instead,
-        // each load touched a quarter of 32 lines: the int8 gate/up GEMM of an 8-expert prefill
-        // layer took 1.12 ms against 0.XX)
-        const int br = 32 * j + 16 * (wvu >> 1) - bm;
-        int blk = (GU ? n0 + (br & 127) : n0 + br) >> 4;
-        blk = blk < (sg.N >> 4) ? blk : (sg.N >> 4) - 1;
-        woff = (uint32_t)blk * 16 * rowbytes + (uint32_t)kt0 * (16 * ROWB64) + (wvu & 1) * 1024 + lane * 16;
-      }
+      const uint32_t woff = (uint32_t)wr * rowbytes + c * 16 + (uint32_t)kt0 * ROWB64;
       if (j < 8) {
         const int rr = 32 * j + 8 * wvu + (lane >> 3);
         const uint32_t toff =
@@ -159,6 +156,12 @@ struct MfmaTile {
       } else {
         off[j] = woff;
       }
+    }
+    if (EL::kTiledW) {
+      wblk0 = (n0 >> 4) + (wvu >> 1);
+      wlast = (sg.N >> 4) - 1;
+      wbytes = 16 * rowbytes;
+      wlane = (wvu & 1) * 1024 + lane * 16 + (uint32_t)kt0 * (16 * ROWB64);
     }
     if (bm == BM) {
       const int wm = wvu & 1, wn = wvu >> 1;
@@ -176,15 +179,25 @@ struct MfmaTile {
     return EL::kTiledW ? frag_lane_off_tiled(kk) : frag_lane_off(kk);
   }
 
-  // Byte advance of the weights for a K-step whose rows advance by ko bytes (tiled: 2 KB units).
-  static __device__ __forceinline__ uint32_t wko(uint32_t ko) { return EL::kTiledW ? 16 * ko : ko; }
+  // Load slot j of a tile of NTS token slots at byte ko of every row, into dst.
+  template <int NTS, bool NT>
+  __device__ __forceinline__ void load_slot(int j, uint32_t ko, uint8_t* dst) {
+    if (EL::kTiledW && j >= NTS) {
+      const int i = GU ? (j - NTS) & 3 : j - NTS;
+      const uint32_t blk = (uint32_t)min(wblk0 + 2 * i, wlast);
+      // (16 * ko: a K-step is a 2 KB unit of every 16-row block)
+      dma16<NT>(slot_base<NTS>(j) + (size_t)(blk * wbytes) + 16 * ko, wlane, (lds_void*)dst);
+    } else {
+      dma16<NT>(slot_base<NTS>(j) + ko, off[j], (lds_void*)dst);
+    }
+  }
 
   // ---- full tiles ----
   template <int S>
   __device__ __forceinline__ void issue_one(int j, uint32_t ko) {
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint8_t* st = stage64_ptr<S>() + wv * 8 * ROWB64;
-    dma16(slot_base<8>(j) + (j < 8 ? ko : wko(ko)), off[j], (lds_void*)(st + j * 32 * ROWB64));
+    load_slot<8, false>(j, ko, st + j * 32 * ROWB64);
   }
 
   template <int S>
@@ -318,8 +331,8 @@ struct MfmaTile {
     // full-height neighbours share (DeepSeek-V3-shaped decode at T = 64 and 256: gate/up -9%).
     // Not the down weights: there the mixed order keeps an expert's short last m-tile next to
     // its full-height siblings, which read the same weight rows (Kimi-K2-shaped down GEMM +7%).
-    if (GU && j >= TB) dma16<true>(slot_base<TB>(j) + wko(ko), off[j], (lds_void*)(st + j * 32 * ROWB64));
-    else dma16(slot_base<TB>(j) + (j < TB ? ko : wko(ko)), off[j], (lds_void*)(st + j * 32 * ROWB64));
+    if (GU && j >= TB) load_slot<TB, true>(j, ko, st + j * 32 * ROWB64);
+    else load_slot<TB, false>(j, ko, st + j * 32 * ROWB64);
   }
 
   template <int TB>

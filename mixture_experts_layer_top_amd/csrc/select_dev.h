@@ -323,7 +323,7 @@ __device__ __forceinline__ void select_block(const SelectArgs& a, const SelectOu
     const int K = g == kGemmGateUp ? a.d : a.f;
     const bool uniform_k = g == kGemmGateUp || !a.has_shared || a.f_sh == a.f;
     const int C = min(a.num_cus, kSplitMaxPieces);
-    const bool mfma_bf16 = e % kNumFam == kFamMfma && !a.fp8 && !a.w4;
+    const bool mfma_bf16 = e % kNumFam == kFamMfma && !a.fp8 && !a.w4;  // (and int8)
     // (lpt[] is the same for every thread)
     m[kMetaOrder] = !mfma_bf16 ? kOrderMix : lpt[g] ? kOrderLongestFirst : two[g] ? kOrderTwoClass
                                                                                   : kOrderMix;
@@ -334,6 +334,13 @@ __device__ __forceinline__ void select_block(const SelectArgs& a, const SelectOu
         if (rem * 4 <= C && nk % 8 == 0) S = 4;
         else if (rem * 2 <= C && nk % 4 == 0) S = 2;
       }
+      if (S > 1) base = ntl - rem;
+    }
+    // int8 lists split the tiles past the last whole round by token rows instead (pieces of 256 / S
+    // rows: no partial sums), in any one-queue order.
+    if (mfma_bf16 && a.i8 && m[kMetaOrder] != kOrderTwoClass) {
+      const int rem = ntl % C;
+      if (rem > 0) S = rem * 4 <= C ? 4 : rem * 2 <= C ? 2 : 1;
       if (S > 1) base = ntl - rem;
     }
     m[kMetaSplitBase] = base;
