@@ -104,7 +104,7 @@ hipError_t launch_combine_grad(const void* dout, const void* y, const int32_t* s
                                const float* w, int T, int k, int d, void* dy, float* dw,
                                hipStream_t s) {
   if (T == 0) return hipSuccess;
-  with_row_shape(d / 8, [&](auto Rc, auto Vc) {
+  with_row_shape(d / 8, T <= kFewRows, [&](auto Rc, auto Vc) {
     constexpr int R = decltype(Rc)::value, V = decltype(Vc)::value;
     const unsigned grid = R == 64 ? ((unsigned)T + 3) / 4 : (unsigned)T;
     combine_grad_kernel<R, V><<<grid, row_block(R), 0, s>>>(dout, y, slot_dst, w, T, k, d / 8, dy, dw);

@@ -15,7 +15,6 @@
 // is far above what the memory asks for.
 #include <type_traits>
 
-#include "fp8_codec.h"
 #include "kernels.h"
 #include "mx_codec.h"
 #include "rows_dev.h"
@@ -25,6 +24,14 @@ namespace moe {
 namespace {
 
 enum NormFormat { kNormBf16 = 0, kNormFp8 = 1, kNormMx = 2, kNormI8 = 3 };
+
+// Four e4m3 codes in a dword, by the conversion instruction: to nearest, ties to even, the sign kept.
+// It equals e4m3_encode on every float below 464 in magnitude (all of them compared), and the scaled
+// values here are at most 448 (1 + 2^-22).
+__device__ __forceinline__ uint32_t e4m3_pack4(const float* v) {
+  int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], p, true);
+}
 
 // 1 / sqrt(sum / d + eps); NaN when the sum of squares is not finite (an infinity or NaN in the
 // row), so that the whole row shows it.
@@ -43,13 +50,15 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
   if (R == 64 && row >= T) return;  // (whole wavefronts; no barrier in this form)
   const int i = R == 64 ? threadIdx.x & 63 : threadIdx.x;
   const size_t base = (size_t)row * nvec;
-  uint4 hv[V], rv[V];
+  uint4 hv[V], rv[V], wr[V];
 #pragma unroll
   for (int s = 0; s < V; ++s) hv[s] = ld16(x, base + min(i + R * s, nvec - 1));
   if (res) {
 #pragma unroll
     for (int s = 0; s < V; ++s) rv[s] = ld16(res, base + min(i + R * s, nvec - 1));
   }
+#pragma unroll
+  for (int s = 0; s < V; ++s) wr[s] = ld16(w, min(i + R * s, nvec - 1));
   double sum[1] = {0.0};
 #pragma unroll
   for (int s = 0; s < V; ++s) {
@@ -76,12 +85,13 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
   const float rstd = row_rstd(sum[0], inv_d, eps);
   auto yvec = [&](int s, float (&v)[8]) {
     float wv[8];
-    unpack8(ld16(w, min(i + R * s, nvec - 1)), wv);
+    unpack8(wr[s], wv);
     unpack8(hv[s], v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * wv[j];
   };
-  double inv = 0.0;
+  Scale row_scale(1.0f);
+  bool bad_row = false;
   if (FMT == kNormI8) {
     uint32_t m[1] = {0u};
 #pragma unroll
@@ -95,7 +105,8 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
     }
     row_reduce<R>(m, redm, MaxOp{});
     const float sc = i8_scale(m[0]);
-    inv = m[0] < kInfBits ? 1.0 / (double)sc : 0.0;
+    bad_row = m[0] >= kInfBits;  // (scale NaN, codes 0)
+    row_scale = Scale(bad_row ? 1.0f : sc);
     if (i == 0) static_cast<float*>(qs)[row] = sc;
   }
 #pragma unroll
@@ -113,29 +124,29 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
     if (idx >= nvec) continue;
     if (y) st16(y, base + idx, pack8(v));
     if (FMT == kNormI8) {
-      const bool bad = inv == 0.0;  // (the row's scale is NaN; codes 0)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = bad ? 0.f : v[j];
-      st8(q, (base + idx) * 8, i8_pack4(v, inv), i8_pack4(v + 4, inv));
+      for (int j = 0; j < 8; ++j) v[j] = bad_row ? 0.f : v[j];
+      st8(q, (base + idx) * 8, i8_pack4(v, row_scale), i8_pack4(v + 4, row_scale));
     }
     if (FMT == kNormFp8 || FMT == kNormMx) {
       const bool bad = m >= kInfBits;
-      double f;
       if (FMT == kNormFp8) {
-        float sc = float(double(__uint_as_float(m)) / 448.0);
-        if (sc == 0.0f) sc = 1.0f;
-        if (bad) sc = 1.0f;
-        f = 1.0 / (double)sc;
+        float sc = __uint_as_float(m) / 448.0f;
+        if (sc == 0.0f || bad) sc = 1.0f;
         if ((idx & 15) == 0) static_cast<float*>(qs)[base / 16 + idx / 16] = sc;
+        const Scale f(sc);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = f.div(v[j]);
       } else {
         const int X = bad ? 127 : mx_scale_code(__uint_as_float(m));
-        f = (double)mx_inv_scale(X);
         if ((idx & 3) == 0) gstore_u8(static_cast<uint8_t*>(qs), base / 4 + idx / 4, X);
-      }
-      uint32_t p[2] = {0u, 0u};
+        const float f = mx_inv_scale(X);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        p[j >> 2] |= uint32_t(e4m3_encode(bad ? 0.f : float(double(v[j]) * f))) << (8 * (j & 3));
+        for (int j = 0; j < 8; ++j) v[j] *= f;
+      }
+      uint32_t p[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) p[j] = e4m3_pack4(v + 4 * j);
       if (bad) p[0] = p[1] = 0x7F7F7F7Fu;  // NaN codes
       st8(q, (base + idx) * 8, p[0], p[1]);
     }
@@ -180,7 +191,7 @@ __global__ __launch_bounds__(row_block(R)) void quant_i8_kernel(const void* __re
   row_reduce<R>(m, redm, MaxOp{});
   const float sc = i8_scale(m[0]);
   const bool bad = m[0] >= kInfBits;
-  const double inv = bad ? 0.0 : 1.0 / (double)sc;
+  const Scale f(bad ? 1.0f : sc);
   if (i == 0) qs[row] = sc;
 #pragma unroll
   for (int s = 0; s < V; ++s) {
@@ -189,7 +200,7 @@ __global__ __launch_bounds__(row_block(R)) void quant_i8_kernel(const void* __re
     vec(s, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = bad ? 0.f : v[j];
-    st8(q, (base + i + R * s) * 8, i8_pack4(v, inv), i8_pack4(v + 4, inv));
+    st8(q, (base + i + R * s) * 8, i8_pack4(v, f), i8_pack4(v + 4, f));
   }
 }
 
@@ -290,7 +301,7 @@ hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float e
                           int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s) {
   if (T == 0) return hipSuccess;
   const int nvec = d / 8;
-  with_row_shape(nvec, [&](auto Rc, auto Vc) {
+  with_row_shape(nvec, T <= kFewRows, [&](auto Rc, auto Vc) {
     constexpr int R = decltype(Rc)::value, V = decltype(Vc)::value;
     const unsigned grid = R == 64 ? ((unsigned)T + 3) / 4 : (unsigned)T;
     auto go = [&](auto F) {
@@ -309,7 +320,7 @@ hipError_t launch_quant_i8(const void* x, bool f32, int T, int d, uint8_t* q, fl
                            hipStream_t s) {
   if (T == 0) return hipSuccess;
   const int nvec = d / 8;
-  with_row_shape(nvec, [&](auto Rc, auto Vc) {
+  with_row_shape(nvec, T <= kFewRows, [&](auto Rc, auto Vc) {
     constexpr int R = decltype(Rc)::value, V = decltype(Vc)::value;
     const unsigned grid = R == 64 ? ((unsigned)T + 3) / 4 : (unsigned)T;
     if (f32) quant_i8_kernel<true, R, V><<<grid, row_block(R), 0, s>>>(x, T, nvec, q, qs);

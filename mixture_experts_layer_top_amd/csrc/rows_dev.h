@@ -12,7 +12,9 @@ constexpr int kMaxRow = 32768;
 
 // Threads (R) and steps (V) for a row of nvec 8-value vectors: one wavefront while 8 steps are
 // enough (no barrier), then the fewest wavefronts; V is the row's own step count, so no step is
-// empty.  Calls f with both as integral constants.  nvec <= kMaxRow / 8.
+// empty.  Few rows (`few`: a decode batch leaves most CUs idle) take a wavefront per 64 or 128 vectors
+// instead: a row's latency is then one or two loads deep.  Calls f with both as integral constants.
+// nvec <= kMaxRow / 8.
 template <int R, int V, int VMAX, class F>
 inline void with_steps(int v, F&& f) {
   if constexpr (V < VMAX) {
@@ -21,12 +23,20 @@ inline void with_steps(int v, F&& f) {
   f(std::integral_constant<int, R>{}, std::integral_constant<int, V>{});
 }
 template <class F>
-inline void with_row_shape(int nvec, F&& f) {
+inline void with_row_shape(int nvec, bool few, F&& f) {
+  if (few && nvec > 64) {
+    if (nvec <= 256) with_steps<256, 1, 1>(1, f);
+    else if (nvec <= 512) with_steps<512, 1, 1>(1, f);
+    else if (nvec <= 1024) with_steps<512, 2, 2>(2, f);
+    else if (nvec <= 4096) with_steps<1024, 2, 4>((nvec + 1023) / 1024, f);
+    return;
+  }
   if (nvec <= 64 * 8) with_steps<64, 1, 8>((nvec + 63) / 64, f);
   else if (nvec <= 128 * 8) with_steps<128, 5, 8>((nvec + 127) / 128, f);
   else if (nvec <= 256 * 8) with_steps<256, 5, 8>((nvec + 255) / 256, f);
   else with_steps<512, 5, 8>((nvec + 511) / 512, f);
 }
+constexpr int kFewRows = 512;  // two rows per CU
 
 // Threads per workgroup: four one-wavefront rows, else one row.
 constexpr int row_block(int R) { return R == 64 ? 256 : R; }
@@ -59,28 +69,62 @@ __device__ __forceinline__ void st8(void* base, size_t off, uint32_t a, uint32_t
   gstore8(base, off, uint2{a, b});
 }
 
+// One lane exchange inside rows of 16 lanes (DPP), for values of 4 or 8 bytes.
+template <int CTRL, class T>
+__device__ __forceinline__ T dpp16(T v) {
+  if constexpr (sizeof(T) == 8) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, false);
+    return __builtin_bit_cast(T, ((uint64_t)hi << 32) | lo);
+  } else {
+    return __builtin_bit_cast(
+        T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+  }
+}
+template <class T>
+__device__ __forceinline__ T read_lane(T v, int lane) {
+  if constexpr (sizeof(T) == 8) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(T, ((uint64_t)hi << 32) | lo);
+  } else {
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+  }
+}
+// Over aligned groups of 16 lanes, in every lane: neighbours, pairs, mirrored halves, mirrored rows.
+template <class T, class Op>
+__device__ __forceinline__ T reduce16(T v, Op op) {
+  v = op(v, dpp16<0xb1>(v));   // quad_perm [1,0,3,2]
+  v = op(v, dpp16<0x4e>(v));   // quad_perm [2,3,0,1]
+  v = op(v, dpp16<0x141>(v));  // row_half_mirror
+  return op(v, dpp16<0x140>(v));  // row_mirror
+}
+
 // Sums (or maxima) of NA values over the R threads of a row, the same in every thread and in a
-// fixed order: a butterfly in each wavefront, then the wavefronts' results in order from LDS.
+// fixed order: rows of 16 lanes, the four rows of a wavefront, then the wavefronts through LDS.
 // red: NA * R / 64 values of its own for every call (no barrier protects a second use).
 template <int R, int NA, class T, class Op>
 __device__ __forceinline__ void row_reduce(T (&v)[NA], T* red, Op op) {
 #pragma unroll
-  for (int i = 0; i < NA; ++i)
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v[i] = op(v[i], __shfl_xor(v[i], o));
+  for (int i = 0; i < NA; ++i) {
+    v[i] = reduce16(v[i], op);
+    v[i] = op(op(read_lane(v[i], 0), read_lane(v[i], 16)), op(read_lane(v[i], 32), read_lane(v[i], 48)));
+  }
   if constexpr (R > 64) {
     constexpr int W = R / 64;
-    const int wv = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < NA; ++i) red[i * W + wv] = v[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      v[i] = red[i * W];
-#pragma unroll
-      for (int w = 1; w < W; ++w) v[i] = op(v[i], red[i * W + w]);
+    for (int i = 0; i < NA; ++i) {  // (W <= 16: lane l of each row of 16 takes wavefront l's, or 0)
+      const int l = lane & 15;
+      v[i] = l < W ? red[i * W + l] : T(0);
+      v[i] = read_lane(reduce16(v[i], op), 0);
     }
   }
 }
@@ -99,33 +143,51 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 // Largest value of each aligned group of 4 (or 16) lanes, in every lane of the group.
 template <int LANES>
 __device__ __forceinline__ uint32_t group_max(uint32_t m) {
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xb1, 0xf, 0xf, false));  // quad_perm [1,0,3,2]
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4e, 0xf, 0xf, false));  // quad_perm [2,3,0,1]
-  if (LANES == 16) {
-    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xf, 0xf, false));  // row_half_mirror
-    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xf, 0xf, false));  // row_mirror
-  }
-  return m;
+  if (LANES == 16) return reduce16(m, MaxOp{});
+  m = max(m, dpp16<0xb1>(m));
+  return max(m, dpp16<0x4e>(m));
 }
 
+// A row's (or group's) quantisation scale, prepared for quotients v / s.  k: a power of two that keeps
+// s normal and 1 / s finite.
+struct Scale {
+  float s, r, k;  // s and 1 / s, both times / over k
+  __device__ __forceinline__ explicit Scale(float sc) {
+    k = sc < 0x1p-60f ? 0x1p64f : 1.0f;
+    s = sc * k;
+    r = 1.0f / s;
+  }
+  // fp32(v / s): the product by the reciprocal, corrected by its remainder
+  __device__ __forceinline__ float div(float v) const {
+    v *= k;
+    const float q = v * r;
+    return fmaf(fmaf(-q, s, v), r, q);
+  }
+  // v / s rounded to a whole number, ties to even: the rounded product is at most one off, and the
+  // remainder, exact in fp32 (a multiple of half an ulp of s, at most s), says so.  (Rounding fp32(v / s)
+  // would not do: amax / 2 over s is 63.4999999, and comes out as 63.5 and then 64.)  A quotient that
+  // is exactly a half step needs an s of few bits, and fp32(amax / 127) of a bf16 amax has few bits only
+  // as a power of two, whose reciprocal is exact, so the product is the tie and rounds to even.
+  __device__ __forceinline__ int whole(float v) const {
+    v *= k;
+    const float n = __builtin_rintf(v * r), e = fmaf(-n, s, v), h = 0.5f * s;
+    return (int)n + (e > h ? 1 : 0) - (e < -h ? 1 : 0);
+  }
+};
+
 // Symmetric int8 rows: s = fp32(amax / 127) (1 when amax is 0 or the quotient underflows to 0; NaN
-// when amax is not finite, so that whatever is multiplied by it shows it), q = round(v / s) to
-// nearest, ties to even.  Both quotients go through float64: amax / 127 is then correctly rounded to
-// fp32 (53 >= 2 * 24 + 2); v * (1 / s) differs from the exact quotient by 2^-52 of it and is rounded
-// to a whole number from there (through fp32, amax / 2 over s = 63.4999999 would come out as 64).  A
-// quotient that is exactly a half step needs an s of few bits, and fp32(amax / 127) of a bf16 amax
-// has few bits only as a power of two, whose reciprocal is exact.
+// when amax is not finite, so that whatever is multiplied by it shows it).  |v| <= amax keeps the
+// codes in [-127, 127].
 __device__ __forceinline__ float i8_scale(uint32_t amax_bits) {
   if (amax_bits >= kInfBits) return __uint_as_float(0x7FC00000u);
-  const float s = float(double(__uint_as_float(amax_bits)) / 127.0);
+  const float s = __uint_as_float(amax_bits) / 127.0f;
   return s == 0.0f ? 1.0f : s;
 }
-// Four codes in a dword.  |v| <= amax, so |v / s| <= 127 (1 + 2^-24): the rounding cannot reach 128.
-__device__ __forceinline__ uint32_t i8_pack4(const float* v, double inv) {
+// Four codes in a dword.
+__device__ __forceinline__ uint32_t i8_pack4(const float* v, const Scale& sc) {
   uint32_t p = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    p |= (uint32_t(int(__builtin_rint(double(v[i]) * inv))) & 0xFFu) << (8 * i);
+  for (int i = 0; i < 4; ++i) p |= (uint32_t(sc.whole(v[i])) & 0xFFu) << (8 * i);
   return p;
 }
 

@@ -308,23 +308,27 @@ def combine(y_perm, slot_dst, topk_w, shared_y=None):
 #
 # bf16 tensors are torch.bfloat16 or their bits as torch.int16, like the rest of this module's; outputs
 # take the input's choice.  Tensors must be contiguous and on one GPU, which need not be the current
-# one: a call runs on that GPU's current stream.
+# one: a call runs on that GPU's current stream.  These calls are a few microseconds of GPU work at
+# decode sizes, so what they do on the host counts: one pass of cheap checks per tensor, and the stream's
+# handle without a Stream object (2 us).
 # ------------------------------------------------------------------------------------------------
-
-def _arg(t, name, shape, *dtypes):
-    """t itself, checked: a contiguous GPU tensor of this shape and one of these types."""
-    if t.dtype not in dtypes:
-        raise MoEError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise MoEError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise MoEError(f"{name} must be contiguous")
-    _dev(t)
-    return t
-
 
 _BF16 = (torch.bfloat16, torch.int16)
 _I8, _I32, _F32 = (torch.int8,), (torch.int32,), (torch.float32,)
+
+
+def _arg(t, name, shape, dtypes, dev):
+    """Checks a tensor: one of these types, this shape, contiguous, on GPU dev (-1: not checked here)."""
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return
+    if t.dtype not in dtypes:
+        raise MoEError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.shape != shape:
+        raise MoEError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise MoEError(f"{name} must be contiguous")
+    if dev >= 0:
+        raise MoEError(f"{name} must live on GPU {dev}, not on {t.device}")
 
 
 def _rows(t, name):
@@ -333,27 +337,28 @@ def _rows(t, name):
     return t.shape
 
 
-def _call(name, dev, *args):
-    """One library call on dev's current stream; tensors among args must live on dev."""
-    for a in args:
-        if isinstance(a, torch.Tensor) and a.device != dev:
-            raise MoEError(f"{name}: tensors on {a.device} and {dev}")
-    raw = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        _check(getattr(lib(), name)(*raw, stream), name)
+def _run(name, dev, *args):
+    """One library call (tensors' addresses and numbers) on GPU dev's current stream."""
+    if dev < 0:
+        raise MoEError("tensors must live on the GPU")
+    fn = getattr(lib(), name)
+    if dev == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(getattr(lib(), name)(*raw, stream), name)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st != MOE_OK:
+        _check(st, name)
 
 
 def quant_act_i8(x: torch.Tensor):
     """bf16 [T, d] -> int8 codes [T, d] and fp32 scales [T] (per token; or per channel of weights)."""
     T, d = _rows(x, "x")
-    _arg(x, "x", (T, d), *_BF16)
-    xq = torch.empty((T, d), dtype=torch.int8, device=x.device)
-    xs = torch.empty(T, dtype=torch.float32, device=x.device)
-    _call("moe_quant_act_i8", x.device, x, T, d, xq, xs)
+    dev = x.get_device()
+    _arg(x, "x", (T, d), _BF16, dev)
+    xq = torch.empty_like(x, dtype=torch.int8)
+    xs = x.new_empty(T, dtype=torch.float32)
+    _run("moe_quant_act_i8", dev, x.data_ptr(), T, d, xq.data_ptr(), xs.data_ptr())
     return xq, xs
 
 
@@ -369,14 +374,16 @@ def int8_tile(w: torch.Tensor) -> torch.Tensor:
 def gemm_i8(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor):
     """bf16 [M, N] = (xq [M, K] * xs [M]) (w [N, K] * w_scale [N])^T; w from int8_tile."""
     (M, K), (N, _) = _rows(xq, "xq"), _rows(w, "w")
-    _arg(xq, "xq", (M, K), *_I8)
-    _arg(xs, "xs", (M,), *_F32)
-    _arg(w, "w", (N, K), *_I8)
-    _arg(w_scale, "w_scale", (N,), *_F32)
+    dev = xq.get_device()
+    _arg(xq, "xq", (M, K), _I8, dev)
+    _arg(xs, "xs", (M,), _F32, dev)
+    _arg(w, "w", (N, K), _I8, dev)
+    _arg(w_scale, "w_scale", (N,), _F32, dev)
     if not getattr(w, "_moe_tiled", False):
         raise MoEError("w must come from int8_tile")
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
-    _call("moe_gemm_i8", xq.device, xq, xs, M, w, w_scale, N, K, y)
+    y = xq.new_empty((M, N), dtype=torch.bfloat16)
+    _run("moe_gemm_i8", dev, xq.data_ptr(), xs.data_ptr(), M, w.data_ptr(), w_scale.data_ptr(), N, K,
+         y.data_ptr())
     return y
 
 
@@ -387,25 +394,29 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None
     act_dtype take (DTYPE_FP8: e4m3 uint8 and fp32 [T, d/128]; DTYPE_MXFP4_A8: e4m3 and E8M0 uint8
     [T, d/32]; DTYPE_INT8: int8 and fp32 [T]; DTYPE_BF16: None)."""
     T, d = _rows(x, "x")
-    _arg(x, "x", (T, d), *_BF16)
-    _arg(weight, "weight", (d,), *_BF16)
-    dev = x.device
-    h = x
+    dev = x.get_device()
+    _arg(x, "x", (T, d), _BF16, dev)
+    _arg(weight, "weight", (d,), _BF16, dev)
+    h, y, q, qs = x, None, None, None
+    rp = hp = yp = qp = sp = None
     if residual is not None:
-        _arg(residual, "residual", (T, d), *_BF16)
+        _arg(residual, "residual", (T, d), _BF16, dev)
         h = torch.empty_like(x)
-    q = qs = None
+        rp, hp = residual.data_ptr(), h.data_ptr()
+    if want_y or act_dtype == DTYPE_BF16:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
     if act_dtype != DTYPE_BF16:
-        q = torch.empty((T, d), dtype=torch.int8 if act_dtype == DTYPE_INT8 else torch.uint8, device=dev)
         if act_dtype == DTYPE_INT8:
-            qs = torch.empty(T, dtype=torch.float32, device=dev)
+            q, qs = torch.empty_like(x, dtype=torch.int8), x.new_empty(T, dtype=torch.float32)
         elif act_dtype == DTYPE_FP8:
-            qs = torch.empty((T, d // 128), dtype=torch.float32, device=dev)
+            q = torch.empty_like(x, dtype=torch.uint8)
+            qs = x.new_empty((T, d // 128), dtype=torch.float32)
         else:
-            qs = torch.empty((T, d // 32), dtype=torch.uint8, device=dev)
-    y = torch.empty_like(x) if want_y or act_dtype == DTYPE_BF16 else None
-    _call("moe_rmsnorm", dev, x, residual, weight, eps, T, d, act_dtype,
-          h if residual is not None else None, y, q, qs)
+            q = torch.empty_like(x, dtype=torch.uint8)
+            qs = x.new_empty((T, d // 32), dtype=torch.uint8)
+        qp, sp = q.data_ptr(), qs.data_ptr()
+    _run("moe_rmsnorm", dev, x.data_ptr(), rp, weight.data_ptr(), eps, T, d, act_dtype, hp, yp, qp, sp)
     return h, y, q, qs
 
 
@@ -414,30 +425,33 @@ def rmsnorm_grad(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     """Gradient of rmsnorm's y (and of h on the residual path, dh): (dx [T, d], dweight fp32 [d] or
     None).  dx is the gradient of x and of residual alike."""
     T, d = _rows(dy, "dy")
-    _arg(dy, "dy", (T, d), *_BF16)
-    _arg(h, "h", (T, d), *_BF16)
-    _arg(weight, "weight", (d,), *_BF16)
+    dev = dy.get_device()
+    _arg(dy, "dy", (T, d), _BF16, dev)
+    _arg(h, "h", (T, d), _BF16, dev)
+    _arg(weight, "weight", (d,), _BF16, dev)
     if dh is not None:
-        _arg(dh, "dh", (T, d), *_BF16)
+        _arg(dh, "dh", (T, d), _BF16, dev)
     dx = torch.empty_like(dy)
     dw = ws = None
     nws = 0
     if want_dweight:
-        dw = torch.empty(d, dtype=torch.float32, device=dy.device)
+        dw = dy.new_empty(d, dtype=torch.float32)
         nws = lib().moe_rmsnorm_grad_workspace_bytes(T, d)
-        ws = torch.empty(max(1, nws), dtype=torch.uint8, device=dy.device)
-    _call("moe_rmsnorm_grad", dy.device, dy, dh, h, weight, eps, T, d, dx, dw, ws, nws)
+        ws = dy.new_empty(nws, dtype=torch.uint8) if nws else None
+    _run("moe_rmsnorm_grad", dev, dy.data_ptr(), _ptr(dh), h.data_ptr(), weight.data_ptr(), eps, T, d,
+         dx.data_ptr(), _ptr(dw), _ptr(ws), nws)
     return dx, dw
 
 
 def route_grad(ids: torch.Tensor, w: torch.Tensor, dw: torch.Tensor, E: int):
     """Gradient of route: ids, w, dw [T, k] -> dlogits fp32 [T, E]."""
     T, k = _rows(ids, "ids")
-    _arg(ids, "ids", (T, k), *_I32)
-    _arg(w, "w", (T, k), *_F32)
-    _arg(dw, "dw", (T, k), *_F32)
-    dl = torch.empty((T, E), dtype=torch.float32, device=ids.device)
-    _call("moe_route_grad", ids.device, ids, w, dw, T, E, k, dl)
+    dev = ids.get_device()
+    _arg(ids, "ids", (T, k), _I32, dev)
+    _arg(w, "w", (T, k), _F32, dev)
+    _arg(dw, "dw", (T, k), _F32, dev)
+    dl = w.new_empty((T, E))
+    _run("moe_route_grad", dev, ids.data_ptr(), w.data_ptr(), dw.data_ptr(), T, E, k, dl.data_ptr())
     return dl
 
 
@@ -445,13 +459,15 @@ def combine_grad(dout: torch.Tensor, y_perm: torch.Tensor, slot_dst: torch.Tenso
     """Gradient of combine: (dy_perm [T*k, d], dtopk_w fp32 [T, k]); shared_y's is dout."""
     T, k = _rows(topk_w, "topk_w")
     d = _rows(dout, "dout")[1]
-    _arg(topk_w, "topk_w", (T, k), *_F32)
-    _arg(dout, "dout", (T, d), *_BF16)
-    _arg(y_perm, "y_perm", (T * k, d), *_BF16)
-    _arg(slot_dst, "slot_dst", (T * k,), *_I32)
+    dev = dout.get_device()
+    _arg(dout, "dout", (T, d), _BF16, dev)
+    _arg(topk_w, "topk_w", (T, k), _F32, dev)
+    _arg(y_perm, "y_perm", (T * k, d), _BF16, dev)
+    _arg(slot_dst, "slot_dst", (T * k,), _I32, dev)
     dy = torch.empty_like(y_perm)
-    dw = torch.empty((T, k), dtype=torch.float32, device=dout.device)
-    _call("moe_combine_grad", dout.device, dout, y_perm, slot_dst, topk_w, T, k, d, dy, dw)
+    dw = torch.empty_like(topk_w)
+    _run("moe_combine_grad", dev, dout.data_ptr(), y_perm.data_ptr(), slot_dst.data_ptr(),
+         topk_w.data_ptr(), T, k, d, dy.data_ptr(), dw.data_ptr())
     return dy, dw
 
 
@@ -461,12 +477,14 @@ def permute_grad(dx_perm: torch.Tensor, slot_dst: torch.Tensor, k: int, add: tor
     if k < 1 or n % k:
         raise MoEError(f"dx_perm has {n} rows, not a multiple of k = {k}")
     T = n // k
-    _arg(dx_perm, "dx_perm", (n, d), *_BF16)
-    _arg(slot_dst, "slot_dst", (n,), *_I32)
+    dev = dx_perm.get_device()
+    _arg(dx_perm, "dx_perm", (n, d), _BF16, dev)
+    _arg(slot_dst, "slot_dst", (n,), _I32, dev)
     if add is not None:
-        _arg(add, "add", (T, d), *_BF16)
-    dx = torch.empty((T, d), dtype=dx_perm.dtype, device=dx_perm.device)
-    _call("moe_permute_grad", dx_perm.device, dx_perm, slot_dst, add, T, k, d, dx)
+        _arg(add, "add", (T, d), _BF16, dev)
+    dx = dx_perm.new_empty((T, d))
+    _run("moe_permute_grad", dev, dx_perm.data_ptr(), slot_dst.data_ptr(), _ptr(add), T, k, d,
+         dx.data_ptr())
     return dx
 
 
