@@ -214,6 +214,7 @@ struct PolicyBounds {
   bool all_few;
 };
 PolicyBounds policy_bounds(const moe_problem* p) {
+  if (is_int8(p)) return PolicyBounds{{0, 0}, {0, 0}, true};
   PolicyBounds b{{1 << 30, 1 << 30}, {0, 0}, true};
   auto add = [&](int i) {
     const SelectPolicy& P = kPolicies[i];
@@ -253,11 +254,18 @@ hipError_t launch_gemms(const SelectOut& o, const moe_problem* p, int gemm, int6
   bool mfma = p->config == MOE_CONFIG_MFMA || (auto_mode && max_rows > pb.thr_min[gemm]);
   const int64_t nt = gemm == kGemmGateUp ? p->d_ff / kMfmaBNGateUp
                                          : (p->d_model + kMfmaBNDown - 1) / kMfmaBNDown;
-  if (mfma && auto_mode && pb.all_few && max_rows <= kFewTileRows && !p->has_shared) {
+  const int few_rows = is_int8(p) ? kInt8FewTileRows : kFewTileRows;
+  if (mfma && auto_mode && pb.all_few && max_rows <= few_rows && !p->has_shared) {
     const int64_t experts = std::min<int64_t>(p->num_experts, total_rows);
-    if (5 * experts * nt < kFewTileRounds5 * (int64_t)cus) mfma = false;
+    if (5 * experts * nt < (is_int8(p) ? kInt8FewTileRounds5 : kFewTileRounds5) * (int64_t)cus)
+      mfma = false;
   }
-  if (is_int8(p)) return moe::launch_gemms_i8(o, gemm, cus, max_rows, stream, mfma, s);
+  if (is_int8(p)) {
+    // (no list streams when even the fewest experts that can hold these rows make enough MFMA tiles)
+    const int64_t fewest = (total_rows + max_rows - 1) / max_rows;
+    const bool never = auto_mode && 5 * fewest * nt >= kInt8FewTileRounds5 * (int64_t)cus;
+    return moe::launch_gemms_i8(o, gemm, cus, max_rows, stream && !never, mfma, s);
+  }
   const int64_t light = p->config == MOE_CONFIG_MFMA ? 0 : (int64_t)pb.thr_max[gemm] * p->num_experts;
   const int64_t min_tiles = (std::max<int64_t>(0, total_rows - light) + kMfmaBM - 1) / kMfmaBM * nt;
   const bool maybe_split =
@@ -265,6 +273,49 @@ hipError_t launch_gemms(const SelectOut& o, const moe_problem* p, int gemm, int6
   const int max_k = gemm == kGemmGateUp ? p->d_model
                                          : std::max(p->d_ff, p->has_shared ? p->d_ff_shared : 0);
   return moe::launch_gemms_bf16(o, gemm, cus, max_rows, max_k, stream, mfma, maybe_split, s, false);
+}
+
+// int8 experts of a small batch: both products without a selection (tok as in Seg).
+bool small_i8(const moe_problem* p) {
+  return is_int8(p) && !p->has_shared && p->config == MOE_CONFIG_AUTO && p->T <= kSmallI8Tokens &&
+         p->d_ff <= kSmallI8MaxK;
+}
+SmallI8 small_gate_up(const moe_problem* p, const moe_weights* w, const FfnWs& f, const void* x,
+                      const float* xs, const int32_t* counts, const int32_t* offsets,
+                      const int32_t* tok) {
+  SmallI8 a;
+  std::memset(&a, 0, sizeof(a));
+  a.counts = counts;
+  a.offsets = offsets;
+  a.tok = tok;
+  a.x = x;
+  a.xs = xs;
+  a.w0 = w->w_gate;
+  a.w1 = w->w_up;
+  a.s0 = w->s_gate;
+  a.s1 = w->s_up;
+  a.out = f.h;
+  a.E = p->num_experts;
+  a.N = p->d_ff;
+  a.K = p->d_model;
+  a.rows = p->T * p->top_k;
+  return a;
+}
+SmallI8 small_down(const moe_problem* p, const moe_weights* w, const FfnWs& f, void* y,
+                   const int32_t* counts, const int32_t* offsets) {
+  SmallI8 a;
+  std::memset(&a, 0, sizeof(a));
+  a.counts = counts;
+  a.offsets = offsets;
+  a.h = static_cast<const float*>(f.h);
+  a.w0 = w->w_down;
+  a.s0 = w->s_down;
+  a.out = y;
+  a.E = p->num_experts;
+  a.N = p->d_model;
+  a.K = p->d_ff;
+  a.rows = p->T * p->top_k;
+  return a;
 }
 
 // int8 experts: the rows of h (and of the shared expert's) quantised between the two GEMMs.
@@ -445,6 +496,13 @@ int moe_grouped_ffn(const moe_problem* p, const void* x_perm, const float* x_per
   SelectOut o{f.segs, f.meta, f.split_part};
   const int64_t n = (int64_t)p->T * p->top_k;
   hipError_t e = hipSuccess;
+  if (small_i8(p)) {
+    e = launch_small_i8(small_gate_up(p, w, f, x_perm, x_perm_scale, counts, offsets, nullptr), true,
+                        cus, stream);
+    if (e == hipSuccess)
+      e = launch_small_i8(small_down(p, w, f, y_perm, counts, offsets), false, cus, stream);
+    return hip_status(e);
+  }
   if (a.mx8) e = launch_quant_act_mx(x_perm, (int)n, p->d_model, f.xq, f.xe, stream);
   if (e == hipSuccess) e = launch_select(a, o, stream);  // caller-given counts: any expert may hold all rows
   if (e == hipSuccess) e = launch_gemms(o, p, kGemmGateUp, n, n, cus, stream);
@@ -767,6 +825,18 @@ int layer_impl(const moe_problem* p, const float* logits, const void* x, const m
     if (e == hipSuccess) e = mark(3);
     if (e == hipSuccess) e = launch_select(a, o, stream);
     if (e == hipSuccess) e = mark(4);
+  }
+  if (small_i8(p)) {
+    if (e == hipSuccess)
+      e = launch_small_i8(small_gate_up(p, w, L.ffn, L.xq, L.xs, counts, offsets, L.tok), true, cus,
+                          stream);
+    if (e == hipSuccess) e = mark(5);
+    if (e == hipSuccess)
+      e = launch_small_i8(small_down(p, w, L.ffn, L.y, counts, offsets), false, cus, stream);
+    if (e == hipSuccess) e = mark(6);
+    if (e == hipSuccess) e = launch_combine(L.y, slot_dst, wts, T, k, d, nullptr, out, stream);
+    if (e == hipSuccess) e = mark(7);
+    return hip_status(e);
   }
   // each token routes to k distinct experts, so no expert (nor the shared one) holds more than T rows
   if (e == hipSuccess && !decode1)

@@ -19,6 +19,7 @@
 #include "common.h"
 #include "kernels.h"
 #include "mfma_tile.h"
+#include "rows_dev.h"
 #include "stream_dev.h"
 
 namespace moe {
@@ -54,9 +55,13 @@ __device__ __forceinline__ float4 gload_f32x4(const float* p, uint32_t i) {
 // streaming tiles
 // ------------------------------------------------------------------------------------------------
 
-// Rows [m0, m0 + rows) (rows <= 16 * MQ) by the 16 weight rows of each wavefront group from n0.
-template <int MQ, bool GU, int WK>
-__device__ __forceinline__ void stream_tile_i8(const Seg& sg, int m0, int rows, int n0, int* red) {
+// Rows [m0, m0 + rows) (rows <= 16 * MQ) by the 16 weight rows of each wavefront group from n0.  XL: the
+// rows' codes lie in LDS, xl bytes apart from xs, and their scales in sxs (MQ = 1); they are read only
+// after `staged` has run, behind the first weight loads.
+template <int MQ, bool GU, int WK, bool XL = false, class Staged = void (*)()>
+__device__ __forceinline__ void stream_tile_i8(const Seg& sg, int m0, int rows, int n0, int* red,
+                                               const uint8_t* xs = nullptr, int xl = 0,
+                                               const float* sxs = nullptr, Staged staged = nullptr) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kg = lane >> 4;
   const int grp = wv / WK, kw = wv % WK;
@@ -70,14 +75,14 @@ __device__ __forceinline__ void stream_tile_i8(const Seg& sg, int m0, int rows, 
     int r = q * 16 + r16;
     r = r < rows ? r : rows - 1;  // padded columns re-read a valid row; never stored
     const int gr = sg.row0 + m0 + r;
-    src[q] = sg.tok ? gload_i32(sg.tok, gr) : gr;
-    xoff[q] = (uint32_t)src[q] * (uint32_t)K + kg * 32;
+    src[q] = XL ? r : sg.tok ? gload_i32(sg.tok, gr) : gr;
+    xoff[q] = (uint32_t)src[q] * (uint32_t)(XL ? xl : K) + kg * 32;
   }
   i32x4 acc0[MQ], acc1[MQ];
 #pragma unroll
   for (int q = 0; q < MQ; ++q) acc0[q] = acc1[q] = i32x4{0, 0, 0, 0};
-  constexpr int U = 2;  // 128-wide chunks per batch
-  struct Batch { uint4 a0[U][2], a1[U][2], b[U][MQ][2]; };
+  constexpr int U = XL || (MQ == 1 && !GU) ? 4 : 2;  // 128-wide chunks per batch
+  struct Batch { uint4 a0[U][2], a1[U][2], b[XL ? 1 : U][MQ][2]; };
   // this wavefront's chunks: kw, kw + WK, ... (the group's wavefronts read adjacent units)
   const int nc = (nkb - kw + WK - 1) / WK;
   auto load = [&](Batch& bt, int i) {
@@ -88,8 +93,10 @@ __device__ __forceinline__ void stream_tile_i8(const Seg& sg, int m0, int rows, 
       for (int h = 0; h < 2; ++h) {
         bt.a0[u][h] = gload16_nt(sg.w0, woff + kb * 2048 + h * 1024);
         if (GU) bt.a1[u][h] = gload16_nt(sg.w1, woff + kb * 2048 + h * 1024);
+        if (!XL) {
 #pragma unroll
-        for (int q = 0; q < MQ; ++q) bt.b[u][q][h] = gload16(sg.a, xoff[q] + kb * 128 + h * 16);
+          for (int q = 0; q < MQ; ++q) bt.b[XL ? 0 : u][q][h] = gload16(sg.a, xoff[q] + kb * 128 + h * 16);
+        }
       }
     }
   };
@@ -101,13 +108,17 @@ __device__ __forceinline__ void stream_tile_i8(const Seg& sg, int m0, int rows, 
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int q = 0; q < MQ; ++q) {
-          acc0[q] = mfma16_i8(bt.a0[u][h], bt.b[u][q][h], acc0[q]);
-          if (GU) acc1[q] = mfma16_i8(bt.a1[u][h], bt.b[u][q][h], acc1[q]);
+          const uint4 b = XL ? *reinterpret_cast<const uint4*>(
+                                   xs + xoff[q] + (uint32_t)(kw + WK * (i + u)) * 128 + h * 16)
+                             : bt.b[XL ? 0 : u][q][h];
+          acc0[q] = mfma16_i8(bt.a0[u][h], b, acc0[q]);
+          if (GU) acc1[q] = mfma16_i8(bt.a1[u][h], b, acc1[q]);
         }
     }
   };
   Batch b0, b1;
   if (nc > 0) load(b0, 0);
+  if constexpr (XL) staged();
   for (int i = 0; i < nc; i += 2 * U) {
     if (i + U < nc) load(b1, i + U);
     compute(b0, i);
@@ -116,8 +127,8 @@ __device__ __forceinline__ void stream_tile_i8(const Seg& sg, int m0, int rows, 
   }
   // split-K sums: wavefronts kw > 0 of a group park theirs in LDS, wavefront 0 adds them
   constexpr int NV = MQ * 4 * (GU ? 2 : 1);
-  __syncthreads();  // red[] may still be read by the previous tile
-  if (kw > 0) {
+  if (WK > 1) __syncthreads();  // red[] may still be read by the previous tile
+  if (WK > 1 && kw > 0) {
     int* dst = red + ((grp * (WK - 1) + kw - 1) * NV) * 64 + lane;
 #pragma unroll
     for (int q = 0; q < MQ; ++q)
@@ -127,7 +138,7 @@ __device__ __forceinline__ void stream_tile_i8(const Seg& sg, int m0, int rows, 
         if (GU) dst[(MQ * 4 + q * 4 + j) * 64] = acc1[q][j];
       }
   }
-  __syncthreads();
+  if (WK > 1) __syncthreads();
   if (kw != 0) return;
 #pragma unroll
   for (int w = 0; w < WK - 1; ++w) {
@@ -148,7 +159,7 @@ __device__ __forceinline__ void stream_tile_i8(const Seg& sg, int m0, int rows, 
   for (int q = 0; q < MQ; ++q) {
     const int r = q * 16 + r16;
     if (r >= rows) continue;
-    const float sx = gload_f32(sg.as, src[q]);
+    const float sx = XL ? sxs[src[q]] : gload_f32(sg.as, src[q]);
     const size_t at = (size_t)(sg.row0 + m0 + r) * N + n0 + 4 * kg;
     float v[4];
 #pragma unroll
@@ -205,6 +216,99 @@ __global__ __launch_bounds__(256) void gemm_stream_i8_dense(Seg sg) {
   __shared__ int red[3 * MQ * 4 * 64];
   const int m0 = (blockIdx.x % sg.mtiles) * (16 * MQ);
   stream_tile_i8<MQ, false, 4>(sg, m0, min(16 * MQ, sg.rows - m0), (blockIdx.x / sg.mtiles) * 16, red);
+}
+
+// ------------------------------------------------------------------------------------------------
+// small batches: at most kSmallI8Tokens tokens
+//
+// A decode step's experts hold a few rows each, and the launches around the weights' stream weigh as
+// much as a part of it: the selection kernel (one workgroup, 8-10 us) and the rows' quantisation (5 us)
+// beside 40 + 30 us of weights at one token (DeepSeek-V3-shaped layer).  Here every workgroup finds the
+// experts that hold rows by itself, from the counts, and a down tile quantises its expert's rows of h
+// into LDS while its first weights are on their way.  Same tiles, same sums, same bits.
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ void small_list(const int32_t* counts, int E, int (&s_exp)[kSmallI8Rows],
+                                           int& s_n) {
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int n = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int e = e0 + lane;
+      const bool has = e < E && gload_i32(counts, e) > 0;
+      const uint64_t m = __ballot(has);
+      const int at = n + __popcll(m & ((1ull << lane) - 1));
+      if (has && at < kSmallI8Rows) s_exp[at] = e;
+      n += __popcll(m);
+    }
+    if (lane == 0) s_n = min(n, kSmallI8Rows);
+  }
+  __syncthreads();
+}
+
+template <bool GU, int WK>
+__global__ __launch_bounds__(256) void gemm_small_i8(SmallI8 a) {
+  constexpr int TN = 64 / WK;  // output columns per workgroup
+  __shared__ int s_exp[kSmallI8Rows];
+  __shared__ int s_n;
+  __shared__ int red[(WK > 1 ? 3 : 1) * 4 * 2 * 64];
+  __shared__ float s_sx[16];
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];  // down: up to 16 rows of codes
+  small_list(a.counts, a.E, s_exp, s_n);
+  const int per = a.N / TN, ntiles = s_n * per, xl = a.K + 16;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
+    const int e = __builtin_amdgcn_readfirstlane(s_exp[t / per]);
+    Seg sg = {};
+    sg.a = a.x;
+    sg.as = a.xs;
+    sg.tok = a.tok;
+    sg.w0 = static_cast<const uint8_t*>(a.w0) + (size_t)e * a.N * a.K;
+    sg.w1 = static_cast<const uint8_t*>(a.w1) + (size_t)e * a.N * a.K;
+    sg.s0 = a.s0 + (size_t)e * a.N;
+    sg.s1 = a.s1 + (size_t)e * a.N;
+    sg.out = a.out;
+    sg.N = a.N;
+    sg.K = a.K;
+    sg.row0 = __builtin_amdgcn_readfirstlane(gload_i32(a.offsets, e));
+    // (never more rows than the batch has, whatever the counts say: the codes' LDS is sized for them)
+    const int rows = min(__builtin_amdgcn_readfirstlane(gload_i32(a.counts, e)), a.rows);
+    const int n0 = (t % per) * TN;
+    for (int m0 = 0; m0 < rows; m0 += 16) {
+      const int r = min(16, rows - m0);
+      if constexpr (GU) {
+        stream_tile_i8<1, true, WK>(sg, m0, r, n0, red);
+      } else {
+        const float* h = a.h + (size_t)(sg.row0 + m0) * a.K;
+        stream_tile_i8<1, false, WK, true>(sg, m0, r, n0, red, s_x, xl, s_sx, [&] {
+          __syncthreads();  // (the last tile's readers are done)
+          // a wavefront per row: its largest magnitude, then its codes (as quant_i8_kernel)
+          for (int i = wv; i < r; i += 4) {
+            const float* row = h + (size_t)i * a.K;
+            uint32_t m[1] = {0u};
+            for (int c = lane * 4; c < a.K; c += 256) {
+              const uint4 v = ld16(row + c, 0);
+              m[0] = max(max(m[0], max(v.x & 0x7FFFFFFFu, v.y & 0x7FFFFFFFu)),
+                         max(v.z & 0x7FFFFFFFu, v.w & 0x7FFFFFFFu));
+            }
+            row_reduce<64>(m, static_cast<uint32_t*>(nullptr), MaxOp{});
+            const float sc = i8_scale(m[0]);
+            const bool bad = m[0] >= kInfBits;
+            const Scale f(bad ? 1.0f : sc);
+            if (lane == 0) s_sx[i] = sc;
+            for (int c = lane * 4; c < a.K; c += 256) {
+              const uint4 u = ld16(row + c, 0);
+              float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                            __uint_as_float(u.w)};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] = bad ? 0.f : v[j];
+              *reinterpret_cast<uint32_t*>(s_x + i * xl + c) = i8_pack4(v, f);
+            }
+          }
+          __syncthreads();
+        });
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -348,8 +452,14 @@ __global__ __launch_bounds__(256, 1) void gemm_mfma_i8(const Seg* __restrict__ s
   for (int i = threadIdx.x; i < nseg; i += blockDim.x) seg_base[i] = segs[i].tile_base;
   __syncthreads();
   MfmaTile<GU, ElemI8> tile;
+  // A list of at most one position per workgroup is handed out without the queues, whose ends every
+  // workgroup would look for in turn (some 10 us): XCD x takes an equal run of positions.
+  const int npos = sbase + ((ntiles - sbase) << lgs), per = (npos + kXcds - 1) / kXcds;
+  const bool once = npos <= (int)gridDim.x && per <= (int)gridDim.x / kXcds && order != kOrderTwoClass;
+  const int mine = blockIdx.x / kXcds < per ? blockIdx.x % kXcds * per + blockIdx.x / kXcds : npos;
   int q = 0;
-  for (;;) {
+  for (bool first = true;; first = false) {
+    if (once && (!first || mine >= npos)) return;
     // (opaque moves: the reciprocals of the queue's divisions are computed here, not held across
     // the K loops)
     const int nt_ = opaque_s(ntiles), nt0_ = opaque_s(ntiles0), ch_ = opaque_s(chunk);
@@ -360,7 +470,8 @@ __global__ __launch_bounds__(256, 1) void gemm_mfma_i8(const Seg* __restrict__ s
       if (t < 0) return;
     } else {
       const int sb_ = opaque_s(sbase);
-      int pos = pop_tile_xcd(meta + kMetaQueue, sb_ + ((nt_ - sb_) << lgs), ch_, &slot, q);
+      int pos = once ? mine
+                     : pop_tile_xcd(meta + kMetaQueue, sb_ + ((nt_ - sb_) << lgs), ch_, &slot, q);
       if (pos < 0) return;
       if (pos >= sb_) {
         hrows = BM >> lgs;
@@ -454,6 +565,19 @@ hipError_t launch_gemms_i8(const SelectOut& o, int g, int num_cus, int64_t max_r
   } else {
     if (stream) launch_stream_i8<false>(ss, ms, num_cus, max_rows, s);
     if (mfma) gemm_mfma_i8<false><<<num_cus, 256, 0, s>>>(sm, mm);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_small_i8(const SmallI8& a, bool gate_up, int num_cus, hipStream_t s) {
+  const size_t lds = gate_up ? 0 : (size_t)std::min(a.rows, 16) * (a.K + 16);
+  const int g = num_cus * (gate_up ? 4 : 5);
+  if (gate_up) {
+    if (a.K >= kStreamSplitK) gemm_small_i8<true, 4><<<g, 256, 0, s>>>(a);
+    else gemm_small_i8<true, 2><<<g, 256, 0, s>>>(a);
+  } else {
+    if (a.K >= kStreamSplitK) gemm_small_i8<false, 4><<<g, 256, lds, s>>>(a);
+    else gemm_small_i8<false, 1><<<g, 256, lds, s>>>(a);
   }
   return hipGetLastError();
 }

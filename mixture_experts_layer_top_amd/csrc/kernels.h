@@ -22,6 +22,10 @@ constexpr int kStreamMaxRows = 64;  // rows per weight-streaming pass
 // expert keeps the whole GEMM on MFMA.
 constexpr int kFewTileRows = 16;
 constexpr int kFewTileRounds5 = 8;
+// int8 experts: MFMA tiles, unless a GEMM's would fill fewer than kInt8FewTileRounds5 / 5 rounds and no
+// expert holds more rows than one streaming pass: then all stream (see kInt8Policy).
+constexpr int kInt8FewTileRows = kStreamMaxRows;
+constexpr int kInt8FewTileRounds5 = 1;
 constexpr int kMfmaBM = 256;        // rows per full LDS-tiled MFMA tile
 constexpr int kMfmaBNGateUp = 128;  // h columns per gate/up MFMA tile (128 gate + 128 up rows)
 constexpr int kMfmaBNDown = 256;    // y columns per down MFMA tile
@@ -222,6 +226,22 @@ hipError_t launch_quant_act(const void* x, int T, int d, uint8_t* xq, float* xs,
 // the rows' quantisation (bf16, or fp32 when f32; d % 8 == 0, d <= 32768).
 hipError_t launch_gemms_i8(const SelectOut& o, int gemm, int num_cus, int64_t max_rows, bool stream,
                            bool mfma, hipStream_t s);
+// The experts' products of at most kSmallI8Tokens tokens (d_ff <= kSmallI8MaxK), without a selection:
+// gate/up writes fp32 h, down quantises its rows of h itself.
+constexpr int kSmallI8Tokens = 16;  // (an expert then holds one 16-row pass, unless ids repeat)
+constexpr int kSmallI8Rows = kSmallI8Tokens * kMaxTopK;
+constexpr int kSmallI8MaxK = 4096;
+struct SmallI8 {
+  const int32_t* counts; const int32_t* offsets;
+  const int32_t* tok;                   // row -> row of x (null: itself)
+  const void* x; const float* xs;       // gate/up: int8 rows and scales
+  const float* h;                       // down: fp32 rows
+  const void* w0; const void* w1;       // gate and up, or down (w1 null)
+  const float* s0; const float* s1;
+  void* out;                            // fp32 h, or bf16 y
+  int E, N, K, rows;
+};
+hipError_t launch_small_i8(const SmallI8& a, bool gate_up, int num_cus, hipStream_t s);
 hipError_t launch_gemm_i8(const void* xq, const float* xs, int M, const void* wq, const float* ws,
                           int N, int K, void* y, int num_cus, hipStream_t s);
 hipError_t launch_quant_i8(const void* x, bool f32, int T, int d, uint8_t* q, float* qs,

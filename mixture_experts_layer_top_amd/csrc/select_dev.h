@@ -82,16 +82,16 @@ __device__ __forceinline__ void select_block(const SelectArgs& a, const SelectOu
   const bool shared = e == a.E;
   const int ffe = shared ? a.f_sh : a.f;
   // The policy ("Decoding the Skew", Abstract: the live histogram matched to offline-tuned
-  // configurations): bf16 (and int8) problems in automatic mode look it up by T and the live effective expert
+  // configurations): bf16 problems in automatic mode look it up by T and the live effective expert
   // count; config >= kConfigPolicy0 forces one; forced families (config 0 / 1) and the streaming-only
   // formats use none.
-  const bool bf16 = !a.fp8 && !a.w4;
+  const bool bf16 = !a.fp8 && !a.w4 && !a.i8;
   const float eeff = bf16 ? block_eeff(e < a.E ? c : 0, a.T * a.k) : 0.f;
   const bool auto_mode = a.config < 0 || a.config >= kConfigPolicy0;
   const int pol = !bf16 || !auto_mode ? -1
                   : a.config >= kConfigPolicy0 ? a.config - kConfigPolicy0
                                                : kPolicyTable[t_bucket(a.T)][eeff_bucket(eeff)];
-  const SelectPolicy P = kPolicies[pol < 0 ? 0 : pol];
+  const SelectPolicy P = a.i8 ? kInt8Policy : kPolicies[pol < 0 ? 0 : pol];
   if (e == 0) {
     if (a.out_eeff) a.out_eeff[0] = eeff;
     if (a.out_policy) a.out_policy[0] = pol;
@@ -144,7 +144,7 @@ __device__ __forceinline__ void select_block(const SelectArgs& a, const SelectOu
                  ? (c + kMfmaBM - 1) / kMfmaBM * (g == 0 ? ffe / kMfmaBNGateUp : nt_dn)
                  : 0;
       w[2 + g] = fm[g] == kFamMfma && c > kMfmaBM ? 1 : 0;
-      w[4 + g] = fm[g] == kFamMfma && c > kFewTileRows ? 1 : 0;
+      w[4 + g] = fm[g] == kFamMfma && c > (a.i8 ? kInt8FewTileRows : kFewTileRows) ? 1 : 0;
     }
     // (streamed down experts hold at most P.thr_dn <= 64 < kMfmaBM rows: one m-tile each)
     w[6] = auto_mode && P.promote && fm[kGemmDown] == kFamStream ? nt_dn : 0;
@@ -157,7 +157,8 @@ __device__ __forceinline__ void select_block(const SelectArgs& a, const SelectOu
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       if (auto_mode && P.few_tile && fm[g] == kFamMfma &&
-          5 * wtot[g] < kFewTileRounds5 * a.num_cus && wtot[4 + g] == 0)
+          5 * wtot[g] < (a.i8 ? kInt8FewTileRounds5 : kFewTileRounds5) * a.num_cus &&
+          wtot[4 + g] == 0)
         fm[g] = kFamStream;
       const int C = min(a.num_cus, kSplitMaxPieces);
       lpt[g] = wtot[g] >= C && wtot[g] < kSplitMaxRounds * C;

@@ -33,6 +33,12 @@ constexpr SelectPolicy kPolicies[] = {
     {0, 0, 0, 0},    // 6: every expert on MFMA tiles
     {64, 64, 0, 0},  // 7: every expert of at most 64 rows streams
 };
+// int8 experts have one policy: MFMA tiles from one row, and the few-tile rule with up to a streaming
+// pass of rows, below a fifth of a round.  Measured with both families forced: 256 experts, d 7168, d_ff
+// 2048, 64 tokens: all MFMA 1.20 against 1.38 ms (the down tiles' 2 KB of K leave a streaming workgroup
+// little to pipeline); 8 experts, d 4096, d_ff 2048, 64 tokens (half a round): 55 against 67 us; 5 of them
+// active (0.3): 52 against 56; 4 experts, d 2048, d_ff 1024, 64 tokens (0.12): 32 against 25.
+constexpr SelectPolicy kInt8Policy = {0, 0, 0, 1};
 constexpr int kNumPolicies = sizeof(kPolicies) / sizeof(kPolicies[0]);
 constexpr int kConfigPolicy0 = 16;  // moe_problem.config = 16 + i forces policy i
 
