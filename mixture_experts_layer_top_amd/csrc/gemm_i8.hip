@@ -210,12 +210,99 @@ __global__ __launch_bounds__(256) void gemm_stream_i8(const Seg* __restrict__ se
   }
 }
 
-// The dense product's streaming form: one segment, 16 columns per workgroup.
-template <int MQ>
+// The dense product's streaming form: 16 * NR weight rows by 16 * MQ token rows per workgroup, whose 4
+// wavefronts split K (interleaved chunks; the sums meet in LDS).  A wavefront's weight blocks share its
+// token fragments and the other way round, so the traffic between L2 and the CU, which bounds all but the
+// smallest batches, falls with both.
+template <int MQ, int NR>
 __global__ __launch_bounds__(256) void gemm_stream_i8_dense(Seg sg) {
-  __shared__ int red[3 * MQ * 4 * 64];
-  const int m0 = (blockIdx.x % sg.mtiles) * (16 * MQ);
-  stream_tile_i8<MQ, false, 4>(sg, m0, min(16 * MQ, sg.rows - m0), (blockIdx.x / sg.mtiles) * 16, red);
+  constexpr int U = MQ * NR == 1 ? 4 : MQ * NR <= 4 ? 2 : 1;  // 128-wide chunks per batch
+  constexpr int NV = MQ * NR * 4;                            // sums per lane
+  __shared__ int red[3 * NV * 64];
+  const int lane = threadIdx.x & 63, kw = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, kg = lane >> 4;
+  const int K = sg.K, N = sg.N, nkb = K / 128;
+  const int m0 = (blockIdx.x % sg.mtiles) * (16 * MQ), rows = min(16 * MQ, sg.rows - m0);
+  const int n0 = (blockIdx.x / sg.mtiles) * (16 * NR);
+  uint32_t woff[NR], xoff[MQ];
+#pragma unroll
+  for (int j = 0; j < NR; ++j)  // (a block past N re-reads the last one; never stored)
+    woff[j] = (uint32_t)min((n0 >> 4) + j, (N >> 4) - 1) * (uint32_t)(nkb * 2048) + lane * 16;
+#pragma unroll
+  for (int q = 0; q < MQ; ++q)  // (a row past the last re-reads it; never stored)
+    xoff[q] = (uint32_t)(m0 + min(q * 16 + r16, rows - 1)) * (uint32_t)K + kg * 32;
+  i32x4 acc[NR][MQ];
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int q = 0; q < MQ; ++q) acc[j][q] = i32x4{0, 0, 0, 0};
+  struct Batch { uint4 w[U][NR][2], x[U][MQ][2]; };
+  const int nc = (nkb - kw + 3) / 4;  // this wavefront's chunks: kw, kw + 4, ...
+  auto load = [&](Batch& bt, int i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t kb = (uint32_t)min(kw + 4 * (i + u), nkb - 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+          bt.w[u][j][h] = sg.mtiles == 1 ? gload16_nt(sg.w0, woff[j] + kb * 2048 + h * 1024)
+                                         : gload16(sg.w0, woff[j] + kb * 2048 + h * 1024);
+#pragma unroll
+        for (int q = 0; q < MQ; ++q) bt.x[u][q][h] = gload16(sg.a, xoff[q] + kb * 128 + h * 16);
+      }
+    }
+  };
+  auto compute = [&](const Batch& bt, int i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u >= nc) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+          for (int q = 0; q < MQ; ++q) acc[j][q] = mfma16_i8(bt.w[u][j][h], bt.x[u][q][h], acc[j][q]);
+    }
+  };
+  Batch b0, b1;
+  if (nc > 0) load(b0, 0);
+  for (int i = 0; i < nc; i += 2 * U) {
+    if (i + U < nc) load(b1, i + U);
+    compute(b0, i);
+    if (i + 2 * U < nc) load(b0, i + 2 * U);
+    if (i + U < nc) compute(b1, i + U);
+  }
+  // every wavefront parks its sums but those of the pieces (j, q) it finishes itself: piece p goes to
+  // wavefront p % 4, slot order (p, wavefront)
+  constexpr int P = NR * MQ;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    if (p % 4 == kw) continue;
+    int* dst = red + (p * 3 + (kw < p % 4 ? kw : kw - 1)) * 256 + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i * 64] = acc[p / MQ][p % MQ][i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    if (p % 4 != kw) continue;
+    const int j = p / MQ, q = p % MQ;
+    const int* src = red + p * 3 * 256 + lane;
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][q][i] += src[w * 256 + i * 64];
+    const int r = q * 16 + r16, n = n0 + 16 * j + 4 * kg;
+    if (r >= rows || n >= N) continue;
+    const float4 s4 = gload_f32x4(sg.s0, n);
+    const float c[4] = {s4.x, s4.y, s4.z, s4.w};
+    const float sx = gload_f32(sg.as, m0 + r);
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = float(acc[j][q][i]) * sx * c[i];
+    gstore8(sg.out, ((size_t)(m0 + r) * N + n) * 2, uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -594,13 +681,32 @@ hipError_t launch_gemm_i8(const void* xq, const float* xs, int M, const void* wq
   sg.rows = M;
   sg.N = N;
   sg.K = K;
-  if (M <= 64) {
-    const int mq = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-    sg.mtiles = 1;
-    sg.ntiles = N / 16;
-    if (mq == 1) gemm_stream_i8_dense<1><<<sg.ntiles, 256, 0, s>>>(sg);
-    else if (mq == 2) gemm_stream_i8_dense<2><<<sg.ntiles, 256, 0, s>>>(sg);
-    else gemm_stream_i8_dense<4><<<sg.ntiles, 256, 0, s>>>(sg);
+  // The widest streaming tile that still gives three quarters of the CUs one (16 * mq token rows, no
+  // more than the batch has, by 16 * nr weight rows); past one and a half rounds of the widest, the MFMA
+  // tiles.  Measured (us; 7168 x 7168, then 2048 x 7168): 16 tokens 1x2 11.6 against 1x1 14.8, 1x1 7.2
+  // against 2x2 8.4; 64 tokens 2x4 20 against 1x1 39 and MFMA 41, 2x1 10 against 2x4 13; 128 tokens 4x4 27
+  // against MFMA 40, 2x2 12 against MFMA 26; 256 tokens MFMA 41 against 4x4 48.
+  constexpr int kTiles[][2] = {{4, 4}, {2, 4}, {2, 2}, {1, 2}, {1, 1}};
+  const int groups = (M + 15) / 16;
+  int mq = 0, nr = 0;
+  for (const auto& c : kTiles) {
+    if (c[0] >= 2 * groups) continue;
+    const int64_t wgs = (int64_t)((groups + c[0] - 1) / c[0]) * ((N / 16 + c[1] - 1) / c[1]);
+    if (c[0] == 4 && 2 * wgs > 3 * num_cus) break;
+    if (4 * wgs < 3 * num_cus && c[0] * c[1] > 1) continue;
+    mq = c[0];
+    nr = c[1];
+    break;
+  }
+  if (mq) {
+    sg.mtiles = (groups + mq - 1) / mq;
+    sg.ntiles = (N / 16 + nr - 1) / nr;
+    const unsigned grid = (unsigned)sg.mtiles * sg.ntiles;
+    if (mq == 4) gemm_stream_i8_dense<4, 4><<<grid, 256, 0, s>>>(sg);
+    else if (mq == 2 && nr == 4) gemm_stream_i8_dense<2, 4><<<grid, 256, 0, s>>>(sg);
+    else if (mq == 2) gemm_stream_i8_dense<2, 2><<<grid, 256, 0, s>>>(sg);
+    else if (nr == 2) gemm_stream_i8_dense<1, 2><<<grid, 256, 0, s>>>(sg);
+    else gemm_stream_i8_dense<1, 1><<<grid, 256, 0, s>>>(sg);
     return hipGetLastError();
   }
   const int g = std::max(kXcds, num_cus / kXcds * kXcds);
@@ -612,9 +718,12 @@ hipError_t launch_gemm_i8(const void* xq, const float* xs, int M, const void* wq
   if (full) {
     while (lgs < 3 && (tiles - full) * (2 << lgs) <= g) ++lgs;
     pieces = (int)(tiles - full) << lgs;
-  } else {  // the tallest tile that gives every CU one
-    while (lgs < 3 && ((M + (BM >> lgs) - 1) / (BM >> lgs)) * (int64_t)sg.ntiles < g) ++lgs;
-    pieces = (M + (BM >> lgs) - 1) / (BM >> lgs) * sg.ntiles;
+  } else {
+    // the shortest tiles that still make one round: a tile's time is mostly its weights', which one CU
+    // draws at some 50 GB/s (7168 x 7168, 512 tokens: 224 tiles of 64 rows 45 us, 448 of 32 73)
+    auto count = [&](int l) { return (int64_t)((M + (BM >> l) - 1) / (BM >> l)) * sg.ntiles; };
+    while (lgs < 3 && count(lgs + 1) <= g) ++lgs;
+    pieces = (int)count(lgs);
   }
   gemm_mfma_i8_dense<<<g, 256, 0, s>>>(sg, full, pieces, lgs);
   return hipGetLastError();
