@@ -252,6 +252,7 @@ hipError_t launch_quant_i8(const void* x, bool f32, int T, int d, uint8_t* q, fl
 hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float eps, int T, int d,
                           int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s);
 constexpr int kNormGradBlocks = 512;
+constexpr int kNormGradRows = 3;  // per workgroup, until there are that many
 int rmsnorm_grad_parts(int T);
 hipError_t launch_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* w,
                                float eps, int T, int d, void* dx, float* dw, float* part,

@@ -13,6 +13,7 @@
 // squares, then the scaling) run from there, and the 8-bit output costs no second read of y.  The
 // sum of squares is held in fp64 across a row: the terms are exact in fp32 and the chip's fp64 rate
 // is far above what the memory asks for.
+#include <algorithm>
 #include <type_traits>
 
 #include "kernels.h"
@@ -206,6 +207,10 @@ __global__ __launch_bounds__(row_block(R)) void quant_i8_kernel(const void* __re
 
 // Norm gradient: every workgroup takes rows blockIdx.x, + gridDim.x, ... and keeps its share of dw
 // in registers; part [gridDim.x][d] receives it (summed by dw_reduce_kernel, in a fixed order).
+// Up to 4096 channels the next row is loaded while this one is reduced (two rows do not fit the
+// registers beyond that).  Both kernels, T x d: 4096 x 4096 with dh 28.3 us (4.75 TB/s; 30.5 without
+// the second row in flight and with 8 columns a workgroup in the sum), 8192 x 7168 with dh 94.6 (4.97),
+// 777 x 7168 15.2 (21.3), 17 x 4096 5.5.
 template <int R, int V>
 __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
     const void* dy, const void* dh, const void* h, const void* __restrict__ w, float eps,
@@ -217,24 +222,38 @@ __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
   for (int s = 0; s < V; ++s)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[s][j] = 0.f;
-  int turn = 0;
-  for (int row = blockIdx.x; row < T; row += gridDim.x, turn ^= 1) {
+  // the row's vectors, and the next row's in flight while this one is reduced and written
+  struct Row { uint4 h[V], g[V], a[V]; };
+  auto load = [&](Row& r, int row) {
     const size_t base = (size_t)row * nvec;
-    uint4 hv[V], gv[V], av[V];
 #pragma unroll
     for (int s = 0; s < V; ++s) {
       const size_t idx = base + min(i + R * s, nvec - 1);
-      hv[s] = ld16(h, idx);
-      gv[s] = ld16(dy, idx);
-      if (dh) av[s] = ld16(dh, idx);
+      r.h[s] = ld16(h, idx);
+      r.g[s] = ld16(dy, idx);
+      if (dh) r.a[s] = ld16(dh, idx);
     }
+  };
+  uint4 wr[V];
+#pragma unroll
+  for (int s = 0; s < V; ++s) wr[s] = ld16(w, min(i + R * s, nvec - 1));
+  constexpr bool kAhead = V <= 2;  // (more vectors a thread: no registers for a second row)
+  Row cur, nxt;
+  if (kAhead) load(cur, blockIdx.x);
+  int turn = 0;
+  for (int row = blockIdx.x; row < T; row += gridDim.x, turn ^= 1) {
+    const bool more = row + (int)gridDim.x < T;
+    // (dx may be dy or dh: a row's own vectors are all loaded before it is written, and no other row's
+    // are written by this call before their workgroup has loaded them)
+    if (!kAhead) load(cur, row);
+    else if (more) load(nxt, row + gridDim.x);
     double sum[2] = {0.0, 0.0};
 #pragma unroll
     for (int s = 0; s < V; ++s) {
       float a[8], g[8], wv[8];
-      unpack8(hv[s], a);
-      unpack8(gv[s], g);
-      unpack8(ld16(w, min(i + R * s, nvec - 1)), wv);
+      unpack8(cur.h[s], a);
+      unpack8(cur.g[s], g);
+      unpack8(wr[s], wv);
       float p = 0.f, c = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -253,18 +272,19 @@ __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
 #pragma unroll
     for (int s = 0; s < V; ++s) {
       float a[8], g[8], wv[8], add[8], o[8];
-      unpack8(hv[s], a);
-      unpack8(gv[s], g);
-      unpack8(ld16(w, min(i + R * s, nvec - 1)), wv);
-      if (dh) unpack8(av[s], add);
+      unpack8(cur.h[s], a);
+      unpack8(cur.g[s], g);
+      unpack8(wr[s], wv);
+      if (dh) unpack8(cur.a[s], add);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[s][j] = fmaf(g[j], a[j] * rstd, dw[s][j]);
         o[j] = rstd * fmaf(-c, a[j], g[j] * wv[j]);
         if (dh) o[j] += add[j];
       }
-      if (i + R * s < nvec) st16(dx, base + i + R * s, pack8(o));
+      if (i + R * s < nvec) st16(dx, (size_t)row * nvec + i + R * s, pack8(o));
     }
+    if (kAhead && more) cur = nxt;
   }
   if (!part) return;
 #pragma unroll
@@ -279,19 +299,30 @@ __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
   }
 }
 
-// dw[c] = sum_b part[b][c]: 8 columns per workgroup, 32 threads take every 32nd partial of a
-// column, then their sums in order.
+// dw[c] = sum_b part[b][c]: 32 columns per workgroup (whole 128-byte lines), its 32 groups of 8 threads
+// take every 32nd partial, then the groups' sums in order.
 __global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict__ part, int nb, int d,
                                                         float* __restrict__ dw) {
-  __shared__ float red[32][9];
-  const int c = threadIdx.x & 7, r = threadIdx.x >> 3, col = blockIdx.x * 8 + c;
-  float s = 0.f;
-  for (int b = r; b < nb; b += 32) s += part[(size_t)b * d + col];
-  red[r][c] = s;
+  __shared__ float red[32][33];
+  const int c = threadIdx.x & 7, r = threadIdx.x >> 3, col = blockIdx.x * 32 + c * 4;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (col < d) {  // (d % 8 == 0)
+#pragma unroll 4
+    for (int b = r; b < nb; b += 32) {
+      const uint4 v = ld16(part, ((size_t)b * d + col) / 4);
+      s[0] += __uint_as_float(v.x);
+      s[1] += __uint_as_float(v.y);
+      s[2] += __uint_as_float(v.z);
+      s[3] += __uint_as_float(v.w);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) red[r][c * 4 + j] = s[j];
   __syncthreads();
-  if (r == 0) {
-    for (int b = 1; b < 32; ++b) s += red[b][c];
-    dw[col] = s;
+  if (threadIdx.x < 32 && blockIdx.x * 32 + (int)threadIdx.x < d) {
+    float v = 0.f;
+    for (int b = 0; b < 32; ++b) v += red[b][threadIdx.x];
+    dw[blockIdx.x * 32 + threadIdx.x] = v;
   }
 }
 
@@ -329,8 +360,12 @@ hipError_t launch_quant_i8(const void* x, bool f32, int T, int d, uint8_t* q, fl
   return hipGetLastError();
 }
 
-// Partial sums of dw: one per workgroup.
-int rmsnorm_grad_parts(int T) { return T < kNormGradBlocks ? T : kNormGradBlocks; }
+// Partial sums of dw: one per workgroup, each 8 d bytes of traffic beside a row's 6 or 8 d.  At 1, 3 and
+// 6 rows per workgroup: 777 x 4096 13.4, 12.3, 13.4 us; 333 x 4096 9.8, 9.9, 12.5; 1500 x 2048 11.1,
+// 11.9, 12.4.
+int rmsnorm_grad_parts(int T) {
+  return T <= 64 ? T : std::min(kNormGradBlocks, std::max(64, (T + kNormGradRows - 1) / kNormGradRows));
+}
 
 hipError_t launch_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* w,
                                float eps, int T, int d, void* dx, float* dw, float* part,
@@ -347,7 +382,7 @@ hipError_t launch_rmsnorm_grad(const void* dy, const void* dh, const void* h, co
     else if (nvec <= 1024) with_steps<256, 1, 4>((nvec + 255) / 256, go);
     else with_steps<512, 3, 4>((nvec + 511) / 512, go);
   }
-  if (dw) dw_reduce_kernel<<<nvec, 256, 0, s>>>(part, nb, d, dw);
+  if (dw) dw_reduce_kernel<<<(d + 31) / 32, 256, 0, s>>>(part, nb, d, dw);
   return hipGetLastError();
 }
 
