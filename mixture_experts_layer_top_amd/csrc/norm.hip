@@ -154,40 +154,43 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
   }
 }
 
-// x [T][d] bf16 or fp32 -> int8 rows and their scales.
+// x [T][d] bf16 or fp32 -> int8 rows and their scales.  A thread takes 16 bytes of x per load (8 bf16
+// values or 4 fp32), so that a wavefront's loads are whole lines in both.  The fp32 rows are a scratch
+// of the experts, read here for the last time, past the caches: 8192 x 14336 98 us (6.0 TB/s), 114
+// with plain loads; 512 x 2048 4.8 us either way.
 template <bool F32, int R, int V>
 __global__ __launch_bounds__(row_block(R)) void quant_i8_kernel(const void* __restrict__ x, int T,
                                                                 int nvec, uint8_t* __restrict__ q,
                                                                 float* __restrict__ qs) {
+  constexpr int N = F32 ? 4 : 8, L = F32 ? 2 * V : V;
   __shared__ uint32_t redm[R / 64];
   const int row = R == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (R == 64 && row >= T) return;
   const int i = R == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const size_t base = (size_t)row * nvec;
-  uint4 a[V], b[F32 ? V : 1];
+  const int n = F32 ? 2 * nvec : nvec;
+  const size_t base = (size_t)row * n;
+  uint4 a[L];
 #pragma unroll
-  for (int s = 0; s < V; ++s) {
-    const size_t idx = base + min(i + R * s, nvec - 1);
-    a[s] = ld16(x, F32 ? 2 * idx : idx);
-    if (F32) b[F32 ? s : 0] = ld16(x, 2 * idx + 1);
+  for (int s = 0; s < L; ++s) {
+    const size_t idx = base + min(i + R * s, n - 1);
+    a[s] = F32 ? ld16_once(x, idx) : ld16(x, idx);
   }
-  auto vec = [&](int s, float (&v)[8]) {
-    if (F32) {
-      const uint4 c = b[F32 ? s : 0];
-      const uint32_t p[8] = {a[s].x, a[s].y, a[s].z, a[s].w, c.x, c.y, c.z, c.w};
+  auto vec = [&](int s, float (&v)[N]) {
+    if constexpr (F32) {
+      const uint32_t p[4] = {a[s].x, a[s].y, a[s].z, a[s].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(p[j]);
+      for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(p[j]);
     } else {
       unpack8(a[s], v);
     }
   };
   uint32_t m[1] = {0u};  // (clamped loads repeat a value of the row: the maximum is unchanged)
 #pragma unroll
-  for (int s = 0; s < V; ++s) {
-    float v[8];
+  for (int s = 0; s < L; ++s) {
+    float v[N];
     vec(s, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m[0] = max(m[0], abs_bits(v[j]));
+    for (int j = 0; j < N; ++j) m[0] = max(m[0], abs_bits(v[j]));
   }
   row_reduce<R>(m, redm, MaxOp{});
   const float sc = i8_scale(m[0]);
@@ -195,13 +198,15 @@ __global__ __launch_bounds__(row_block(R)) void quant_i8_kernel(const void* __re
   const Scale f(bad ? 1.0f : sc);
   if (i == 0) qs[row] = sc;
 #pragma unroll
-  for (int s = 0; s < V; ++s) {
-    if (i + R * s >= nvec) continue;
-    float v[8];
+  for (int s = 0; s < L; ++s) {
+    if (i + R * s >= n) continue;
+    float v[N];
     vec(s, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = bad ? 0.f : v[j];
-    st8(q, (base + i + R * s) * 8, i8_pack4(v, f), i8_pack4(v + 4, f));
+    for (int j = 0; j < N; ++j) v[j] = bad ? 0.f : v[j];
+    const size_t at = (base + i + R * s) * N;
+    if constexpr (F32) gstore4(q, at, i8_pack4(v, f));
+    else st8(q, at, i8_pack4(v, f), i8_pack4(v + 4, f));
   }
 }
 

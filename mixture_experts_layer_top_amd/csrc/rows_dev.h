@@ -72,9 +72,7 @@ __device__ __forceinline__ uint4 ld16_once(const void* base, size_t vec) {
   return __builtin_bit_cast(uint4, v);
 }
 __device__ __forceinline__ void st16_once(void* base, size_t vec, const uint4& v) {
-  __builtin_nontemporal_store(
-      __builtin_bit_cast(u32x4, v),
-      reinterpret_cast<__attribute__((address_space(1))) u32x4*>((gwchar*)base) + vec);
+  gstore16_nt(base, vec * 16, v);
 }
 __device__ __forceinline__ void st8(void* base, size_t off, uint32_t a, uint32_t b) {
   gstore8(base, off, uint2{a, b});
