@@ -305,3 +305,175 @@ def test_norm_sort_experts_together_in_a_graph(moe):
                 room[r] += wn[r, j, None] * (sl + np.abs(v) * 2.0 ** -7)
     want = f64(hh) + o
     assert (np.abs(f64(gh) - want) <= 1.01 * room + (np.abs(o) + np.abs(want)) * 2.0 ** -8).all()
+
+
+# ------------------------------------------------------------------------------------------------
+# the tile choices
+# ------------------------------------------------------------------------------------------------
+
+# Dense products by the tile they take on 256 CUs: 64 x 64, 64 weight rows by 32 tokens (a ragged last
+# weight block), 32 x 32, 32 by 16, 16 x 16; MFMA pieces only (32, 64 and 128 rows), whole tiles with 1,
+# 2, 4 and 8 pieces per tile behind them, and none.
+TILES = [(64, 12352, 128), (100, 6160, 256), (33, 6208, 128), (20, 3120, 384), (16, 6160, 256), (7, 2064, 640),
+         (130, 12304, 128), (520, 7168, 128), (700, 11280, 128), (2100, 11520, 128), (2100, 10240, 128),
+         (2100, 8208, 256), (2100, 8192, 128), (2048, 8192, 128)]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+def test_gemm_i8_tiles(moe, M, N, K):
+    xq, w = _codes(M, K, seed=M), _codes(N, K, seed=N + 1)
+    xs, ws = _scales(M, seed=K), _scales(N, seed=K + 1)
+    t = moe.int8_tile(w)
+    y = moe.gemm_i8(xq, xs, t, ws)
+    # (a float64 product of these codes is exact: its sums stay below 2^53)
+    ref = (xq.double() @ w.double().T) * xs.double()[:, None] * ws.double()
+    assert ((y.double() - ref).abs() <= ref.abs() * (2.0 ** -8 + 2.0 ** -21)).all()
+    # a row has the same bits alone, from the smallest tile
+    one = moe.gemm_i8(xq[:1].contiguous(), xs[:1].contiguous(), t, ws)
+    assert torch.equal(one[0], y[0])
+
+
+def test_gemm_i8_up_to_the_offset_limit(moe):
+    """M * K and N * K just below 2^32: rows far apart are the rows of a small product."""
+    K = 32640
+    n = 2 ** 32 // K // 16 * 16
+    assert 2 ** 32 - 16 * K <= n * K < 2 ** 32
+    few, fs = _codes(16, K, seed=1), _scales(16, seed=2)
+    other, os_ = _codes(48, K, seed=3), _scales(48, seed=4)
+    x, xs = few.repeat(n // 16, 1), fs.repeat(n // 16)
+    want = moe.gemm_i8(few, fs, moe.int8_tile(other), os_)  # [16, 48]
+    y = moe.gemm_i8(x, xs, moe.int8_tile(other), os_)
+    assert torch.equal(y.view(-1, 16, 48), want.expand(n // 16, 16, 48))
+    t = moe.int8_tile(x)
+    for M in (1, 30, 48):
+        got = moe.gemm_i8(other[:M].contiguous(), os_[:M].contiguous(), t, xs)
+        small = moe.gemm_i8(other[:M].contiguous(), os_[:M].contiguous(), moe.int8_tile(few), fs)
+        assert torch.equal(got.view(M, -1, 16), small[:, None].expand(M, n // 16, 16)), M
+
+
+def test_quant_act_i8_past_32_bit_offsets(moe):
+    d = 7168
+    T = 2 ** 32 // d + 100
+    few = _bf16(4, d, seed=5)
+    q, s = moe.quant_act_i8(few.repeat(T // 4, 1))
+    wq, ws = moe.quant_act_i8(few)
+    assert torch.equal(q.view(-1, 4, d), wq.expand(T // 4, 4, d)) and torch.equal(s.view(-1, 4), ws.expand(T // 4, 4))
+
+
+# ------------------------------------------------------------------------------------------------
+# lists in pieces, and small batches
+# ------------------------------------------------------------------------------------------------
+
+# MFMA lists whose last round is cut by token rows: less than a round of tiles (2 and 4 pieces each),
+# and a round and some (a tall tile's pieces, a short tail's, empty ones).
+PIECES = [([200, 256, 30, 64], 256, 4096), ([256, 129, 1], 128, 2048), ([700, 1, 513], 256, 7168),
+          ([300] * 9, 128, 2048), ([256, 40] * 9, 128, 2048)]
+
+
+@pytest.mark.parametrize("counts,d,f", PIECES, ids=lambda v: str(v).replace(" ", ""))
+def test_grouped_ffn_in_pieces(moe, counts, d, f):
+    xq, xs, cnt, off = _rows(counts, d, seed=7)
+    W = Experts(moe, len(counts), d, f, seed=8)
+    n = xq.shape[0]
+    y = moe.grouped_ffn(xq, xs, cnt, off, W.ew, n, 1, moe.CONFIG_MFMA)
+    assert torch.equal(y, moe.grouped_ffn(xq, xs, cnt, off, W.ew, n, 1, moe.CONFIG_STREAM))
+    assert torch.equal(y, moe.grouped_ffn(xq, xs, cnt, off, W.ew, n, 1))
+    e = len(counts) - 1
+    s = slice(int(off[e]), n)
+    ref, slack = R.expert_i8(f64(xq[s]), f64(xs[s]), W.get(e))
+    assert (np.abs(f64(y.view(torch.bfloat16))[s] - ref) <=
+            slack * (1 + 2.0 ** -7) + np.abs(ref) * (2.0 ** -8 + 2.0 ** -20)).all()
+
+
+# At most 16 tokens: counts, T, k, d, f.  All rows with one expert (a token's ids may repeat), passes of
+# 16 and a tail, a long K in either product, many experts of one row, experts that all hold none.
+SMALL = [([0, 32], 16, 2, 256, 256), ([17, 0, 15], 16, 2, 128, 384), ([0] * 7 + [128], 16, 8, 128, 128),
+         ([0, 3, 1, 0, 4], 4, 2, 4224, 256), ([1, 1, 0, 2], 2, 2, 256, 4096), ([1] * 8 + [0] * 56, 1, 8, 256, 128),
+         ([1, 0] * 64, 8, 8, 128, 128), ([0, 0], 16, 1, 128, 128), ([3, 2] + [0] * 6, 16, 8, 128, 256)]
+
+
+@pytest.mark.parametrize("counts,T,k,d,f", SMALL, ids=lambda v: str(v).replace(" ", "")[:24])
+def test_grouped_ffn_small_batches(moe, counts, T, k, d, f):
+    xq, xs, cnt, off = _rows(counts, d, seed=12)
+    W = Experts(moe, len(counts), d, f, seed=13)
+    n = xq.shape[0]
+    q = torch.zeros(T * k, d, dtype=torch.int8, device="cuda")
+    s = torch.ones(T * k, device="cuda")
+    q[:n], s[:n] = xq, xs
+    y = moe.grouped_ffn(q, s, cnt, off, W.ew, T, k)[:n].view(torch.bfloat16)
+    for cfg in (moe.CONFIG_STREAM, moe.CONFIG_MFMA):
+        assert torch.equal(y, moe.grouped_ffn(q, s, cnt, off, W.ew, T, k, cfg)[:n].view(torch.bfloat16))
+    for e, c in enumerate(counts):
+        if c and (e < 3 or c > 1):
+            a = slice(int(off[e]), int(off[e + 1]))
+            ref, slack = R.expert_i8(f64(xq[a]), f64(xs[a]), W.get(e))
+            assert (np.abs(f64(y[a]) - ref) <= slack * (1 + 2.0 ** -7) + np.abs(ref) * (2.0 ** -8 + 2.0 ** -20)).all(), e
+
+
+def _direct(moe, xq, xs, cnt, off, W, T, k, d, f, y, ws):
+    import ctypes
+    p = moe.problem(T, d, f, cnt.numel(), k, wdtype=moe.DTYPE_INT8)
+    w = W.ew.struct()
+    return moe.lib().moe_grouped_ffn(ctypes.byref(p), xq.data_ptr(), xs.data_ptr(), cnt.data_ptr(), off.data_ptr(),
+                                     ctypes.byref(w), y.data_ptr(), ws.data_ptr(), ws.numel(),
+                                     torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_two_calls_at_once_with_their_own_workspaces(moe, T):
+    """Two streams, two workspaces that hold NaN bytes: neither call reads what it has not written, rows
+    behind the last expert's stay as they were, and a NaN row stays alone."""
+    import ctypes
+    d, f, k, E = 384, 512, 2, 6
+    counts = [T, 0, T // 2, 1, 0, 0]
+    W = Experts(moe, E, d, f, seed=17)
+    xq, xs, cnt, off = _rows(counts, d, seed=18)
+    n = xq.shape[0]
+    want = moe.grouped_ffn(xq, xs, cnt, off, W.ew, n, 1, moe.CONFIG_STREAM)
+    bad = xs.clone()
+    bad[1] = float("nan")
+    q = torch.zeros(T * k, d, dtype=torch.int8, device="cuda")
+    q[:n] = xq
+    need = moe.lib().moe_grouped_ffn_workspace_bytes(ctypes.byref(moe.problem(T, d, f, E, k, wdtype=moe.DTYPE_INT8)))
+    ys, streams, keep = [], [torch.cuda.Stream(), torch.cuda.Stream()], []
+    scales = []
+    for src in (xs, bad):
+        s = torch.full((T * k,), float("nan"), device="cuda")
+        s[:n] = src
+        scales.append(s)
+    torch.cuda.synchronize()
+    for rep in range(3):
+        for st, s in zip(streams, scales):
+            with torch.cuda.stream(st):
+                ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+                y = torch.full((T * k, d), 7, dtype=torch.int16, device="cuda")
+                assert _direct(moe, q, s, cnt, off, W, T, k, d, f, y, ws) == 0
+                ys.append(y)
+                keep.append(ws)
+    torch.cuda.synchronize()
+    ok = torch.arange(n, device="cuda") != 1
+    for i, y in enumerate(ys):
+        assert (y[n:] == 7).all()
+        assert torch.equal(y[:n][ok], want[ok])
+        if i % 2:
+            assert y[1].view(torch.bfloat16).isnan().all()
+        else:
+            assert torch.equal(y[1], want[1])
+
+
+def test_layer_of_one_token_in_a_graph(moe):
+    """The small path captured, with eager calls on the same weights between the replays."""
+    d, f, E, k = 512, 256, 16, 4
+    W = Experts(moe, E, d, f, seed=23)
+    x, lg = _bf16(1, d, seed=1), torch.randn(1, E, generator=_gen(2)).cuda()
+    moe.layer(lg, x.view(torch.int16), W.ew, k)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = moe.layer(lg, x.view(torch.int16), W.ew, k)
+    for seed in (1, 5, 6, 7):
+        x.copy_(_bf16(1, d, seed=seed))
+        lg.copy_(torch.randn(1, E, generator=_gen(seed + 100)).cuda())
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, moe.layer(lg, x.view(torch.int16), W.ew, k))

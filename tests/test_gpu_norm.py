@@ -215,3 +215,43 @@ def test_rmsnorm_grad_against_differences(moe):
     assert abs(num - (f64(dx) * v).sum()) <= (np.abs(f64(dx) * v)).sum() * 2.0 ** -8 + 1e-6
     num = (f(f64(h), f64(w) + e * vw) - f(f64(h), f64(w) - e * vw)) / (2 * e)
     assert abs(num - (f64(dw) * vw).sum()) <= (np.abs(f64(dw) * vw)).sum() * 2.0 ** -18 + 1e-6
+
+
+def test_rmsnorm_past_32_bit_offsets(moe):
+    """More than 2^32 bytes per tensor: every fourth row is the same row."""
+    d = 7168
+    T = 2 ** 31 // d // 4 * 4 + 400
+    x, res, w = _bf16(4, d, seed=1), _bf16(4, d, seed=2), _bf16(d, seed=3)
+    big = [t.repeat(T // 4, 1) for t in (x, res)]
+    few = moe.rmsnorm(x, w, res, EPS, moe.DTYPE_INT8)
+    got = moe.rmsnorm(big[0], w, big[1], EPS, moe.DTYPE_INT8)
+    for a, b in zip(got, few):
+        assert torch.equal(a.view(T // 4, 4, -1), b.view(1, 4, -1).expand(T // 4, 4, -1))
+    del got
+    dy, dh, h = _bf16(4, d, seed=4), _bf16(4, d, seed=5), few[0]
+    dx0, _ = moe.rmsnorm_grad(dy, h, w, dh, EPS)
+    dx, dw = moe.rmsnorm_grad(dy.repeat(T // 4, 1), h.repeat(T // 4, 1), w, dh.repeat(T // 4, 1), EPS)
+    assert torch.equal(dx.view(T // 4, 4, d), dx0.expand(T // 4, 4, d))
+    # dw: a workgroup adds T / 512 rows one after another, the sum over workgroups 16 and then 32 more;
+    # each term is within 12 u
+    n = h.double() / (h.double().square().mean(1, keepdim=True) + EPS).sqrt()
+    terms = dy.double() * n
+    room = (T / 512 + 1 + 48 + 12) * 2.0 ** -24 * terms.abs().sum(0) * (T // 4)
+    assert ((dw.double() - terms.sum(0) * (T // 4)).abs() <= room).all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 191, 193, 1535, 1536, 1537])
+def test_rmsnorm_grad_weight_by_rows(moe, T):
+    """Row counts around those at which workgroups take one, some and many rows."""
+    d = 136
+    h, dy, w = _bf16(T, d, seed=T), _bf16(T, d, seed=T + 1), _bf16(d, seed=3)
+    dx, dw = moe.rmsnorm_grad(dy, h, w, None, EPS)
+    hd = h.double()
+    rstd = (hd.square().mean(1, keepdim=True) + EPS).rsqrt()
+    g = dy.double() * w.double()
+    want = rstd * (g - hd * rstd * rstd * (g * hd).mean(1, keepdim=True))
+    # (g - n mean(g n)) / rms: both products and their sums within 2^-20 of their magnitudes, then bf16
+    mag = rstd * (g.abs() + (hd * rstd).abs() * rstd * (g * hd).abs().mean(1, keepdim=True))
+    assert ((dx.double() - want).abs() <= want.abs() * 2.0 ** -8 + mag * 2.0 ** -19).all()
+    terms = dy.double() * hd * rstd
+    assert ((dw.double() - terms.sum(0)).abs() <= (T + 60) * 2.0 ** -24 * terms.abs().sum(0)).all()

@@ -160,3 +160,35 @@ def test_way_back_together(moe):
         ex, ew, _ = chain(sx)
         torch.cuda.synchronize()
         assert torch.equal(gx, ex) and torch.equal(gw, ew)
+
+
+def test_rows_past_32_bit_offsets(moe):
+    """More than 2^32 bytes of rows: every 16th token is the same token."""
+    T, k, d = 40000, 8, 7168
+    dst = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    y, dout, w = _bf16(16 * k, d, seed=1), _bf16(16, d, seed=2), torch.rand(16, k, generator=_gen(3)).cuda()
+    dy0, dw0 = moe.combine_grad(dout, y, dst[:16 * k], w)
+    rep = T // 16
+    big = y.repeat(rep, 1)
+    dy, dw = moe.combine_grad(dout.repeat(rep, 1), big, dst, w.repeat(rep, 1))
+    assert torch.equal(dy.view(rep, 16 * k, d), dy0.expand(rep, 16 * k, d))
+    # (16 tokens and 40000 take different numbers of threads per row: another order of the d products)
+    mag = (dout.double()[:, None].abs() * y.double().view(16, k, d).abs()).sum(-1)
+    assert ((dw.double().view(rep, 16, k) - dw0.double()).abs() <= 2 * (d // 64 + 16) * 2.0 ** -24 * mag).all()
+    dx0 = moe.permute_grad(y, dst[:16 * k], k)
+    dx = moe.permute_grad(big, dst, k)
+    assert torch.equal(dx.view(rep, 16, d), dx0.expand(rep, 16, d))
+
+
+@pytest.mark.parametrize("T,d", [(1500, 7168), (70000, 128)])
+def test_combine_grad_beyond_the_last_level_cache(moe, T, d):
+    """Sizes whose rows pass the caches by give the bits of their parts, which do not."""
+    k = 8
+    dst = torch.randperm(T * k, generator=_gen(1)).to(torch.int32).cuda()
+    y, dout, w = _bf16(T * k, d, seed=2), _bf16(T, d, seed=3), torch.rand(T, k, generator=_gen(4)).cuda()
+    dy, dw = moe.combine_grad(dout, y, dst, w)
+    half = 800
+    p = dst[:half * k].long()
+    dyh, dwh = moe.combine_grad(dout[:half].contiguous(), y[p].contiguous(),
+                                torch.arange(half * k, dtype=torch.int32, device="cuda"), w[:half].contiguous())
+    assert torch.equal(dy[p], dyh) and torch.equal(dw[:half], dwh)
