@@ -97,12 +97,15 @@ enum moe_dtype {
  * use them to cover each.  Block-scaled fp8 weights in automatic mode put experts of more than 128
  * rows (mxfp4 weights with mxfp8 activations: more than 64) on the MFMA tiles when a GEMM's MFMA
  * tiles fill at least one round of compute units, the others on the streaming tiles (no policy
- * table); mxfp4 weights with bf16 activations always stream. */
+ * table); mxfp4 weights with bf16 activations always stream.  int8 weights in automatic mode use the
+ * MFMA tiles, unless a GEMM's would fill less than a fifth of a round and no expert holds more than 64
+ * rows, and at most 16 tokens (no shared expert, d_ff <= 4096) stream without a selection; every choice
+ * gives the same bits. */
 enum moe_config {
   MOE_CONFIG_AUTO = -1,
   MOE_CONFIG_STREAM = 0, /* weight-streaming tiles: up to 64 of an expert's rows per pass */
   MOE_CONFIG_MFMA = 1,   /* LDS-tiled MFMA tiles: bf16 64, 128 or 256 rows (from the rows a tile
-                            holds) x 256 weight rows; fp8 and mxfp4 with mxfp8 activations
+                            holds) x 256 weight rows, int8 also 32; fp8 and mxfp4 with mxfp8 activations
                             256 x 256 (mxfp4 with bf16 activations: MOE_ERR_UNSUPPORTED) */
   MOE_CONFIG_FUSED = 2,  /* moe_layer of one bf16 token without a shared expert, d_model and d_ff
                             <= 8192: the whole layer in one launch ("Weave", Abstract:
@@ -173,7 +176,7 @@ typedef struct moe_routing {
   int32_t* slot_dst; /* [T*k] */
   float* eeff;        /* [1]: the live effective expert count the bf16 selection computed */
   int32_t* policy;    /* [1]: the policy it applied (-1 when a family was forced); neither is
-                         written for fp8 / mxfp4 weights or the single-token bf16 path */
+                         written for fp8, mxfp4 or int8 weights or the single-token bf16 path */
 } moe_routing;
 
 /* Route: topk_ids[t][j] = j-th largest logit's expert (ties -> lower id), topk_w[t][j] = its
@@ -247,7 +250,7 @@ int moe_fp8_tile(const void* src, void* dst, int64_t rows, int64_t cols, hipStre
 int moe_combine(const void* y_perm, const int32_t* slot_dst, const float* topk_w, int T, int k,
                 int d, const void* shared_y, void* out, hipStream_t stream);
 
-/* The whole layer: route -> permute -> (fp8: quantise activations) -> grouped gate/up + SwiGLU ->
+/* The whole layer: route -> permute -> (fp8, int8: quantise activations) -> grouped gate/up + SwiGLU ->
  * grouped down (+ shared expert) -> combine.  The token gather is fused into the gate/up GEMM's
  * activation loads.  For a single bf16 token without a shared expert (T = 1, d <= 8192, config
  * not forcing MFMA tiles) routing, permutation and selection run inside the gate/up kernel: same
@@ -260,7 +263,8 @@ size_t moe_layer_workspace_bytes(const moe_problem* p);
 
 /* moe_layer with phase timing: records events[0] before the first launch and events[i] after
  * phase i, for the phases route (1), permute (2), activation quantisation (3, empty for bf16),
- * tile selection (4), gate/up GEMM + SwiGLU (5), down GEMM (6) and combine (7).  (In the
+ * tile selection (4), gate/up GEMM + SwiGLU (5), down GEMM (6, with the quantisation of h for int8
+ * weights) and combine (7).  (In the
  * single-token case of moe_layer phases 1-4 are empty and phase 5 includes them.)  The caller creates
  * the MOE_TRACE_EVENTS events (hipEventCreate) and reads them after the stream has passed them.
  * NULL entries are skipped (each recorded timing event adds a few microseconds of GPU time, so

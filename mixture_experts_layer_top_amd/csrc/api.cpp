@@ -740,8 +740,8 @@ int layer_impl(const moe_problem* p, const float* logits, const void* x, const m
   a.h = L.ffn.h; a.hs = L.ffn.hs;
   a.h_sh = L.ffn.h_sh; a.hs_sh = L.ffn.hs_sh;
   a.y = L.y; a.y_sh = L.ffn.y_sh;
-  a.out_eeff = out_eeff;
-  a.out_policy = out_policy;
+  a.out_eeff = a.i8 ? nullptr : out_eeff;
+  a.out_policy = a.i8 ? nullptr : out_policy;
   SelectOut o{L.ffn.segs, L.ffn.meta, L.ffn.split_part};
 
   hipError_t e = mark(0);

@@ -477,3 +477,40 @@ def test_layer_of_one_token_in_a_graph(moe):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, moe.layer(lg, x.view(torch.int16), W.ew, k))
+
+
+@pytest.mark.parametrize("T,d,f,E,k,sf", [(2, 256, 4096, 16, 2, 0), (9, 384, 256, 64, 8, 0), (16, 256, 384, 9, 8, 0),
+                                          (16, 256, 4224, 4, 2, 0), (17, 256, 256, 9, 8, 0), (16, 256, 256, 4, 2, 128)])
+def test_layer_around_the_small_path(moe, T, d, f, E, k, sf):
+    """Every way through moe_layer at few tokens gives the same bits; a traced call records the phases, and
+    neither writes the bf16 selection's outputs."""
+    x, logits = _bf16(T, d, seed=T + 2), torch.randn(T, E, generator=_gen(T + 3)).cuda()
+    W = Experts(moe, E, d, f, seed=31, shared_f=sf)
+    xb = x.view(torch.int16)
+    out = moe.layer(logits, xb, W.ew, k)
+    for cfg in (moe.CONFIG_STREAM, moe.CONFIG_MFMA):
+        assert torch.equal(out, moe.layer(logits, xb, W.ew, k, cfg))
+    keep = dict(eeff=torch.full((1,), 5.0, device="cuda"), policy=torch.full((1,), 77, dtype=torch.int32, device="cuda"))
+    L = moe.Layer(W.ew, T, E, k)
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(moe.TRACE_EVENTS)]
+    for e in ev:
+        e.record()  # (creates the handle)
+    got = L.traced(logits, xb, [e.cuda_event for e in ev], keep)
+    torch.cuda.synchronize()
+    assert torch.equal(got, out) and float(keep["eeff"]) == 5.0 and int(keep["policy"]) == 77
+    assert all(a.elapsed_time(b) >= 0 for a, b in zip(ev, ev[1:]))
+    # and the oracle
+    xq, xs = moe.quant_act_i8(x)
+    ids, w = moe.route(logits, k)
+    want, room = np.zeros((T, d)), np.zeros((T, d))
+    idn, wn, qn, sn = ids.cpu().numpy(), f64(w), f64(xq), f64(xs)
+    for e in range(E):
+        t, j = np.nonzero(idn == e)
+        if len(t):
+            ref, slack = R.expert_i8(qn[t], sn[t], W.get(e))
+            np.add.at(want, t, wn[t, j][:, None] * ref)
+            np.add.at(room, t, wn[t, j][:, None] * (slack + np.abs(ref) * 2.0 ** -7))
+    if sf:
+        r, sk = R.expert_i8(qn, sn, W.get_shared())
+        want, room = want + r, room + sk + np.abs(r) * 2.0 ** -7
+    assert (np.abs(f64(out.view(torch.bfloat16)) - want) <= room * 1.01 + np.abs(want) * 2.0 ** -8).all()
