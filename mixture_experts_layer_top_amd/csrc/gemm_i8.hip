@@ -212,8 +212,10 @@ __global__ __launch_bounds__(256) void gemm_stream_i8(const Seg* __restrict__ se
 
 // The dense product's streaming form: 16 * NR weight rows by 16 * MQ token rows per workgroup, whose 4
 // wavefronts split K (interleaved chunks; the sums meet in LDS).  A wavefront's weight blocks share its
-// token fragments and the other way round, so the traffic between L2 and the CU, which bounds all but the
-// smallest batches, falls with both.
+// token fragments and the other way round, so the traffic between L2 and the CUs, which bounds all but the
+// smallest batches (some 40 GB/s per CU with all of them loading, with twice the loads in flight too),
+// falls with both.  7168 x 7168: 16 tokens 12 us (4.3 TB/s of weights), 64 19, 128 27; 2048 x 7168: 64
+// tokens 7.8, 256 13.3.
 template <int MQ, int NR>
 __global__ __launch_bounds__(256) void gemm_stream_i8_dense(Seg sg) {
   constexpr int U = MQ * NR == 1 ? 4 : MQ * NR <= 4 ? 2 : 1;  // 128-wide chunks per batch
@@ -222,8 +224,12 @@ __global__ __launch_bounds__(256) void gemm_stream_i8_dense(Seg sg) {
   const int lane = threadIdx.x & 63, kw = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kg = lane >> 4;
   const int K = sg.K, N = sg.N, nkb = K / 128;
-  const int m0 = (blockIdx.x % sg.mtiles) * (16 * MQ), rows = min(16 * MQ, sg.rows - m0);
-  const int n0 = (blockIdx.x / sg.mtiles) * (16 * NR);
+  // (the tiles of one weight block on one XCD, whose L2 they share)
+  const int tile = sg.mtiles == 1 ? blockIdx.x
+                                  : (blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+  if (tile >= sg.mtiles * sg.ntiles) return;
+  const int m0 = (tile % sg.mtiles) * (16 * MQ), rows = min(16 * MQ, sg.rows - m0);
+  const int n0 = (tile / sg.mtiles) * (16 * NR);
   uint32_t woff[NR], xoff[MQ];
 #pragma unroll
   for (int j = 0; j < NR; ++j)  // (a block past N re-reads the last one; never stored)
@@ -681,34 +687,13 @@ hipError_t launch_gemm_i8(const void* xq, const float* xs, int M, const void* wq
   sg.rows = M;
   sg.N = N;
   sg.K = K;
-  // The widest streaming tile that still gives three quarters of the CUs one (16 * mq token rows, no
-  // more than the batch has, by 16 * nr weight rows); past one and a half rounds of the widest, the MFMA
-  // tiles.  Measured (us; 7168 x 7168, then 2048 x 7168): 16 tokens 1x2 11.6 against 1x1 14.8, 1x1 7.2
-  // against 2x2 8.4; 64 tokens 2x4 20 against 1x1 39 and MFMA 41, 2x1 10 against 2x4 13; 128 tokens 4x4 27
-  // against MFMA 40, 2x2 12 against MFMA 26; 256 tokens MFMA 41 against 4x4 48.
-  constexpr int kTiles[][2] = {{4, 4}, {2, 4}, {2, 2}, {1, 2}, {1, 1}};
-  const int groups = (M + 15) / 16;
-  int mq = 0, nr = 0;
-  for (const auto& c : kTiles) {
-    if (c[0] >= 2 * groups) continue;
-    const int64_t wgs = (int64_t)((groups + c[0] - 1) / c[0]) * ((N / 16 + c[1] - 1) / c[1]);
-    if (c[0] == 4 && 2 * wgs > 3 * num_cus) break;
-    if (4 * wgs < 3 * num_cus && c[0] * c[1] > 1) continue;
-    mq = c[0];
-    nr = c[1];
-    break;
-  }
-  if (mq) {
-    sg.mtiles = (groups + mq - 1) / mq;
-    sg.ntiles = (N / 16 + nr - 1) / nr;
-    const unsigned grid = (unsigned)sg.mtiles * sg.ntiles;
-    if (mq == 4) gemm_stream_i8_dense<4, 4><<<grid, 256, 0, s>>>(sg);
-    else if (mq == 2 && nr == 4) gemm_stream_i8_dense<2, 4><<<grid, 256, 0, s>>>(sg);
-    else if (mq == 2) gemm_stream_i8_dense<2, 2><<<grid, 256, 0, s>>>(sg);
-    else if (nr == 2) gemm_stream_i8_dense<1, 2><<<grid, 256, 0, s>>>(sg);
-    else gemm_stream_i8_dense<1, 1><<<grid, 256, 0, s>>>(sg);
-    return hipGetLastError();
-  }
+  // A tile's time is mostly its rows' way from L2 (tokens and weights alike), which all CUs together draw
+  // at 9 (streaming) to 12 TB/s (LDS DMA), so the choice is the tile of the fewest rows times rounds of
+  // CUs; an MFMA tile's rows count three quarters.  Measured with each tile forced (us): 7168 x 7168,
+  // 16 tokens 1x2 12.2 (1x1 15.7, 2x2 12.9), 64 tokens 2x4 19.4 (4x4 28, 2x2 24, MFMA 41), 128 tokens 4x4
+  // 26.6 (2x4 30, MFMA 40), 192 tokens MFMA 40.3 (4x4 46.6); 2048 x 7168, 64 tokens 1x2 7.8 (2x2 10.9,
+  // 1x1 11.8, 4x4 20), 160 tokens 2x4 13.2 (1x2 16.9, 2x2 18.6, 4x4 20), 384 tokens 4x4 20.5 (2x4 22, 2x2
+  // 26, MFMA 27); 14336 x 4096, 48 tokens 4x4 17.9 (2x4 18.8), 96 tokens MFMA 26.1 (4x4 28).
   const int g = std::max(kXcds, num_cus / kXcds * kXcds);
   sg.ntiles = (N + kMfmaBNDown - 1) / kMfmaBNDown;
   sg.mtiles = (M + BM - 1) / BM;
@@ -719,11 +704,35 @@ hipError_t launch_gemm_i8(const void* xq, const float* xs, int M, const void* wq
     while (lgs < 3 && (tiles - full) * (2 << lgs) <= g) ++lgs;
     pieces = (int)(tiles - full) << lgs;
   } else {
-    // the shortest tiles that still make one round: a tile's time is mostly its weights', which one CU
-    // draws at some 50 GB/s (7168 x 7168, 512 tokens: 224 tiles of 64 rows 45 us, 448 of 32 73)
+    // the shortest tiles that still make one round (7168 x 7168, 512 tokens: 224 tiles of 64 rows 45 us,
+    // 448 of 32 73)
     auto count = [&](int l) { return (int64_t)((M + (BM >> l) - 1) / (BM >> l)) * sg.ntiles; };
     while (lgs < 3 && count(lgs + 1) <= g) ++lgs;
     pieces = (int)count(lgs);
+  }
+  constexpr int kTiles[][2] = {{1, 1}, {1, 2}, {2, 2}, {2, 4}, {4, 4}};  // 16 token rows x 16 weight rows
+  const int groups = (M + 15) / 16;
+  int64_t best = (full ? (tiles + g - 1) / g * (BM + BNW) : (BM >> lgs) + BNW) * 12;
+  int mq = 0, nr = 0;
+  for (const auto& c : kTiles) {
+    if (c[0] >= 2 * groups) continue;
+    const int64_t wgs = (int64_t)((groups + c[0] - 1) / c[0]) * ((N / 16 + c[1] - 1) / c[1]);
+    const int64_t cost = (wgs + num_cus - 1) / num_cus * (c[0] + c[1]) * 16 * 16;
+    if (cost > best) continue;
+    best = cost;
+    mq = c[0];
+    nr = c[1];
+  }
+  if (mq) {
+    sg.mtiles = (groups + mq - 1) / mq;
+    sg.ntiles = (N / 16 + nr - 1) / nr;
+    const unsigned grid = ((unsigned)sg.mtiles * sg.ntiles + kXcds - 1) / kXcds * kXcds;
+    if (mq == 4) gemm_stream_i8_dense<4, 4><<<grid, 256, 0, s>>>(sg);
+    else if (mq == 2 && nr == 4) gemm_stream_i8_dense<2, 4><<<grid, 256, 0, s>>>(sg);
+    else if (mq == 2) gemm_stream_i8_dense<2, 2><<<grid, 256, 0, s>>>(sg);
+    else if (nr == 2) gemm_stream_i8_dense<1, 2><<<grid, 256, 0, s>>>(sg);
+    else gemm_stream_i8_dense<1, 1><<<grid, 256, 0, s>>>(sg);
+    return hipGetLastError();
   }
   gemm_mfma_i8_dense<<<g, 256, 0, s>>>(sg, full, pieces, lgs);
   return hipGetLastError();

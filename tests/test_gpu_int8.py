@@ -311,12 +311,14 @@ def test_norm_sort_experts_together_in_a_graph(moe):
 # the tile choices
 # ------------------------------------------------------------------------------------------------
 
-# Dense products by the tile they take on 256 CUs: 64 x 64, 64 weight rows by 32 tokens (a ragged last
-# weight block), 32 x 32, 32 by 16, 16 x 16; MFMA pieces only (32, 64 and 128 rows), whole tiles with 1,
-# 2, 4 and 8 pieces per tile behind them, and none.
-TILES = [(64, 12352, 128), (100, 6160, 256), (33, 6208, 128), (20, 3120, 384), (16, 6160, 256), (7, 2064, 640),
-         (130, 12304, 128), (520, 7168, 128), (700, 11280, 128), (2100, 11520, 128), (2100, 10240, 128),
-         (2100, 8208, 256), (2100, 8192, 128), (2048, 8192, 128)]
+# Dense products by the tile they take on 256 CUs (16 token rows x 16 weight rows): 4x4, 2x4, 1x2, 2x2 and
+# 1x1, with ragged last blocks and, for two m-tiles or more, a grid that is no multiple of 8; then MFMA
+# pieces only (32, 64, 128 and 256 rows), whole tiles with 1, 2, 4 and 8 pieces per tile behind them, and
+# with none.
+TILES = [(64, 12352, 128), (100, 6160, 256), (33, 6208, 128), (160, 2064, 128), (20, 3120, 384), (16, 6160, 256),
+         (33, 3120, 128), (30, 6160, 128), (7, 2064, 640), (130, 12304, 128), (520, 7168, 128), (900, 7184, 128),
+         (700, 11280, 128), (2100, 11520, 128), (2100, 10240, 128), (2100, 8208, 256), (2100, 8192, 128),
+         (2048, 8192, 128)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
