@@ -99,8 +99,8 @@ enum moe_dtype {
  * tiles fill at least one round of compute units, the others on the streaming tiles (no policy
  * table); mxfp4 weights with bf16 activations always stream.  int8 weights in automatic mode use the
  * MFMA tiles, unless a GEMM's would fill less than a fifth of a round and no expert holds more than 64
- * rows, and at most 16 tokens (no shared expert, d_ff <= 4096) stream without a selection; every choice
- * gives the same bits. */
+ * rows; few tokens (up to 16, or 32 over many small experts; no shared expert) stream without a
+ * selection.  Every choice gives the same bits. */
 enum moe_config {
   MOE_CONFIG_AUTO = -1,
   MOE_CONFIG_STREAM = 0, /* weight-streaming tiles: up to 64 of an expert's rows per pass */

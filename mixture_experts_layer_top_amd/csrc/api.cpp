@@ -277,8 +277,10 @@ hipError_t launch_gemms(const SelectOut& o, const moe_problem* p, int gemm, int6
 
 // int8 experts of a small batch: both products without a selection (tok as in Seg).
 bool small_i8(const moe_problem* p) {
-  return is_int8(p) && !p->has_shared && p->config == MOE_CONFIG_AUTO && p->T <= kSmallI8Tokens &&
-         p->d_ff <= kSmallI8MaxK;
+  if (!is_int8(p) || p->has_shared || p->config != MOE_CONFIG_AUTO) return false;
+  if (p->T <= kSmallI8Tokens) return small_i8_lds(p->T * p->top_k, p->d_ff) <= kSmallI8Lds;
+  return p->T <= 2 * kSmallI8Tokens && p->T * p->top_k <= 4 * p->num_experts &&
+         p->d_ff <= kSmallI8WideK;
 }
 SmallI8 small_gate_up(const moe_problem* p, const moe_weights* w, const FfnWs& f, const void* x,
                       const float* xs, const int32_t* counts, const int32_t* offsets,

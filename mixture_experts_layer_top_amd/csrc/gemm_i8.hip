@@ -312,13 +312,14 @@ __global__ __launch_bounds__(256) void gemm_stream_i8_dense(Seg sg) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// small batches: at most kSmallI8Tokens tokens
+// small batches (kernels.h: kSmallI8Tokens)
 //
 // A decode step's experts hold a few rows each, and the launches around the weights' stream weigh as
 // much as a part of it: the selection kernel (one workgroup, 8-10 us) and the rows' quantisation (5 us)
-// beside 40 + 30 us of weights at one token (DeepSeek-V3-shaped layer).  Here every workgroup finds the
-// experts that hold rows by itself, from the counts, and a down tile quantises its expert's rows of h
-// into LDS while its first weights are on their way.  Same tiles, same sums, same bits.
+// beside 37 + 24 us of weights at one token (DeepSeek-V3-shaped layer; 61 us in all, 82 with them).
+// Here every workgroup finds the experts that hold rows by itself, from the counts, and a down tile
+// quantises its expert's rows of h into LDS while its first weights are on their way.  Same tiles, same
+// sums, same bits.
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ void small_list(const int32_t* counts, int E, int (&s_exp)[kSmallI8Rows],
                                            int& s_n) {
@@ -663,14 +664,14 @@ hipError_t launch_gemms_i8(const SelectOut& o, int g, int num_cus, int64_t max_r
 }
 
 hipError_t launch_small_i8(const SmallI8& a, bool gate_up, int num_cus, hipStream_t s) {
-  const size_t lds = gate_up ? 0 : (size_t)std::min(a.rows, 16) * (a.K + 16);
   const int g = num_cus * (gate_up ? 4 : 5);
   if (gate_up) {
     if (a.K >= kStreamSplitK) gemm_small_i8<true, 4><<<g, 256, 0, s>>>(a);
     else gemm_small_i8<true, 2><<<g, 256, 0, s>>>(a);
   } else {
-    if (a.K >= kStreamSplitK) gemm_small_i8<false, 4><<<g, 256, lds, s>>>(a);
-    else gemm_small_i8<false, 1><<<g, 256, lds, s>>>(a);
+    // (64 columns per workgroup whatever K: with 16 and K split over the wavefronts four times as many
+    // quantise the same rows; 64 experts of 4096 x 4096, 8 tokens: 371 us against 526)
+    gemm_small_i8<false, 1><<<g, 256, small_i8_lds(a.rows, a.K), s>>>(a);
   }
   return hipGetLastError();
 }

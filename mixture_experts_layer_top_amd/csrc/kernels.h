@@ -226,11 +226,18 @@ hipError_t launch_quant_act(const void* x, int T, int d, uint8_t* xq, float* xs,
 // the rows' quantisation (bf16, or fp32 when f32; d % 8 == 0, d <= 32768).
 hipError_t launch_gemms_i8(const SelectOut& o, int gemm, int num_cus, int64_t max_rows, bool stream,
                            bool mfma, hipStream_t s);
-// The experts' products of at most kSmallI8Tokens tokens (d_ff <= kSmallI8MaxK), without a selection:
-// gate/up writes fp32 h, down quantises its rows of h itself.
-constexpr int kSmallI8Tokens = 16;  // (an expert then holds one 16-row pass, unless ids repeat)
-constexpr int kSmallI8Rows = kSmallI8Tokens * kMaxTopK;
-constexpr int kSmallI8MaxK = 4096;
+// The experts' products of few tokens, without a selection: gate/up writes fp32 h, down quantises its
+// rows of h itself, every workgroup anew, which costs as much as its weights from some 16 rows.  So at most
+// kSmallI8Tokens tokens whose codes fit kSmallI8Lds bytes of LDS, or twice as many when an expert holds at
+// most 4 rows on average and d_ff <= kSmallI8WideK.  Measured against the lists (us): 64 experts, d 7168,
+// d_ff 2048, k 8: 1 token 60 and 90, 16 365 and 407, 32 449 and 468; d 2048, d_ff 1024: 32 tokens 75
+// and 125; 16 experts of 4096 x 4096, k 8: 1 token 73 and 85, 16 165 and 164, 24 198 and 164; 8 experts,
+// d 4096, d_ff 7168, k 8: 1 token 122 and 139, 8 166 and 140.
+constexpr int kSmallI8Tokens = 16;
+constexpr int kSmallI8Rows = 2 * kSmallI8Tokens * kMaxTopK;
+constexpr int kSmallI8Lds = 66 << 10;
+constexpr int kSmallI8WideK = 2048;
+constexpr int small_i8_lds(int rows, int K) { return (rows < 16 ? rows : 16) * (K + 16); }
 struct SmallI8 {
   const int32_t* counts; const int32_t* offsets;
   const int32_t* tok;                   // row -> row of x (null: itself)

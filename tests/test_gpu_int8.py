@@ -387,11 +387,14 @@ def test_grouped_ffn_in_pieces(moe, counts, d, f):
             slack * (1 + 2.0 ** -7) + np.abs(ref) * (2.0 ** -8 + 2.0 ** -20)).all()
 
 
-# At most 16 tokens: counts, T, k, d, f.  All rows with one expert (a token's ids may repeat), passes of
+# Few tokens: counts, T, k, d, f.  All rows with one expert (a token's ids may repeat), passes of
 # 16 and a tail, a long K in either product, many experts of one row, experts that all hold none.
 SMALL = [([0, 32], 16, 2, 256, 256), ([17, 0, 15], 16, 2, 128, 384), ([0] * 7 + [128], 16, 8, 128, 128),
          ([0, 3, 1, 0, 4], 4, 2, 4224, 256), ([1, 1, 0, 2], 2, 2, 256, 4096), ([1] * 8 + [0] * 56, 1, 8, 256, 128),
-         ([1, 0] * 64, 8, 8, 128, 128), ([0, 0], 16, 1, 128, 128), ([3, 2] + [0] * 6, 16, 8, 128, 256)]
+         ([1, 0] * 64, 8, 8, 128, 128), ([0, 0], 16, 1, 128, 128), ([3, 2] + [0] * 6, 16, 8, 128, 256),
+         # one token and a few of a wide expert; up to 32 tokens over many experts, and all rows with one
+         ([1, 1], 1, 2, 128, 14336), ([0, 3, 1], 4, 1, 256, 14336), ([4] * 64, 32, 8, 128, 256),
+         ([256] + [0] * 63, 32, 8, 128, 128), ([0, 17] * 4 + [0] * 12, 24, 3, 256, 2048)]
 
 
 @pytest.mark.parametrize("counts,T,k,d,f", SMALL, ids=lambda v: str(v).replace(" ", "")[:24])
@@ -482,7 +485,8 @@ def test_layer_of_one_token_in_a_graph(moe):
 
 
 @pytest.mark.parametrize("T,d,f,E,k,sf", [(2, 256, 4096, 16, 2, 0), (9, 384, 256, 64, 8, 0), (16, 256, 384, 9, 8, 0),
-                                          (16, 256, 4224, 4, 2, 0), (17, 256, 256, 9, 8, 0), (16, 256, 256, 4, 2, 128)])
+                                          (16, 256, 4224, 4, 2, 0), (17, 256, 256, 9, 8, 0), (16, 256, 256, 4, 2, 128),
+                                          (32, 256, 384, 64, 8, 0), (24, 128, 2048, 12, 2, 0), (33, 256, 384, 64, 8, 0)])
 def test_layer_around_the_small_path(moe, T, d, f, E, k, sf):
     """Every way through moe_layer at few tokens gives the same bits; a traced call records the phases, and
     neither writes the bf16 selection's outputs."""
