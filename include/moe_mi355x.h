@@ -48,7 +48,10 @@
  *     kernels address rows with 32-bit byte offsets, so moe_layer and moe_grouped_ffn also need
  *     T*k*max(d_model, d_ff, d_ff_shared)*2 < 2^32 and d_model*max(d_ff, d_ff_shared)*2 < 2^32
  *     (every activation, h and y buffer and each expert matrix below 4 GiB); moe_quant_act needs
- *     T*d/128 < 2^31 and moe_permute's gather T*k*d/128 < 2^31.  Outside them: MOE_ERR_UNSUPPORTED.
+ *     T*d/128 < 2^31 and moe_permute's gather T*k*d/128 < 2^31.  moe_quant_act_i8, moe_rmsnorm,
+ *     moe_rmsnorm_grad, moe_route_grad and moe_combine_grad need T < 2^25, moe_permute_grad fewer than
+ *     2^32 threads (d / 8 per token, rounded up to 256 unless a multiple of 64).  Outside them:
+ *     MOE_ERR_UNSUPPORTED.
  *   - Calls are reentrant: no mutable global state (the device's compute-unit count is queried on
  *     every call); concurrent calls need distinct workspaces.  The one exception is
  *     moe_layer_noalloc, whose workspace is a static per-GPU array (see its declaration).

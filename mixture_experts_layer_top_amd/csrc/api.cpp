@@ -66,6 +66,8 @@ bool is_int8(const moe_problem* p) { return p->wdtype == MOE_DTYPE_INT8; }
 // Longest row of the row kernels (norm, int8 rows): a row stays in one workgroup's registers.
 constexpr int kMaxRowLen = 32768;
 constexpr int kMaxRowLenGrad = 16384;  // (the norm's gradient keeps two rows and its share of dw)
+// Rows of a call: a wavefront or more each, and a launch has fewer than 2^32 threads.
+constexpr int kMaxRowCount = 1 << 25;
 
 int check_problem(const moe_problem* p) {
   if (!p) return MOE_ERR_INVALID_ARG;
@@ -526,7 +528,7 @@ int moe_combine(const void* y_perm, const int32_t* slot_dst, const float* topk_w
 
 int moe_quant_act_i8(const void* x, int T, int d, int8_t* xq, float* xs, hipStream_t stream) {
   if (T < 0 || d <= 0) return MOE_ERR_INVALID_ARG;
-  if (d % 16 || d > kMaxRowLen) return MOE_ERR_UNSUPPORTED;
+  if (d % 16 || d > kMaxRowLen || T >= kMaxRowCount) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !xq || !xs || !aligned16(x) || !aligned16(xq)) return MOE_ERR_INVALID_ARG;
   return hip_status(
@@ -558,7 +560,7 @@ int moe_rmsnorm(const void* x, const void* residual, const void* weight, float e
     case MOE_DTYPE_INT8: fmt = 3; step = 16; break;
     default: return MOE_ERR_UNSUPPORTED;
   }
-  if (d % step || d > kMaxRowLen) return MOE_ERR_UNSUPPORTED;
+  if (d % step || d > kMaxRowLen || T >= kMaxRowCount) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !weight) return MOE_ERR_INVALID_ARG;
   if (fmt == 0 ? !y : (!q || !q_scale)) return MOE_ERR_INVALID_ARG;
@@ -569,7 +571,7 @@ int moe_rmsnorm(const void* x, const void* residual, const void* weight, float e
 }
 
 size_t moe_rmsnorm_grad_workspace_bytes(int T, int d) {
-  if (T < 0 || d <= 0 || d % 8 || d > kMaxRowLenGrad) return 0;
+  if (T < 0 || d <= 0 || d % 8 || d > kMaxRowLenGrad || T >= kMaxRowCount) return 0;
   Carver c{nullptr};
   c.take<float>((size_t)rmsnorm_grad_parts(T) * d);
   return c.used;
@@ -579,7 +581,7 @@ int moe_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* 
                      int T, int d, void* dx, float* dweight, void* ws, size_t ws_bytes,
                      hipStream_t stream) {
   if (T < 0 || d <= 0 || !(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
-  if (d % 8 || d > kMaxRowLenGrad) return MOE_ERR_UNSUPPORTED;
+  if (d % 8 || d > kMaxRowLenGrad || T >= kMaxRowCount) return MOE_ERR_UNSUPPORTED;
   if (T == 0 && !dweight) return MOE_OK;
   if (T > 0 && (!dy || !h || !weight || !dx)) return MOE_ERR_INVALID_ARG;
   const void* al[] = {dy, dh, h, weight, dx, dweight};
@@ -597,6 +599,7 @@ int moe_route_grad(const int32_t* topk_ids, const float* topk_w, const float* dt
                    int k, float* dlogits, hipStream_t stream) {
   int st = check_route_shape(T, E, k);
   if (st) return st;
+  if (T >= kMaxRowCount) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!topk_ids || !topk_w || !dtopk_w || !dlogits) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_route_grad(topk_ids, topk_w, dtopk_w, T, E, k, dlogits, stream));
@@ -606,8 +609,7 @@ int moe_combine_grad(const void* dout, const void* y_perm, const int32_t* slot_d
                      const float* topk_w, int T, int k, int d, void* dy_perm, float* dtopk_w,
                      hipStream_t stream) {
   if (T < 0 || k <= 0 || d <= 0) return MOE_ERR_INVALID_ARG;
-  if (k > kMaxTopK || d % 128 || d > kMaxRowLen) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)T * k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (k > kMaxTopK || d % 128 || d > kMaxRowLen || T >= kMaxRowCount) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!dy_perm && !dtopk_w) return MOE_ERR_INVALID_ARG;
   if (!dout || !slot_dst || (dy_perm && !topk_w) || (dtopk_w && !y_perm)) return MOE_ERR_INVALID_ARG;
@@ -623,6 +625,9 @@ int moe_permute_grad(const void* dx_perm, const int32_t* slot_dst, const void* d
   if (T < 0 || k <= 0 || d <= 0) return MOE_ERR_INVALID_ARG;
   if (k > kMaxTopK || d % 128) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)T * k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  const int64_t lanes = d / 8;  // (launch_combine's workgroups)
+  if (T * (lanes % 64 ? (lanes + 255) / 256 * 256 : lanes) >= (int64_t(1) << 32))
+    return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!dx_perm || !slot_dst || !dx) return MOE_ERR_INVALID_ARG;
   if (!aligned16(dx_perm) || !aligned16(dx) || !aligned16(dx_add)) return MOE_ERR_INVALID_ARG;

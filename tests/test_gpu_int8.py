@@ -520,3 +520,16 @@ def test_layer_around_the_small_path(moe, T, d, f, E, k, sf):
         r, sk = R.expert_i8(qn, sn, W.get_shared())
         want, room = want + r, room + sk + np.abs(r) * 2.0 ** -7
     assert (np.abs(f64(out.view(torch.bfloat16)) - want) <= room * 1.01 + np.abs(want) * 2.0 ** -8).all()
+
+
+def test_quant_act_i8_of_the_most_rows(moe):
+    """2^25 - 1 rows: the first and the last are those of a small call."""
+    T = 2 ** 25 - 1
+    few = _bf16(7, 16, seed=9)
+    x = torch.zeros(T, 16, dtype=torch.bfloat16, device="cuda")
+    x[:7], x[-7:] = few, few
+    q, s = moe.quant_act_i8(x)
+    wq, ws = moe.quant_act_i8(few)
+    for part in (slice(0, 7), slice(T - 7, T)):
+        assert torch.equal(q[part], wq) and torch.equal(s[part], ws)
+    assert (s[7:-7] == 1).all() and not q[7:-7].any()

@@ -255,3 +255,21 @@ def test_rmsnorm_grad_weight_by_rows(moe, T):
     assert ((dx.double() - want).abs() <= want.abs() * 2.0 ** -8 + mag * 2.0 ** -19).all()
     terms = dy.double() * hd * rstd
     assert ((dw.double() - terms.sum(0)).abs() <= (T + 60) * 2.0 ** -24 * terms.abs().sum(0)).all()
+
+
+def test_rmsnorm_of_the_most_rows(moe):
+    """2^25 - 1 rows, forward and backward: the first and the last are those of a small call."""
+    T = 2 ** 25 - 1
+    few, g, w = _bf16(7, 8, seed=9), _bf16(7, 8, seed=10), _bf16(8, seed=11)
+    x = torch.zeros(T, 8, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros_like(x)
+    x[:7], x[-7:], dy[:7], dy[-7:] = few, few, g, g
+    y = moe.rmsnorm(x, w, None, EPS)[1]
+    dx, dw = moe.rmsnorm_grad(dy, x, w, None, EPS)
+    want, (wdx, wdw) = moe.rmsnorm(few, w, None, EPS)[1], moe.rmsnorm_grad(g, few, w, None, EPS)
+    for part in (slice(0, 7), slice(T - 7, T)):
+        assert torch.equal(y[part], want) and torch.equal(dx[part], wdx)
+    assert not y[7:-7].any() and not dx[7:-7].any()
+    # (14 rows that are not zero, in some order: twice the small sum within their roundings)
+    n = few.double() * (few.double().square().mean(1, keepdim=True) + EPS).rsqrt()
+    assert ((dw.double() - 2 * wdw.double()).abs() <= 2 * 30 * 2.0 ** -24 * (g.double() * n).abs().sum(0) * 2).all()

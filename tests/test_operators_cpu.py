@@ -165,3 +165,15 @@ def test_binding_refusals():
     assert ew.wdtype == moe.DTYPE_INT8 and ew.struct().layout == moe.LAYOUT_ROW_MAJOR
     g._moe_tiled = True
     assert ew.struct().layout == moe.LAYOUT_TILED
+
+
+def test_more_rows_than_a_launch_has_threads_for(L):
+    T = 1 << 25
+    assert L.moe_quant_act_i8(A, T, 16, A, A, None) == UNS
+    assert L.moe_rmsnorm(A, None, A, 1e-6, T, 8, moe.DTYPE_BF16, None, A, None, None, None) == UNS
+    assert L.moe_rmsnorm_grad(A, None, A, A, 1e-6, T, 8, A, A, A, 1 << 30, None) == UNS
+    assert L.moe_rmsnorm_grad_workspace_bytes(T, 8) == 0 and L.moe_rmsnorm_grad_workspace_bytes(T - 1, 8) > 0
+    assert L.moe_route_grad(A, A, A, T, 8, 2, A, None) == UNS
+    assert L.moe_combine_grad(A, A, A, A, T, 2, 128, A, A, None) == UNS
+    assert L.moe_permute_grad(A, A, None, 1 << 24, 2, 128, A, None) == UNS  # 256 threads each
+    assert L.moe_permute_grad(A, A, None, 1 << 26, 2, 512, A, None) == UNS  # 64 threads each
