@@ -13,7 +13,9 @@
 //  * stream (light experts, small dense products): a workgroup's 4 wavefronts split K over 16 weight
 //    rows (K >= kStreamSplitK) or 32, up to 64 token rows per pass; weights go straight from HBM
 //    into MFMA registers, 1 KB contiguous per load in the tiled layout (moe_fp8_tile).
-//  * mfma (mfma_tile.h): 256 weight rows by 32 to 256 token rows staged through LDS.
+//  * mfma (mfma_tile.h): 256 weight rows by 32 to 256 token rows staged through LDS; dense 4096 x 4096 x
+//    14336 222 us (2.17 POP/s, 0.99 of the library's product; the chip's power limit), 8 experts of
+//    4096 x 14336, 8192 rows 930 + 470 us (2.05).
 #include <algorithm>
 
 #include "common.h"
