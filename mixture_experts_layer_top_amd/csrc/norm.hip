@@ -28,8 +28,8 @@ namespace {
 enum NormFormat { kNormBf16 = 0, kNormFp8 = 1, kNormMx = 2, kNormI8 = 3 };
 
 // Four e4m3 codes in a dword, by the conversion instruction: to nearest, ties to even, the sign kept.
-// It equals e4m3_encode on every float below 464 in magnitude (all of them compared), and the scaled
-// values here are at most 448 (1 + 2^-22).
+// It equals e4m3_encode on values up to 448 in magnitude and does not saturate above 464, so the caller
+// limits its values.
 __device__ __forceinline__ uint32_t e4m3_pack4(const float* v) {
   int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], p, true);
@@ -137,8 +137,9 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
         if (sc == 0.0f || bad) sc = 1.0f;
         if ((idx & 15) == 0) static_cast<float*>(qs)[base / 16 + idx / 16] = sc;
         const Scale f(sc);
+        // (a subnormal scale holds few bits: amax over it may reach 670, and saturates)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = f.div(v[j]);
+        for (int j = 0; j < 8; ++j) v[j] = __builtin_amdgcn_fmed3f(f.div(v[j]), -448.0f, 448.0f);
       } else {
         const int X = bad ? 127 : mx_scale_code(__uint_as_float(m));
         if ((idx & 3) == 0) gstore_u8(static_cast<uint8_t*>(qs), base / 4 + idx / 4, X);

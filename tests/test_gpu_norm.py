@@ -273,3 +273,26 @@ def test_rmsnorm_of_the_most_rows(moe):
     # (14 rows that are not zero, in some order: twice the small sum within their roundings)
     n = few.double() * (few.double().square().mean(1, keepdim=True) + EPS).rsqrt()
     assert ((dw.double() - 2 * wdw.double()).abs() <= 2 * 30 * 2.0 ** -24 * (g.double() * n).abs().sum(0) * 2).all()
+
+
+def test_rmsnorm_e4m3_groups_of_subnormal_scale(moe):
+    """fp32(amax / 448) of a few bits: quotients up to 1.5 * 448 saturate and stay finite.  h is 2^-133 in
+    every column and w whole multiples of 2^-17 * 2^-9, so y is a whole multiple n of 2^-149 (rstd is
+    1000 (1 + 2^-23) at most off, n below 2^11 and away from half steps)."""
+    d = 2048
+    n = np.array([464, 625, 1000, 448, 1100, 300, 671, 1119, 480, 1561, 500, 667, 1343, 2000, 230, 5])
+    unit = 65536 * 1000.0  # y / 2^-149 of w = 1
+    w = torch.from_numpy(n / unit).to(torch.bfloat16).repeat_interleave(128).cuda()
+    x = torch.full((3, d), 2.0 ** -133, dtype=torch.bfloat16, device="cuda")
+    x[1] *= -1
+    exact = np.outer([1, -1, 1], f64(w) * unit)  # (w is rounded: n is only near it)
+    keep = np.abs(np.abs(exact) % 1 - 0.5) > 2.0 ** -10
+    got = np.rint(exact)
+    s = np.repeat(np.rint(np.abs(got).reshape(3, -1, 128).max(-1) / 448.0), 128, 1)
+    s = np.where(s == 0, 2.0 ** 149, s)  # the scale 1, in units
+    _, _, q, qs = moe.rmsnorm(x, w, None, EPS, moe.DTYPE_FP8)
+    assert np.array_equal(np.repeat(f64(qs), 128, 1)[keep], (s * 2.0 ** -149)[keep])
+    want = fp8_e4m3.encode(np.clip(got / s, -448, 448))
+    assert ((q.cpu().numpy() & 0x7F) != 0x7F).all()
+    assert np.array_equal(q.cpu().numpy()[keep], want[keep])
+    assert (want & 0x7F == 0x7E).any()
