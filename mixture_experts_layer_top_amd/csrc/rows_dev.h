@@ -169,11 +169,12 @@ struct Scale {
     s = sc * k;
     r = 1.0f / s;
   }
-  // fp32(v / s): the product by the reciprocal, corrected by its remainder
+  // fp32(v / s): the product by the reciprocal, corrected by its remainder (which is +0 for a zero of
+  // either sign, so the sign is put back)
   __device__ __forceinline__ float div(float v) const {
     v *= k;
     const float q = v * r;
-    return fmaf(fmaf(-q, s, v), r, q);
+    return copysignf(fmaf(fmaf(-q, s, v), r, q), v);
   }
   // v / s rounded to a whole number, ties to even: the rounded product is at most one off, and the
   // remainder, exact in fp32 (a multiple of half an ulp of s, at most s), says so.  (Rounding fp32(v / s)

@@ -296,3 +296,21 @@ def test_rmsnorm_e4m3_groups_of_subnormal_scale(moe):
     assert ((q.cpu().numpy() & 0x7F) != 0x7F).all()
     assert np.array_equal(q.cpu().numpy()[keep], want[keep])
     assert (want & 0x7F == 0x7E).any()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp8"])
+def test_rmsnorm_codes_are_the_quantisers(moe, fmt):
+    """h = +-1 and eps = 0 make rstd exactly 1 and y = +-w in full: the rows and scales of the quantisers on
+    y, bit for bit, for groups of every magnitude that bf16 has."""
+    d = 8192
+    g = torch.Generator().manual_seed(3)
+    mag = torch.linspace(-132, 120, d // 32).repeat_interleave(32)
+    w = (torch.randn(d, generator=g) * torch.exp2(mag)).to(torch.bfloat16).cuda()
+    w[64:96] = 0
+    sign = torch.randint(0, 2, (5, d), generator=g).mul_(2).sub_(1).to(torch.bfloat16).cuda()
+    y = sign * w
+    _, got, q, qs = moe.rmsnorm(sign, w, None, 0.0, ACTS[fmt])
+    assert torch.equal(got, y)
+    quant = moe.quant_act if fmt == "fp8" else moe.quant_act_mx
+    wq, ws = quant(y.view(torch.int16))
+    assert torch.equal(qs, ws) and torch.equal(q, wq)
