@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.h"
+#include "i8_codec.h"
 
 namespace moe {
 
@@ -158,50 +159,6 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m) {
   if (LANES == 16) return reduce16(m, MaxOp{});
   m = max(m, dpp16<0xb1>(m));
   return max(m, dpp16<0x4e>(m));
-}
-
-// A row's (or group's) quantisation scale, prepared for quotients v / s.  k: a power of two that keeps
-// s normal and 1 / s finite.
-struct Scale {
-  float s, r, k;  // s and 1 / s, both times / over k
-  __device__ __forceinline__ explicit Scale(float sc) {
-    k = sc < 0x1p-60f ? 0x1p64f : 1.0f;
-    s = sc * k;
-    r = 1.0f / s;
-  }
-  // fp32(v / s): the product by the reciprocal, corrected by its remainder (which is +0 for a zero of
-  // either sign, so the sign is put back)
-  __device__ __forceinline__ float div(float v) const {
-    v *= k;
-    const float q = v * r;
-    return copysignf(fmaf(fmaf(-q, s, v), r, q), v);
-  }
-  // v / s rounded to a whole number, ties to even: the rounded product is at most one off, and the
-  // remainder, exact in fp32 (a multiple of half an ulp of s, at most s), says so.  (Rounding fp32(v / s)
-  // would not do: amax / 2 over s is 63.4999999, and comes out as 63.5 and then 64.)  A quotient that
-  // is exactly a half step needs an s of few bits, and fp32(amax / 127) of a bf16 amax has few bits only
-  // as a power of two, whose reciprocal is exact, so the product is the tie and rounds to even.
-  __device__ __forceinline__ int whole(float v) const {
-    v *= k;
-    const float n = __builtin_rintf(v * r), e = fmaf(-n, s, v), h = 0.5f * s;
-    return (int)n + (e > h ? 1 : 0) - (e < -h ? 1 : 0);
-  }
-};
-
-// Symmetric int8 rows: s = fp32(amax / 127) (1 when amax is 0 or the quotient underflows to 0; NaN
-// when amax is not finite, so that whatever is multiplied by it shows it).  |v| <= amax keeps the
-// codes in [-127, 127].
-__device__ __forceinline__ float i8_scale(uint32_t amax_bits) {
-  if (amax_bits >= kInfBits) return __uint_as_float(0x7FC00000u);
-  const float s = __uint_as_float(amax_bits) / 127.0f;
-  return s == 0.0f ? 1.0f : s;
-}
-// Four codes in a dword.
-__device__ __forceinline__ uint32_t i8_pack4(const float* v, const Scale& sc) {
-  uint32_t p = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p |= (uint32_t(sc.whole(v[i])) & 0xFFu) << (8 * i);
-  return p;
 }
 
 }  // namespace moe

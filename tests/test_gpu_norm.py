@@ -298,6 +298,26 @@ def test_rmsnorm_e4m3_groups_of_subnormal_scale(moe):
     assert (want & 0x7F == 0x7E).any()
 
 
+def test_rmsnorm_int8_half_steps(moe):
+    """Exact half steps of a scale that is no power of two: 16384 values whose squares sum to 16384 and
+    w = 255 / 128 make y = h w and s = 255 / 128 exactly; h = n + 1/2 rounds to the even side."""
+    d = 16384
+    row = np.zeros(d)
+    row[0] = 127  # 16129; the half steps below bring 203.5, ones and two halves the other 51.5
+    row[1:12] = [0.5, -0.5, 1.5, -1.5, 2.5, -2.5, 3.5, -3.5, 4.5, -4.5, 11.0]
+    left = d - (row ** 2).sum()
+    ones = int(left)
+    row[20:20 + ones] = 1
+    row[4000:4000 + int((left - ones) * 4)] = 0.5
+    assert (row ** 2).sum() == d
+    x = torch.from_numpy(np.stack([row, -row])).to(torch.bfloat16).cuda()
+    w = torch.full((d,), 255 / 128, dtype=torch.bfloat16, device="cuda")
+    _, _, q, qs = moe.rmsnorm(x, w, None, 0.0, moe.DTYPE_INT8)
+    assert (qs == 255 / 128).all()
+    want = np.rint(np.stack([row, -row]))  # (numpy rounds halves to even)
+    assert np.array_equal(f64(q), want)
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "mxfp8"])
 def test_rmsnorm_codes_are_the_quantisers(moe, fmt):
     """h = +-1 and eps = 0 make rstd exactly 1 and y = +-w in full: the rows and scales of the quantisers on

@@ -1,0 +1,72 @@
+"""The library's int8 row codec (csrc/i8_codec.h: the rows of the norm, of the activations and of the
+experts' h) against float64 on the CPU.
+
+An fp32 quotient v / s of at most 2^8 is a half step exactly or at least 2^-26 away from one, so its
+float64 quotient rounds to the right whole number, ties included."""
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "mixture_experts_layer_top_amd", "csrc")
+HARNESS = os.path.join(os.path.dirname(os.path.abspath(__file__)), "i8_encode_harness.cpp")
+HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+
+
+@pytest.fixture(scope="module")
+def codec(tmp_path_factory):
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not available")
+    so = str(tmp_path_factory.mktemp("codec") / "i8_harness.so")
+    subprocess.run([HIPCC, "-x", "hip", "--cuda-host-only", "-O2", "-fPIC", "-shared", f"-I{CSRC}", HARNESS,
+                    "-o", so], check=True, capture_output=True)
+    lib = ctypes.CDLL(so)
+    lib.i8_row_scale.argtypes, lib.i8_row_scale.restype = [ctypes.c_uint32], ctypes.c_float
+    lib.i8_row_codes.argtypes = [ctypes.c_float, ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p]
+
+    def row(v):
+        """(scale, codes) of one row of fp32 values, a multiple of four of them."""
+        v = np.ascontiguousarray(v, np.float32)
+        s = np.float32(lib.i8_row_scale(int(np.abs(v).max().view(np.uint32))))
+        q = np.empty(v.size, np.int8)
+        lib.i8_row_codes(s, v.ctypes.data, v.size // 4, q.ctypes.data)
+        return s, q.astype(np.int64)
+
+    return row
+
+
+def check(codec, v):
+    v = np.asarray(v, np.float32)
+    s, q = codec(v)
+    want_s = np.float32(np.abs(v).max().astype(np.float64) / 127)
+    assert s == (want_s if want_s else np.float32(1))
+    assert np.array_equal(q, np.rint(v.astype(np.float64) / np.float64(s)))
+    return s, q
+
+
+def test_rows_of_every_magnitude(codec):
+    r = np.random.default_rng(1)
+    for e in range(-110, 120, 7):
+        v = (r.normal(size=64) * 2.0 ** e).astype(np.float32)
+        check(codec, v)
+        check(codec, (v.view(np.uint32) & 0xFFFF0000).view(np.float32))  # bf16 values
+    s, q = codec(np.zeros(8, np.float32))
+    assert s == 1 and not q.any()
+
+
+def test_exact_half_steps_round_to_even(codec):
+    """Scales of few bits that are no power of two: s (n + 1/2) is an fp32 value, and 127 s another, so the
+    row holds exact ties while 1 / s is rounded."""
+    v = np.float32(float.fromhex("0x1.01c664p+0"))
+    s, q = codec(np.array([v, v / 2, -v / 2, v / 4], np.float32))
+    assert s * np.float64(127) == v and q.tolist()[:3] == [127, 64, -64]
+    n = np.arange(127)
+    for bits in range(1, 2 ** 10, 2):  # (s (2 n + 1) fits 24 bits)
+        s = np.float32(bits * 2.0 ** -20)
+        half = s.astype(np.float64) * (n + 0.5)
+        row = np.concatenate([[s * 127.0], half, -half, [0]]).astype(np.float32)
+        got, q = check(codec, row)
+        assert got == s and np.array_equal(q[1:128], 2 * ((n + 1) // 2))
