@@ -24,7 +24,7 @@ struct Scale {
     const float q = v * r;
     return copysignf(fmaf(fmaf(-q, s, v), r, q), v);
   }
-  // v / s rounded to a whole number, ties to even: the rounded product is at most one off, and the
+  // v / s rounded to a whole number in [-127, 127], ties to even: the rounded product is at most one off, and the
   // remainder, exact in fp32 (a multiple of half an ulp of s, at most s), says so.  (Rounding fp32(v / s)
   // would not do: amax / 2 over s is 63.4999999, and comes out as 63.5 and then 64.)  A remainder of
   // exactly half of s is a tie, and an odd n then goes to the even side: with 1 / s rounded (s of few bits
@@ -34,13 +34,14 @@ struct Scale {
     const float n = __builtin_rintf(v * r), e = fmaf(-n, s, v), h = 0.5f * s;
     const int i = (int)n;
     const bool off = fabsf(e) > h || (fabsf(e) == h && (i & 1));
-    return i + (off ? (e > 0.0f ? 1 : -1) : 0);
+    const int q = i + (off ? (e > 0.0f ? 1 : -1) : 0);
+    return q > 127 ? 127 : q < -127 ? -127 : q;
   }
 };
 
 // Symmetric int8 rows: s = fp32(amax / 127) (1 when amax is 0 or the quotient underflows to 0; NaN
-// when amax is not finite, so that whatever is multiplied by it shows it).  |v| <= amax keeps the
-// codes in [-127, 127].
+// when amax is not finite, so that whatever is multiplied by it shows it).  |v| <= amax keeps |v| / s
+// below 127 (1 + 2^-23), but for a subnormal s of few bits, where it may reach 190: whole() cuts it at 127.
 __host__ __device__ __forceinline__ float i8_scale(uint32_t amax_bits) {
   if (amax_bits >= 0x7F800000u) return __builtin_bit_cast(float, 0x7FC00000u);
   const float s = __builtin_bit_cast(float, amax_bits) / 127.0f;

@@ -298,6 +298,19 @@ def test_rmsnorm_e4m3_groups_of_subnormal_scale(moe):
     assert (want & 0x7F == 0x7E).any()
 
 
+def test_rmsnorm_int8_rows_of_subnormal_scale(moe):
+    """y of n 2^-149, n up to 150, over a scale of 2^-149: codes are cut at 127 and keep their sign."""
+    n = np.array([150, -150, 128, -140, 127, -120, 3, 0] * 32)
+    x = torch.from_numpy(np.stack([np.sign(n), -np.sign(n)]) * 2.0 ** -133).to(torch.bfloat16).cuda()
+    # (rstd is 1000 to within 2^-23; a step of w is 1/256, so y is near n, away from half steps)
+    w = torch.from_numpy(np.abs(n) / 65536e3).to(torch.bfloat16).cuda()
+    y = np.stack([np.sign(n), -np.sign(n)]) * f64(w) * 65536e3
+    assert (np.abs(np.abs(y) % 1 - 0.5) > 2.0 ** -10).all() and np.rint(np.abs(y)).max() == 150
+    _, _, q, qs = moe.rmsnorm(x, w, None, EPS, moe.DTYPE_INT8)
+    assert (f64(qs) == 2.0 ** -149).all()
+    assert np.array_equal(f64(q), np.clip(np.rint(y), -127, 127))
+
+
 def test_rmsnorm_int8_half_steps(moe):
     """Exact half steps of a scale that is no power of two: 16384 values whose squares sum to 16384 and
     w = 255 / 128 make y = h w and s = 255 / 128 exactly; h = n + 1/2 rounds to the even side."""

@@ -70,3 +70,13 @@ def test_exact_half_steps_round_to_even(codec):
         row = np.concatenate([[s * 127.0], half, -half, [0]]).astype(np.float32)
         got, q = check(codec, row)
         assert got == s and np.array_equal(q[1:128], 2 * ((n + 1) // 2))
+
+
+def test_subnormal_scales_cut_codes_at_127(codec):
+    """A subnormal fp32(amax / 127) has few bits: amax over it may reach 190, and its code is +-127."""
+    for n in (1, 2, 63, 64, 65, 100, 127, 128, 150, 190, 191, 253, 254, 255, 318, 500, 700, 1000, 2 ** 14 + 1, 2 ** 20 + 3):
+        v = np.array([n, -n, n // 2, -(n // 3)]) * 2.0 ** -149
+        s, q = codec(v)
+        want_s = np.float32(n * 2.0 ** -149 / 127)
+        assert s == (want_s if want_s else np.float32(1))
+        assert np.array_equal(q, np.clip(np.rint(v / np.float64(s)), -127, 127)), n
