@@ -298,10 +298,10 @@ int moe_layer_noalloc(const moe_problem* p, const float* logits, const void* x,
                       hipStream_t stream);
 
 /* int8 activation quantisation (MOE_DTYPE_INT8): per token, s = fp32(amax / 127) (s = 1 when amax is 0
- * or the quotient underflows to 0), q = round(x / s), ties to even, at most 127 in magnitude (fp32 rows,
- * the norm's and h's, whose s is subnormal may exceed it and are cut).  A row holding an infinity or
- * NaN gets s = NaN and zero codes, so whatever is computed from it is NaN.  Also for weights at load
- * time: rows [N][K] -> per-channel codes and scales.
+ * or the quotient underflows to 0; the next float up where amax / s would round past 127, which only a
+ * subnormal s of an fp32 row does: the norm's or h's), q = round(x / s), ties to even, in [-127, 127].  A
+ * row holding an infinity or NaN gets s = NaN and zero codes, so whatever is computed from it is NaN.
+ * Also for weights at load time: rows [N][K] -> per-channel codes and scales.
  *   x [T][d] bf16 -> xq [T][d] int8, xs [T] fp32.  d % 16 == 0, d <= 32768; x, xq 16-byte aligned. */
 int moe_quant_act_i8(const void* x, int T, int d, int8_t* xq, float* xs, hipStream_t stream);
 

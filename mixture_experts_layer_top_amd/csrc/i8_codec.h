@@ -24,35 +24,52 @@ struct Scale {
     const float q = v * r;
     return copysignf(fmaf(fmaf(-q, s, v), r, q), v);
   }
-  // v / s rounded to a whole number in [-127, 127], ties to even: the rounded product is at most one off, and the
-  // remainder, exact in fp32 (a multiple of half an ulp of s, at most s), says so.  (Rounding fp32(v / s)
-  // would not do: amax / 2 over s is 63.4999999, and comes out as 63.5 and then 64.)  A remainder of
-  // exactly half of s is a tie, and an odd n then goes to the even side: with 1 / s rounded (s of few bits
-  // but no power of two) the product may lie on either side of it.
+  // v / s rounded to a whole number, ties to even, |v| / s < 127.5: the rounded product is at most one off,
+  // and the remainder, exact in fp32 (a multiple of half an ulp of s, at most s), says so.  (Rounding
+  // fp32(v / s) would not do: amax / 2 over s is 63.4999999, and comes out as 63.5 and then 64.)  A
+  // remainder of exactly half of s is a tie, and an odd n then goes to the even side: with 1 / s rounded
+  // (s of few bits but no power of two) the product may lie on either side of it.
   __host__ __device__ __forceinline__ int whole(float v) const {
     v *= k;
     const float n = __builtin_rintf(v * r), e = fmaf(-n, s, v), h = 0.5f * s;
     const int i = (int)n;
     const bool off = fabsf(e) > h || (fabsf(e) == h && (i & 1));
-    const int q = i + (off ? (e > 0.0f ? 1 : -1) : 0);
-    return q > 127 ? 127 : q < -127 ? -127 : q;
+    return i + (off ? (e > 0.0f ? 1 : -1) : 0);
   }
 };
 
 // Symmetric int8 rows: s = fp32(amax / 127) (1 when amax is 0 or the quotient underflows to 0; NaN
-// when amax is not finite, so that whatever is multiplied by it shows it).  |v| <= amax keeps |v| / s
-// below 127 (1 + 2^-23), but for a subnormal s of few bits, where it may reach 190: whole() cuts it at 127.
+// when amax is not finite, so that whatever is multiplied by it shows it).  A subnormal s has few bits, and
+// amax over it may reach 190: where it would round past 127, s is the next float up.  So |v| <= amax keeps
+// |v| / s below 127.5 and the codes in [-127, 127].
 __host__ __device__ __forceinline__ float i8_scale(uint32_t amax_bits) {
   if (amax_bits >= 0x7F800000u) return __builtin_bit_cast(float, 0x7FC00000u);
-  const float s = __builtin_bit_cast(float, amax_bits) / 127.0f;
-  return s == 0.0f ? 1.0f : s;
+  const float amax = __builtin_bit_cast(float, amax_bits), s = amax / 127.0f;
+  if (s >= 0x1p-126f) return s;
+  if (s == 0.0f) return 1.0f;
+  return fmaf(s * 0x1p64f, 127.5f, -amax * 0x1p64f) > 0.0f
+             ? s
+             : __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, s) + 1);
 }
-// Four codes in a dword.
+// Four codes in a dword.  v * r is within 127.5 * 2^-24 of v / s, so its nearest whole number is the code
+// unless it lies within 2^-15 of a half step; then all four are found from their remainders.  (That
+// for every value: the norm of 4096 rows of 4096 22.9 us against 18.4, of 16 rows of 7168 5.2 against 4.3, the
+// down product of one token, which quantises h, 25.8 against 23.9.)
 __host__ __device__ __forceinline__ uint32_t i8_pack4(const float* v, const Scale& sc) {
-  uint32_t p = 0;
+  constexpr float kWhole = 0x1.8p23f;  // added, it leaves whole numbers: the sum's low byte is the code
+  uint32_t c[4];
+  float far = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) p |= (uint32_t(sc.whole(v[i])) & 0xFFu) << (8 * i);
-  return p;
+  for (int i = 0; i < 4; ++i) {
+    const float a = v[i] * sc.k, t = fmaf(a, sc.r, kWhole);
+    c[i] = __builtin_bit_cast(uint32_t, t);
+    far = fmaxf(far, fabsf(fmaf(a, sc.r, kWhole - t)));
+  }
+  if (far > 0.5f - 0x1p-15f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = (uint32_t)sc.whole(v[i]);
+  }
+  return (c[0] & 0xFFu) | (c[1] & 0xFFu) << 8 | (c[2] & 0xFFu) << 16 | c[3] << 24;
 }
 
 }  // namespace moe

@@ -5,8 +5,8 @@ TEST INFRASTRUCTURE ONLY (see oracle/__init__.py).  Plain numpy from the formula
 
   norm      n = h / sqrt(mean(h^2) + eps), y = n * w.  With g = dy * w, the gradient of sum(dy * y):
             dh = (g - n * mean(g * n)) / sqrt(mean(h^2) + eps), dw = sum over rows of dy * n.
-  int8 rows s = fp32(amax / 127) per row (1 when amax = 0 or the quotient underflows), q = round(v / s),
-            at most 127 in magnitude (a subnormal s of few bits makes amax / s larger).
+  int8 rows s = fp32(amax / 127) per row (1 when amax = 0 or the quotient underflows; the next fp32
+            up where amax / s would round past 127, s being subnormal), q = round(v / s).
   experts   h = silu(g) * u with g, u = (q_x s_x) (q_w s_w)^T; h's rows quantised as above; then the
             down product.  `slack` bounds what a code of h one step aside can do to y: codes whose
             exact quotient lies within `near` of a half step may round either way in fp32.
@@ -31,9 +31,11 @@ def rmsnorm_grad(dy, h, w, eps):
 def quant_i8(v):
     """Codes (float64 whole numbers) and the fp32 scales of rows, as float64."""
     v = np.asarray(v, np.float64)
-    s = (np.abs(v).max(-1) / 127.0).astype(np.float32)
+    amax = np.abs(v).max(-1)
+    s = (amax / 127.0).astype(np.float32)
+    s = np.where((s > 0) & (amax >= 127.5 * s.astype(np.float64)), np.nextafter(s, np.float32(np.inf)), s)
     s = np.where(s == 0, np.float32(1), s).astype(np.float64)
-    return np.clip(np.rint(v / s[..., None]), -127, 127), s
+    return np.rint(v / s[..., None]), s
 
 
 def gemm_i8(xq, xs, wq, ws):

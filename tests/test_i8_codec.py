@@ -72,11 +72,28 @@ def test_exact_half_steps_round_to_even(codec):
         assert got == s and np.array_equal(q[1:128], 2 * ((n + 1) // 2))
 
 
-def test_subnormal_scales_cut_codes_at_127(codec):
-    """A subnormal fp32(amax / 127) has few bits: amax over it may reach 190, and its code is +-127."""
-    for n in (1, 2, 63, 64, 65, 100, 127, 128, 150, 190, 191, 253, 254, 255, 318, 500, 700, 1000, 2 ** 14 + 1, 2 ** 20 + 3):
+def test_subnormal_scales(codec):
+    """A subnormal fp32(amax / 127) has few bits, and amax over it may reach 190: the next float up then."""
+    for n in [*range(1, 700), 1000, 16129, 2 ** 14 + 1, 2 ** 20 + 3]:
         v = np.array([n, -n, n // 2, -(n // 3)]) * 2.0 ** -149
         s, q = codec(v)
-        want_s = np.float32(n * 2.0 ** -149 / 127)
-        assert s == (want_s if want_s else np.float32(1))
-        assert np.array_equal(q, np.clip(np.rint(v / np.float64(s)), -127, 127)), n
+        u = n // 127 + (2 * (n % 127) > 127)  # round(n / 127), which is no half step
+        u += u > 0 and 2 * n >= 255 * u
+        assert s == (np.float32(u * 2.0 ** -149) if u else 1)
+        assert np.array_equal(q, np.rint(v / np.float64(s))) and np.abs(q).max() <= 127, n
+
+
+def test_codes_near_half_steps(codec):
+    """The floats next to every half step, for scales of all bits: the short way of four codes must not take
+    one of them."""
+    r = np.random.default_rng(2)
+    for e in (-140, -100, -40, 0, 60, 110):
+        for _ in range(50):
+            s = np.float32((1 + r.random()) * 2.0 ** e)
+            top = np.float32(s.astype(np.float64) * 127)
+            got, _ = codec(np.full(4, top))
+            half = (got.astype(np.float64) * (np.arange(127) + 0.5)).astype(np.float32)
+            row = np.concatenate([half, np.nextafter(half, np.float32(0)), np.nextafter(half, np.float32(np.inf))])
+            row = row[np.abs(row) <= top]
+            row = np.concatenate([row, -row, np.full(4, top)])
+            s2, q = check(codec, row[:row.size // 4 * 4] if row.size % 4 else row)
