@@ -314,7 +314,7 @@ int moe_gemm_i8(const int8_t* xq, const float* xs, int M, const int8_t* wq, cons
                 int K, void* y, hipStream_t stream);
 
 /* RMS norm in front of the layer: h = bf16(x + residual) (h = x when residual is NULL),
- * y = h / sqrt(mean(h^2) + eps) * weight, in fp32 (the sum of squares in fp64).
+ * y = h / sqrt(mean(h^2) + eps) * weight, in fp32 (squares that leave fp32's range in fp64).
  *   x, residual [T][d] bf16, weight [d] bf16, eps >= 0.
  *   h_out [T][d] bf16 or NULL: the new residual stream; it may be x or residual itself.
  *   y [T][d] bf16 (may be NULL when there is an 8-bit output).
@@ -323,9 +323,9 @@ int moe_gemm_i8(const int8_t* xq, const float* xs, int M, const int8_t* wq, cons
  *   scales [T][d/128] (d % 128 == 0); MOE_DTYPE_MXFP4_A8 e4m3 with E8M0 scales [T][d/32] (d % 32 == 0);
  *   MOE_DTYPE_INT8 int8 with fp32 scales [T] (d % 16 == 0) -- each by the rules of moe_quant_act,
  *   moe_quant_act_mx and moe_quant_act_i8.
- * d % 8 == 0 and d <= 32768, else MOE_ERR_UNSUPPORTED; pointers 16-byte aligned.  A row whose sum of
- * squares is not finite (an infinity or NaN in it, or |h| above about 2^60) gives NaN in all of its y,
- * NaN codes (e4m3) or a NaN scale (int8); other rows are not affected. */
+ * d % 8 == 0 and d <= 32768, else MOE_ERR_UNSUPPORTED; pointers 16-byte aligned.  A row that holds an
+ * infinity or NaN gives NaN in all of its y, NaN codes (e4m3) or a NaN scale (int8), and so does a zero
+ * row with eps = 0; other rows are not affected. */
 int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int T, int d,
                 int act_dtype, void* h_out, void* y, void* q, void* q_scale, hipStream_t stream);
 

@@ -11,8 +11,8 @@
 //
 // All of it is bound by HBM: a row is read once into registers, both passes over it (the sum of
 // squares, then the scaling) run from there, and the 8-bit output costs no second read of y.  The
-// sum of squares is held in fp64 across a row: the terms are exact in fp32 and the chip's fp64 rate
-// is far above what the memory asks for.  Forward with a residual and e4m3 rows: 8192 x 7168 98 us (5.4
+// sum of squares is held in fp64 across a row, over fp32 chains of eight; a row whose squares leave
+// fp32's range (row_rstd) is summed again in fp64 from its registers.  Forward with a residual and e4m3 rows: 8192 x 7168 98 us (5.4
 // TB/s, a copy's rate), 1 x 7168 3.3 us.
 #include <algorithm>
 #include <type_traits>
@@ -35,18 +35,38 @@ __device__ __forceinline__ uint32_t e4m3_pack4(const float* v) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], p, true);
 }
 
-// 1 / sqrt(sum / d + eps); NaN when the sum of squares is not finite (an infinity or NaN in the
-// row), so that the whole row shows it.
-__device__ __forceinline__ float row_rstd(double sum, double inv_d, float eps) {
+// A vector through an opaque move (computations on it stay where they are written).
+__device__ __forceinline__ uint4 opaque(uint4 v) {
+  asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+  return v;
+}
+
+// Whether fp32 held the squares of a row: its mean square (with eps) is finite and so far above
+// the smallest float that what underflowed does not count (2^-149 a term against 2^-100).
+__device__ __forceinline__ bool row_in_range(double sum, double inv_d, float eps) {
   const float m = float(sum * inv_d) + eps;
-  return m < __uint_as_float(kInfBits) ? 1.0f / sqrtf(m) : __uint_as_float(0x7FC00000u);
+  return m >= 0x1p-100f && m < __uint_as_float(kInfBits);
+}
+// 1 / sqrt(sum / d + eps) of a row in range.
+__device__ __forceinline__ float row_rstd(double sum, double inv_d, float eps) {
+  return 1.0f / sqrtf(float(sum * inv_d) + eps);
+}
+// The same of any row, from squares summed in fp64 (which bf16's never leave): for a small row the value
+// over 2^32, which kSmallRow times the row's values make good; NaN for a row that holds an infinity or
+// NaN, so that the whole row shows it (and for a zero row without eps, 0 / 0).
+constexpr float kSmallRow = 0x1p32f;
+__device__ __forceinline__ float wide_rstd(double sum, double inv_d, float eps, bool& small) {
+  const double m = sum * inv_d + (double)eps;
+  small = m < 1.0;
+  if (!(m < __builtin_inf())) return __uint_as_float(0x7FC00000u);
+  return small ? 0x1p68f / sqrtf(float(m * 0x1p200)) : 0x1p-100f / sqrtf(float(m * 0x1p-200));
 }
 
 template <int FMT, int R, int V>
 __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
     const void* x, const void* res, const void* __restrict__ w, float eps, double inv_d, int T,
     int nvec, void* h_out, void* y, uint8_t* q, void* qs) {
-  __shared__ double red[R / 64];
+  __shared__ double red[2][R / 64];
   __shared__ uint32_t redm[R / 64];
   const int row = R == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (R == 64 && row >= T) return;  // (whole wavefronts; no barrier in this form)
@@ -83,8 +103,36 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
       sum[0] += (double)p;
     }
   }
-  row_reduce<R>(sum, red, SumOp{});
-  const float rstd = row_rstd(sum[0], inv_d, eps);
+  row_reduce<R>(sum, red[0], SumOp{});
+  float rstd = row_rstd(sum[0], inv_d, eps);
+  if (!row_in_range(sum[0], inv_d, eps)) {  // (the same in all threads of the row)
+    sum[0] = 0.0;
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      // (unpacked anew, one vector's doubles at a time: this path must not cost the other registers)
+      __builtin_amdgcn_sched_barrier(0);
+      float h[8];
+      unpack8(opaque(hv[s]), h);
+      if (i + R * s < nvec) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[0] = fma((double)h[j], (double)h[j], sum[0]);
+      }
+    }
+    row_reduce<R>(sum, red[1], SumOp{});
+    bool small;
+    rstd = wide_rstd(sum[0], inv_d, eps, small);
+    if (small) {  // (exact: the values are below 2^-42)
+#pragma unroll
+      for (int s = 0; s < V; ++s) {
+        __builtin_amdgcn_sched_barrier(0);
+        float h[8];
+        unpack8(opaque(hv[s]), h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] *= kSmallRow;
+        hv[s] = pack8(h);
+      }
+    }
+  }
   auto yvec = [&](int s, float (&v)[8]) {
     float wv[8];
     unpack8(wr[s], wv);
@@ -274,7 +322,8 @@ __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
     }
     // (two buffers in turn: a wavefront that is a row ahead writes the other one)
     row_reduce<R>(sum, red[turn], SumOp{});
-    const float rstd = row_rstd(sum[0], inv_d, eps);
+    const float m = float(sum[0] * inv_d) + eps;
+    const float rstd = m < __uint_as_float(kInfBits) ? 1.0f / sqrtf(m) : __uint_as_float(0x7FC00000u);
     const float c = float(sum[1] * inv_d) * rstd * rstd;
 #pragma unroll
     for (int s = 0; s < V; ++s) {

@@ -348,3 +348,37 @@ def test_rmsnorm_codes_are_the_quantisers(moe, fmt):
     quant = moe.quant_act if fmt == "fp8" else moe.quant_act_mx
     wq, ws = quant(y.view(torch.int16))
     assert torch.equal(qs, ws) and torch.equal(q, wq)
+
+
+RANGE = [(2.0 ** -133, 0.0), (1e-38, 0.0), (1e-30, 0.0), (1e-23, 0.0), (1e-20, 1e-44), (1e-19, 1e-38), (1e-12, 0.0),
+         (1e18, EPS), (1e20, EPS), (1e30, 0.0), (5e37, EPS)]
+
+
+@pytest.mark.parametrize("scale,eps", RANGE, ids=str)
+@pytest.mark.parametrize("d", [256, 4224, 16384])
+def test_rmsnorm_of_every_magnitude(moe, d, scale, eps):
+    """Squares below and above fp32's range, without eps or with one as small: y is still h / rms * w to
+    within 2^-20, or half a step of the smallest float, before it is rounded."""
+    x64 = np.random.default_rng(d).normal(size=(5, d)) * scale
+    x = torch.from_numpy(x64).to(torch.bfloat16).cuda()
+    x[3, 5:] = x[1, 5:]  # (a row that shares most of another's values)
+    x[4] = 1  # an ordinary row beside them
+    w = _bf16(d, seed=d)
+    ref = R.rmsnorm(f64(x), f64(w), float(np.float32(eps)))
+    for act in ACTS.values():
+        h, y, q, qs = moe.rmsnorm(x, w, None, eps, act)
+        assert torch.equal(h, x)
+        assert (np.abs(f64(y) - ref) <= np.abs(ref) * (2.0 ** -8 + Y) + 2.0 ** -134).all()
+        if act != moe.DTYPE_BF16:
+            v, s = values(moe, act, q, qs, d)
+            step = s / 2 if act == moe.DTYPE_INT8 else np.maximum(np.abs(ref) * 2.0 ** -4, s * 2.0 ** -10)
+            assert (np.abs(v - ref) <= step + np.abs(ref) * 2 * Y).all()
+
+
+def test_rmsnorm_zero_row_without_eps(moe):
+    """0 / 0, in that row alone."""
+    x, w = _bf16(3, 384, seed=1), _bf16(384, seed=2)
+    clean = moe.rmsnorm(x, w, None, 0.0)[1]
+    x[1] = 0
+    y = moe.rmsnorm(x, w, None, 0.0)[1]
+    assert y[1].isnan().all() and torch.equal(y[[0, 2]], clean[[0, 2]])
