@@ -51,25 +51,28 @@ __host__ __device__ __forceinline__ float i8_scale(uint32_t amax_bits) {
              ? s
              : __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, s) + 1);
 }
-// Four codes in a dword.  v * r is within 127.5 * 2^-24 of v / s, so its nearest whole number is the code
-// unless it lies within 2^-15 of a half step; then all four are found from their remainders.  (That
-// for every value: the norm of 4096 rows of 4096 22.9 us against 18.4, of 16 rows of 7168 5.2 against 4.3, the
+// 4 N codes, four in a dword.  v * r is within 127.5 * 2^-24 of v / s, so its nearest whole number is the
+// code unless it lies within 2^-16 of a half step; then all of them are found from their remainders.  (That for
+// every value: the norm of 4096 rows of 4096 22.9 us against 18.4, of 16 rows of 7168 5.2 against 4.3, the
 // down product of one token, which quantises h, 25.8 against 23.9.)
-__host__ __device__ __forceinline__ uint32_t i8_pack4(const float* v, const Scale& sc) {
+template <int N>
+__host__ __device__ __forceinline__ void i8_pack(const float* v, const Scale& sc, uint32_t* out) {
   constexpr float kWhole = 0x1.8p23f;  // added, it leaves whole numbers: the sum's low byte is the code
-  uint32_t c[4];
+  uint32_t c[4 * N];
   float far = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4 * N; ++i) {
     const float a = v[i] * sc.k, t = fmaf(a, sc.r, kWhole);
     c[i] = __builtin_bit_cast(uint32_t, t);
     far = fmaxf(far, fabsf(fmaf(a, sc.r, kWhole - t)));
   }
-  if (far > 0.5f - 0x1p-15f) {
+  if (far > 0.5f - 0x1p-16f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = (uint32_t)sc.whole(v[i]);
+    for (int i = 0; i < 4 * N; ++i) c[i] = (uint32_t)sc.whole(v[i]);
   }
-  return (c[0] & 0xFFu) | (c[1] & 0xFFu) << 8 | (c[2] & 0xFFu) << 16 | c[3] << 24;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    out[i] = (c[4 * i] & 0xFFu) | (c[4 * i + 1] & 0xFFu) << 8 | (c[4 * i + 2] & 0xFFu) << 16 | c[4 * i + 3] << 24;
 }
 
 }  // namespace moe

@@ -176,7 +176,9 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
     if (FMT == kNormI8) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = bad_row ? 0.f : v[j];
-      st8(q, (base + idx) * 8, i8_pack4(v, row_scale), i8_pack4(v + 4, row_scale));
+      uint32_t c[2];
+      i8_pack<2>(v, row_scale, c);
+      st8(q, (base + idx) * 8, c[0], c[1]);
     }
     if (FMT == kNormFp8 || FMT == kNormMx) {
       const bool bad = m >= kInfBits;
@@ -255,8 +257,10 @@ __global__ __launch_bounds__(row_block(R)) void quant_i8_kernel(const void* __re
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] = bad ? 0.f : v[j];
     const size_t at = (base + i + R * s) * N;
-    if constexpr (F32) gstore4(q, at, i8_pack4(v, f));
-    else st8(q, at, i8_pack4(v, f), i8_pack4(v + 4, f));
+    uint32_t c[N / 4];
+    i8_pack<N / 4>(v, f, c);
+    if constexpr (F32) gstore4(q, at, c[0]);
+    else st8(q, at, c[0], c[1]);
   }
 }
 
