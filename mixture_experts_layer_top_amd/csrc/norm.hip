@@ -62,6 +62,32 @@ __device__ __forceinline__ float wide_rstd(double sum, double inv_d, float eps, 
   return small ? 0x1p68f / sqrtf(float(m * 0x1p200)) : 0x1p-100f / sqrtf(float(m * 0x1p-200));
 }
 
+// The wide sums of a row out of range, two values at a time in a loop, and its values times kSmallRow
+// (exact: a small row's are below 2^-42): a path that must not cost the other one registers.
+__device__ __forceinline__ float bf16_lo(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
+__device__ __forceinline__ uint4 turned(const uint4& v) { return make_uint4(v.y, v.z, v.w, v.x); }
+__device__ __forceinline__ void add_squares(uint4 h, double& sum) {
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j, h = turned(h)) {
+    const double a = bf16_lo(h.x), b = bf16_hi(h.x);
+    sum = fma(b, b, fma(a, a, sum));
+  }
+}
+__device__ __forceinline__ void add_products(uint4 h, uint4 g, uint4 w, double& sum) {
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j, h = turned(h), g = turned(g), w = turned(w)) {
+    sum = fma((double)bf16_lo(g.x) * (double)bf16_lo(w.x), (double)bf16_lo(h.x), sum);
+    sum = fma((double)bf16_hi(g.x) * (double)bf16_hi(w.x), (double)bf16_hi(h.x), sum);
+  }
+}
+__device__ __forceinline__ uint4 enlarged(uint4 h) {
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j, h = turned(h))
+    h.x = pack_bf16x2(bf16_lo(h.x) * kSmallRow, bf16_hi(h.x) * kSmallRow);
+  return h;
+}
+
 template <int FMT, int R, int V>
 __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
     const void* x, const void* res, const void* __restrict__ w, float eps, double inv_d, int T,
@@ -108,29 +134,14 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
   if (!row_in_range(sum[0], inv_d, eps)) {  // (the same in all threads of the row)
     sum[0] = 0.0;
 #pragma unroll
-    for (int s = 0; s < V; ++s) {
-      // (unpacked anew, one vector's doubles at a time: this path must not cost the other registers)
-      __builtin_amdgcn_sched_barrier(0);
-      float h[8];
-      unpack8(opaque(hv[s]), h);
-      if (i + R * s < nvec) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[0] = fma((double)h[j], (double)h[j], sum[0]);
-      }
-    }
+    for (int s = 0; s < V; ++s)
+      if (i + R * s < nvec) add_squares(hv[s], sum[0]);
     row_reduce<R>(sum, red[1], SumOp{});
     bool small;
     rstd = wide_rstd(sum[0], inv_d, eps, small);
-    if (small) {  // (exact: the values are below 2^-42)
+    if (small) {
 #pragma unroll
-      for (int s = 0; s < V; ++s) {
-        __builtin_amdgcn_sched_barrier(0);
-        float h[8];
-        unpack8(opaque(hv[s]), h);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] *= kSmallRow;
-        hv[s] = pack8(h);
-      }
+      for (int s = 0; s < V; ++s) hv[s] = enlarged(hv[s]);
     }
   }
   auto yvec = [&](int s, float (&v)[8]) {
@@ -274,7 +285,7 @@ template <int R, int V>
 __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
     const void* dy, const void* dh, const void* h, const void* __restrict__ w, float eps,
     double inv_d, int T, int nvec, void* dx, float* __restrict__ part) {
-  __shared__ double red[2][2 * R / 64];
+  __shared__ double red[4][2 * R / 64];
   const int i = threadIdx.x;
   float dw[V][8];
 #pragma unroll
@@ -326,9 +337,36 @@ __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
     }
     // (two buffers in turn: a wavefront that is a row ahead writes the other one)
     row_reduce<R>(sum, red[turn], SumOp{});
-    const float m = float(sum[0] * inv_d) + eps;
-    const float rstd = m < __uint_as_float(kInfBits) ? 1.0f / sqrtf(m) : __uint_as_float(0x7FC00000u);
-    const float c = float(sum[1] * inv_d) * rstd * rstd;
+    // (unpacked anew behind the sums: values kept across the branch below would take a third more
+    // registers, and with up to three vectors a wavefront's place)
+#pragma unroll
+    for (int s = 0; s < V && V < 4; ++s) {
+      cur.h[s] = opaque(cur.h[s]);
+      cur.g[s] = opaque(cur.g[s]);
+      wr[s] = opaque(wr[s]);
+    }
+    float rstd = row_rstd(sum[0], inv_d, eps);
+    float c = float(sum[1] * inv_d) * rstd * rstd;
+    float up = 1.0f;
+    if (!row_in_range(sum[0], inv_d, eps) || !(fabs(sum[1]) < __builtin_inf())) {
+      // (the row's sums in fp64, as in the forward kernel; the same in all threads)
+      sum[0] = sum[1] = 0.0;
+#pragma unroll
+      for (int s = 0; s < V; ++s) {
+        if (i + R * s >= nvec) continue;
+        add_squares(cur.h[s], sum[0]);
+        add_products(cur.h[s], cur.g[s], wr[s], sum[1]);
+      }
+      row_reduce<R>(sum, red[2 + turn], SumOp{});
+      bool small;
+      rstd = wide_rstd(sum[0], inv_d, eps, small);
+      if (small) {
+        up = kSmallRow;
+#pragma unroll
+        for (int s = 0; s < V; ++s) cur.h[s] = enlarged(cur.h[s]);
+      }
+      c = float(sum[1] * inv_d * (double)up * (double)rstd * (double)rstd);
+    }
 #pragma unroll
     for (int s = 0; s < V; ++s) {
       float a[8], g[8], wv[8], add[8], o[8];
@@ -339,7 +377,7 @@ __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[s][j] = fmaf(g[j], a[j] * rstd, dw[s][j]);
-        o[j] = rstd * fmaf(-c, a[j], g[j] * wv[j]);
+        o[j] = rstd * fmaf(-c, a[j], g[j] * wv[j]) * up;
         if (dh) o[j] += add[j];
       }
       if (i + R * s < nvec) st16(dx, (size_t)row * nvec + i + R * s, pack8(o));

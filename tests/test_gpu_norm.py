@@ -382,3 +382,40 @@ def test_rmsnorm_zero_row_without_eps(moe):
     x[1] = 0
     y = moe.rmsnorm(x, w, None, 0.0)[1]
     assert y[1].isnan().all() and torch.equal(y[[0, 2]], clean[[0, 2]])
+
+
+@pytest.mark.parametrize("scale,eps", RANGE, ids=str)
+@pytest.mark.parametrize("d", [256, 4104, 16384])
+def test_rmsnorm_grad_of_every_magnitude(moe, d, scale, eps):
+    """The gradient of such rows: the tolerances of ordinary ones, and half a step of bf16's smallest value
+    (and of fp32's, times n's magnitude, inside)."""
+    T = 5
+    x64 = np.random.default_rng(d).normal(size=(T, d)) * scale
+    h = torch.from_numpy(x64).to(torch.bfloat16).cuda()
+    h[4] = _bf16(d, seed=7)  # an ordinary row beside them
+    w = _bf16(d, seed=d)
+    # (so that dx is a bf16 number: dy / scale)
+    dy, dh = _bf16(T, d, seed=1, std=1e-3 if scale < 1 else 1e3), _bf16(T, d, seed=2, std=1e-3)
+    eps = float(np.float32(eps))
+    dx, dw = moe.rmsnorm_grad(dy, h, w, dh, eps)
+    dy64, h64, w64 = f64(dy), f64(h), f64(w)
+    ref, refw = R.rmsnorm_grad(dy64, h64, w64, eps)
+    r = 1 / np.sqrt((h64 ** 2).mean(-1, keepdims=True) + eps)
+    g, n = dy64 * w64, h64 * r
+    terms = r * (np.abs(g) + np.abs(n) * np.abs(g * n).mean(-1, keepdims=True)) + np.abs(f64(dh))
+    ref = ref + f64(dh)
+    assert (np.abs(f64(dx) - ref) <= np.abs(ref) * 2.0 ** -8 + terms * 2 * Y + 2.0 ** -133).all()
+    assert (np.abs(f64(dw) - refw) <= (1 + 16 + 32 + 14) * 2.0 ** -24 * np.abs(dy64 * n).sum(0)).all()
+
+
+def test_rmsnorm_grad_of_non_finite_rows(moe):
+    """An infinity or NaN in h makes its row of dx NaN; an infinite dy makes mean(g n) infinite and so its
+    row of dx, g - n mean(g n), infinite or (at its own place) NaN.  The other rows are left."""
+    T, d = 6, 4104
+    h, dy, w = _bf16(T, d, seed=1), _bf16(T, d, seed=2), _bf16(d, seed=3)
+    want, _ = moe.rmsnorm_grad(dy, h, w, None, EPS)
+    h[1, 5], h[3, 4103], dy[4, 0] = float("inf"), float("nan"), float("-inf")
+    dx, dw = moe.rmsnorm_grad(dy, h, w, None, EPS)
+    assert dx[[1, 3]].isnan().all() and dx[4].isfinite().logical_not().all() and dx[4, 0].isnan()
+    assert torch.equal(dx[[0, 2, 5]], want[[0, 2, 5]])
+    assert dw[5].isnan() and dw[4103].isnan()
