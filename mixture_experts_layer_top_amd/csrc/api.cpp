@@ -749,7 +749,9 @@ int layer_impl(const moe_problem* p, const float* logits, const void* x, const m
   a.y = L.y; a.y_sh = L.ffn.y_sh;
   a.out_eeff = a.i8 ? nullptr : out_eeff;
   a.out_policy = a.i8 ? nullptr : out_policy;
-  SelectOut o{L.ffn.segs, L.ffn.meta, L.ffn.split_part};
+  // (no segments: launch_front_small, which every small batch takes, then selects nothing)
+  const bool small = small_i8(p);
+  SelectOut o{small ? nullptr : L.ffn.segs, L.ffn.meta, L.ffn.split_part};
 
   hipError_t e = mark(0);
   if (p->config == MOE_CONFIG_FUSED) {  // (check_problem admitted one bf16 token, no shared expert)
@@ -830,10 +832,10 @@ int layer_impl(const moe_problem* p, const float* logits, const void* x, const m
     if (e == hipSuccess && a.mx8) e = launch_quant_act_mx(x, T, d, L.xq, L.xe, stream);
     if (e == hipSuccess && a.i8) e = launch_quant_i8(x, false, T, d, L.xq, L.xs, stream);
     if (e == hipSuccess) e = mark(3);
-    if (e == hipSuccess) e = launch_select(a, o, stream);
+    if (e == hipSuccess && !small) e = launch_select(a, o, stream);
     if (e == hipSuccess) e = mark(4);
   }
-  if (small_i8(p)) {
+  if (small) {
     if (e == hipSuccess)
       e = launch_small_i8(small_gate_up(p, w, L.ffn, L.xq, L.xs, counts, offsets, L.tok), true, cus,
                           stream);

@@ -240,6 +240,7 @@ __global__ __launch_bounds__(1024) void front_small_kernel(const float* __restri
       tok[row] = s / k;
     }
   }
+  if (!so.segs) return;  // (the experts' kernels take no lists)
   __syncthreads();
   select_block(sa, so, running, s_off);
 }

@@ -533,3 +533,21 @@ def test_quant_act_i8_of_the_most_rows(moe):
     for part in (slice(0, 7), slice(T - 7, T)):
         assert torch.equal(q[part], wq) and torch.equal(s[part], ws)
     assert (s[7:-7] == 1).all() and not q[7:-7].any()
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 16, 2), (16, 64, 8), (32, 64, 4)])
+def test_layer_of_few_tokens_selects_nothing(moe, T, E, k):
+    """Few tokens stream without a selection, in the whole layer too: the tile lists in the workspace (by far
+    its largest piece here) are not written, where a forced family writes the heads of its lists."""
+    W = Experts(moe, E, 128, 128, seed=41)
+    x, logits = _bf16(T, 128, seed=1).view(torch.int16), torch.randn(T, E, generator=_gen(2)).cuda()
+
+    def untouched(cfg):
+        L = moe.Layer(W.ew, T, E, k, cfg)
+        L.ws.fill_(0xA5)
+        out = L(logits, x).clone()
+        at = torch.nonzero(L.ws != 0xA5)[:, 0].cpu().numpy()
+        return int(np.diff(np.concatenate([[-1], at, [L.ws.numel()]])).max()), out
+
+    (auto, a), (forced, b) = untouched(moe.CONFIG_AUTO), untouched(moe.CONFIG_STREAM)
+    assert auto > 1.5 * forced and torch.equal(a, b)
