@@ -47,8 +47,8 @@
  *   - Limits: 1 <= k <= 8, k <= E <= 512, d_model and d_ff multiples of 128, T*k < 2^31.  The
  *     kernels address rows with 32-bit byte offsets, so moe_layer and moe_grouped_ffn also need
  *     T*k*max(d_model, d_ff, d_ff_shared)*2 < 2^32 and d_model*max(d_ff, d_ff_shared)*2 < 2^32
- *     (every activation, h and y buffer and each expert matrix below 4 GiB); moe_quant_act needs
- *     T*d/128 < 2^31 and moe_permute's gather T*k*d/128 < 2^31.  moe_quant_act_i8, moe_rmsnorm,
+ *     (every activation, h and y buffer and each expert matrix below 4 GiB; int8 experts' fp32 h, in the
+ *     workspace, below 8); moe_quant_act needs T*d/128 < 2^31 and moe_permute's gather T*k*d/128 < 2^31.  moe_quant_act_i8, moe_rmsnorm,
  *     moe_rmsnorm_grad, moe_route_grad and moe_combine_grad need T < 2^25, moe_permute_grad fewer than
  *     2^32 threads (d / 8 per token, rounded up to 256 unless a multiple of 64).  Outside them:
  *     MOE_ERR_UNSUPPORTED.

@@ -47,7 +47,8 @@ int device_cus() {
 }
 
 // The kernels address activation, h and y rows and one expert's weight matrix with 32-bit byte
-// offsets (one VGPR per address instead of two): every such buffer must stay below 4 GiB.
+// offsets (one VGPR per address instead of two): every such buffer must stay below 4 GiB (but for the
+// fp32 h of int8 experts, see check_problem).
 constexpr int64_t kMaxOffsetBytes = int64_t(1) << 32;
 
 int check_route_shape(int T, int E, int k) {
@@ -95,8 +96,9 @@ int check_problem(const moe_problem* p) {
        p->d_ff > kStreamXlMaxK))
     return MOE_ERR_UNSUPPORTED;
   if (policy && p->wdtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;  // (streaming only)
-  // 32-bit byte offsets: x [T][d], h [T*k][f], y [T*k][d], shared h [T][f_sh] (2 bytes per value
-  // at most) and each expert's [f][d] matrices must stay below 4 GiB
+  // 32-bit byte offsets: x [T][d], h [T*k][f], y [T*k][d], shared h [T][f_sh] at 2 bytes per value and
+  // each expert's [f][d] matrices must stay below 4 GiB.  (int8 experts' fp32 h may reach 8 GiB: its
+  // writers and its quantisation use 64-bit offsets, the quantised rows are a quarter of it.)
   const int64_t n = (int64_t)p->T * p->top_k;
   const int64_t f_sh = p->has_shared ? p->d_ff_shared : 0;
   const int64_t wide = std::max<int64_t>(std::max(p->d_model, p->d_ff), f_sh);

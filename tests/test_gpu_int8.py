@@ -551,3 +551,28 @@ def test_layer_of_few_tokens_selects_nothing(moe, T, E, k):
 
     (auto, a), (forced, b) = untouched(moe.CONFIG_AUTO), untouched(moe.CONFIG_STREAM)
     assert auto > 1.5 * forced and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cfg", ["auto", "stream"])
+def test_grouped_ffn_of_h_past_32_bit_offsets(moe, cfg):
+    """fp32 h of more than 2^32 bytes: an expert's rows are eight rows over and over."""
+    d, f, rep = 128, 32768, 2064
+    assert 16 * rep * f * 4 > 2 ** 32 and 16 * rep * f * 2 < 2 ** 32
+    W = Experts(moe, 2, d, f, seed=43)
+    xq, xs, cnt, off = _rows([8, 8], d, seed=44)
+    few = moe.grouped_ffn(xq, xs, cnt, off, W.ew, 16, 1, moe.CONFIG_MFMA)
+    big = xq.view(2, 1, 8, d).expand(2, rep, 8, d).reshape(-1, d)
+    y = moe.grouped_ffn(big, xs.view(2, 1, 8).expand(2, rep, 8).reshape(-1), cnt * rep, off * rep, W.ew, 16 * rep, 1,
+                        {"auto": moe.CONFIG_AUTO, "stream": moe.CONFIG_STREAM}[cfg])
+    assert torch.equal(y.view(2, rep, 8, d), few.view(2, 1, 8, d).expand(2, rep, 8, d))
+
+
+def test_layer_of_shared_h_past_32_bit_offsets(moe):
+    """The same of the shared expert, in the whole layer."""
+    d, f, sf, E, rep = 128, 128, 32768, 2, 4128
+    assert 8 * rep * sf * 4 > 2 ** 32 and 8 * rep * sf * 2 < 2 ** 32
+    W = Experts(moe, E, d, f, seed=45, shared_f=sf)
+    x, logits = _bf16(8, d, seed=1).view(torch.int16), torch.randn(8, E, generator=_gen(2)).cuda()
+    few = moe.layer(logits, x, W.ew, 1)
+    out = moe.layer(logits.repeat(rep, 1), x.repeat(rep, 1), W.ew, 1)
+    assert torch.equal(out.view(rep, 8, d), few.expand(rep, 8, d))
