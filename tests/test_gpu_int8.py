@@ -576,3 +576,17 @@ def test_layer_of_shared_h_past_32_bit_offsets(moe):
     few = moe.layer(logits, x, W.ew, 1)
     out = moe.layer(logits.repeat(rep, 1), x.repeat(rep, 1), W.ew, 1)
     assert torch.equal(out.view(rep, 8, d), few.expand(rep, 8, d))
+
+
+@pytest.mark.parametrize("T,k", [(16, 1), (15, 2), (2, 8)])
+def test_small_batch_of_the_largest_lds(moe, T, k):
+    """Sixteen rows of 4096 codes: the small path's down tiles take 65792 bytes of LDS, more than 64 KB."""
+    d, f, E = 128, 4096, 8
+    W = Experts(moe, E, d, f, seed=47)
+    counts = [T * k, 0, 0, 0, 0, 0, 0, 0] if k == 1 else [16] + [0] * 6 + [T * k - 16]
+    xq, xs, cnt, off = _rows(counts, d, seed=48)
+    y = moe.grouped_ffn(xq, xs, cnt, off, W.ew, T, k)
+    assert torch.equal(y, moe.grouped_ffn(xq, xs, cnt, off, W.ew, T, k, moe.CONFIG_STREAM))
+    ref, slack = R.expert_i8(f64(xq[:16]), f64(xs[:16]), W.get(0))
+    got = f64(y.view(torch.bfloat16))[:16]
+    assert (np.abs(got - ref) <= slack * (1 + 2.0 ** -7) + np.abs(ref) * (2.0 ** -8 + 2.0 ** -20)).all()
