@@ -308,7 +308,9 @@ def combine(y_perm, slot_dst, topk_w, shared_y=None):
 #
 # bf16 tensors are torch.bfloat16 or their bits as torch.int16, like the rest of this module's; outputs
 # take the input's choice.  Tensors must be contiguous and on one GPU, which need not be the current
-# one: a call runs on that GPU's current stream.  These calls are a few microseconds of GPU work at
+# one: a call runs on that GPU's current stream.  (The layer's own steps above and Layer run on the
+# current GPU, which has to be the tensors'.)  No call records anything for autograd: outputs never require
+# grad, and a training step calls the gradients by name.  These calls are a few microseconds of GPU work at
 # decode sizes, so what they do on the host counts: one pass of cheap checks per tensor, and the stream's
 # handle without a Stream object (2 us).
 # ------------------------------------------------------------------------------------------------
@@ -368,7 +370,8 @@ def int8_tile(w: torch.Tensor) -> torch.Tensor:
     if w.dtype != torch.int8:
         raise MoEError(f"w must be torch.int8, not {w.dtype}")
     _dev(w)
-    return fp8_tile(w)
+    with torch.cuda.device(w.get_device()):
+        return fp8_tile(w)
 
 
 def gemm_i8(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor):

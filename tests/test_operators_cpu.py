@@ -177,3 +177,41 @@ def test_more_rows_than_a_launch_has_threads_for(L):
     assert L.moe_combine_grad(A, A, A, A, T, 2, 128, A, A, None) == UNS
     assert L.moe_permute_grad(A, A, None, 1 << 24, 2, 128, A, None) == UNS  # 256 threads each
     assert L.moe_permute_grad(A, A, None, 1 << 26, 2, 512, A, None) == UNS  # 64 threads each
+
+
+def test_binding_runs_on_the_tensors_gpu(monkeypatch):
+    """Tensors of a GPU that is not the current one: the library is called with that GPU current and its
+    stream, tiling included."""
+    import contextlib
+    current = [0]
+
+    @contextlib.contextmanager
+    def device(i):
+        was, current[0] = current[0], i
+        yield
+        current[0] = was
+
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: calls.append((name, current[0], args[-1])) or 0
+
+    class OnGpu1:
+        dtype, is_cuda, device, shape = torch.int8, True, torch.device("cuda", 1), (16, 128)
+        get_device = staticmethod(lambda: 1)
+        contiguous = empty_like = lambda self: self
+        numel = staticmethod(lambda: 2048)
+        data_ptr = staticmethod(lambda: 0)
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    monkeypatch.setattr(moe, "_stream", lambda: 100 + current[0])
+    monkeypatch.setattr(moe, "lib", Lib)
+    monkeypatch.setattr(torch, "empty_like", lambda t: OnGpu1())
+    moe._run("moe_quant_act_i8", 1, 7)
+    assert moe.int8_tile(OnGpu1())._moe_tiled
+    moe._run("moe_quant_act_i8", 0, 7)
+    assert calls == [("moe_quant_act_i8", 1, 101), ("moe_fp8_tile", 1, 101), ("moe_quant_act_i8", 0, 100)]
+    assert current == [0]
