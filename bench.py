@@ -115,6 +115,8 @@ def algorithmic(p, n_active: int):
 TRAFFIC_SOURCES = ("mixture_experts_layer_top_amd/csrc/gemm_bf16.hip",
                    "mixture_experts_layer_top_amd/csrc/common.h",
                    "mixture_experts_layer_top_amd/csrc/kernels.h",
+                   "mixture_experts_layer_top_amd/csrc/mfma_dev.h",
+                   "mixture_experts_layer_top_amd/csrc/mfma_tile.h",
                    "mixture_experts_layer_top_amd/csrc/select_dev.h")
 
 
