@@ -397,7 +397,7 @@ __global__ __launch_bounds__(256) void gemm_small_i8(SmallI8 a) {
                             __uint_as_float(u.w)};
 #pragma unroll
               for (int j = 0; j < 4; ++j) v[j] = bad ? 0.f : v[j];
-              i8_pack<1>(v, f, reinterpret_cast<uint32_t*>(s_x + i * xl + c));
+              i8_pack<1, false>(v, f, reinterpret_cast<uint32_t*>(s_x + i * xl + c));
             }
           }
           __syncthreads();

@@ -26,15 +26,20 @@ struct Scale {
   }
   // v / s rounded to a whole number, ties to even, |v| / s < 127.5: the rounded product is at most one off,
   // and the remainder, exact in fp32 (a multiple of half an ulp of s, at most s), says so.  (Rounding
-  // fp32(v / s) would not do: amax / 2 over s is 63.4999999, and comes out as 63.5 and then 64.)  A
-  // remainder of exactly half of s is a tie, and an odd n then goes to the even side: with 1 / s rounded
-  // (s of few bits but no power of two) the product may lie on either side of it.
+  // fp32(v / s) would not do: amax / 2 over s is 63.4999999, and comes out as 63.5 and then 64.)
+  // A remainder of exactly half of s is a tie, and an odd n then goes to the even side: with 1 / s rounded
+  // (s of few bits but no power of two) the product may lie on either side of it.  BF16 rows have no such
+  // ties: fp32(amax / 127) of a bf16 amax has few bits only as a power of two, whose reciprocal is exact,
+  // so the product is the tie and rounds to even.
+  template <bool BF16>
   __host__ __device__ __forceinline__ int whole(float v) const {
     v *= k;
     const float n = __builtin_rintf(v * r), e = fmaf(-n, s, v), h = 0.5f * s;
     const int i = (int)n;
-    const bool off = fabsf(e) > h || (fabsf(e) == h && (i & 1));
-    return i + (off ? (e > 0.0f ? 1 : -1) : 0);
+    if (BF16) return i + (e > h ? 1 : 0) - (e < -h ? 1 : 0);
+    // (over half: a positive difference, or none and an odd n)
+    const int over = __builtin_bit_cast(int, fmaf(2.0f, fabsf(e), -s)) + (i & 1);
+    return i + (over > 0 ? (__builtin_bit_cast(int, e) >> 31 | 1) : 0);
   }
 };
 
@@ -51,24 +56,30 @@ __host__ __device__ __forceinline__ float i8_scale(uint32_t amax_bits) {
              ? s
              : __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, s) + 1);
 }
-// 4 N codes, four in a dword.  v * r is within 127.5 * 2^-24 of v / s, so its nearest whole number is the
-// code unless it lies within 2^-16 of a half step; then all of them are found from their remainders.  (That for
-// every value: the norm of 4096 rows of 4096 22.9 us against 18.4, of 16 rows of 7168 5.2 against 4.3, the
-// down product of one token, which quantises h, 25.8 against 23.9.)
-template <int N>
+// 4 N codes, four in a dword.  For fp32 rows a value's nearest whole number is taken from its product with r
+// and counts unless v / s, from r and what it is off, lies within 2^-23 of a half step; then all of them are
+// found from their remainders.  (That for every value: the norm of 4096 rows of 4096 19.7 us against 17.5, of
+// 16 rows of 7168 4.5 against 4.2; h of 8192 x 14336 98.9 against 96.7.)  bf16 rows hold +-amax / 2, which is
+// near a half step, every few hundred values, and the remainders' way is the faster (2048 rows of 4096 8.0
+// us against 10.5).
+template <int N, bool BF16>
 __host__ __device__ __forceinline__ void i8_pack(const float* v, const Scale& sc, uint32_t* out) {
   constexpr float kWhole = 0x1.8p23f;  // added, it leaves whole numbers: the sum's low byte is the code
   uint32_t c[4 * N];
-  float far = 0.0f;
+  float far = BF16 ? 1.0f : 0.0f;
+  if (!BF16) {
+    const float lo = fmaf(-sc.s, sc.r, 1.0f) * sc.r;  // 1 / s - r
 #pragma unroll
-  for (int i = 0; i < 4 * N; ++i) {
-    const float a = v[i] * sc.k, t = fmaf(a, sc.r, kWhole);
-    c[i] = __builtin_bit_cast(uint32_t, t);
-    far = fmaxf(far, fabsf(fmaf(a, sc.r, kWhole - t)));
+    for (int i = 0; i < 4 * N; ++i) {
+      const float a = v[i] * sc.k, t = fmaf(a, sc.r, kWhole);
+      c[i] = __builtin_bit_cast(uint32_t, t);
+      // (the product less the whole number is exact but for its last bit, 2^-25 at most)
+      far = fmaxf(far, fabsf(fmaf(a, lo, fmaf(a, sc.r, kWhole - t))));
+    }
   }
-  if (far > 0.5f - 0x1p-16f) {
+  if (far > 0.5f - 0x1p-23f) {
 #pragma unroll
-    for (int i = 0; i < 4 * N; ++i) c[i] = (uint32_t)sc.whole(v[i]);
+    for (int i = 0; i < 4 * N; ++i) c[i] = (uint32_t)sc.whole<BF16>(v[i]);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i)

@@ -188,7 +188,7 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = bad_row ? 0.f : v[j];
       uint32_t c[2];
-      i8_pack<2>(v, row_scale, c);
+      i8_pack<2, false>(v, row_scale, c);
       st8(q, (base + idx) * 8, c[0], c[1]);
     }
     if (FMT == kNormFp8 || FMT == kNormMx) {
@@ -269,7 +269,7 @@ __global__ __launch_bounds__(row_block(R)) void quant_i8_kernel(const void* __re
     for (int j = 0; j < N; ++j) v[j] = bad ? 0.f : v[j];
     const size_t at = (base + i + R * s) * N;
     uint32_t c[N / 4];
-    i8_pack<N / 4>(v, f, c);
+    i8_pack<N / 4, !F32>(v, f, c);
     if constexpr (F32) gstore4(q, at, c[0]);
     else st8(q, at, c[0], c[1]);
   }

@@ -25,14 +25,20 @@ def codec(tmp_path_factory):
                     "-o", so], check=True, capture_output=True)
     lib = ctypes.CDLL(so)
     lib.i8_row_scale.argtypes, lib.i8_row_scale.restype = [ctypes.c_uint32], ctypes.c_float
-    lib.i8_row_codes.argtypes = [ctypes.c_float, ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p]
+    for f in (lib.i8_row_codes, lib.i8_row_codes_bf16):
+        f.argtypes = [ctypes.c_float, ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p]
 
     def row(v):
-        """(scale, codes) of one row of fp32 values, a multiple of four of them."""
+        """(scale, codes) of one row of fp32 values, a multiple of four of them; bf16 values the same by both
+        ways."""
         v = np.ascontiguousarray(v, np.float32)
         s = np.float32(lib.i8_row_scale(int(np.abs(v).max().view(np.uint32))))
         q = np.empty(v.size, np.int8)
         lib.i8_row_codes(s, v.ctypes.data, v.size // 4, q.ctypes.data)
+        if not (v.view(np.uint32) & 0xFFFF).any():
+            b = np.empty_like(q)
+            lib.i8_row_codes_bf16(s, v.ctypes.data, v.size // 4, b.ctypes.data)
+            assert np.array_equal(q, b)
         return s, q.astype(np.int64)
 
     return row
@@ -55,6 +61,18 @@ def test_rows_of_every_magnitude(codec):
         check(codec, (v.view(np.uint32) & 0xFFFF0000).view(np.float32))  # bf16 values
     s, q = codec(np.zeros(8, np.float32))
     assert s == 1 and not q.any()
+
+
+def test_every_bf16_value_below_every_amax(codec):
+    """All bf16 magnitudes from amax / 256 to amax, for every mantissa of amax: the halves of amax, exact
+    ties of power-of-two scales and all quotients between."""
+    for m in range(128, 256):
+        top = np.float32(m * 2.0 ** -7)
+        p = np.arange(128, 256)
+        v = np.concatenate([p * 2.0 ** -j for j in range(7, 16)]).astype(np.float32)
+        v = v[v <= top]
+        v = np.concatenate([v, -v, [top] * ((-2 * v.size) % 4 + 4)])
+        check(codec, v[:v.size // 4 * 4])
 
 
 def test_exact_half_steps_round_to_even(codec):
