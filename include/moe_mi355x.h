@@ -318,8 +318,9 @@ int moe_gemm_i8(const int8_t* xq, const float* xs, int M, const int8_t* wq, cons
  *   x, residual [T][d] bf16, weight [d] bf16, eps >= 0.
  *   h_out [T][d] bf16 or NULL: the new residual stream; it may be x or residual itself.
  *   y [T][d] bf16 (may be NULL when there is an 8-bit output).
- *   act_dtype names the weight format whose activations q and q_scale receive, quantised from the
- *   fp32 y in one rounding: MOE_DTYPE_BF16 none (q, q_scale ignored); MOE_DTYPE_FP8_E4M3 e4m3 with fp32
+ *   act_dtype names the format of q and q_scale, quantised from the fp32 y in one rounding (e4m3 rows
+ *   and int8 rows are what moe_permute and moe_grouped_ffn take; MXFP8 rows have no taker among these
+ *   calls, whose MXFP4 experts quantise bf16 rows themselves; moe_layer takes bf16 x only): MOE_DTYPE_BF16 none (q, q_scale ignored); MOE_DTYPE_FP8_E4M3 e4m3 with fp32
  *   scales [T][d/128] (d % 128 == 0); MOE_DTYPE_MXFP4_A8 e4m3 with E8M0 scales [T][d/32] (d % 32 == 0);
  *   MOE_DTYPE_INT8 int8 with fp32 scales [T] (d % 16 == 0) -- each by the rules of moe_quant_act,
  *   moe_quant_act_mx and moe_quant_act_i8.

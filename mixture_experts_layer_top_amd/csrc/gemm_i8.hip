@@ -4,7 +4,7 @@
 //   acc[row][n] = sum_k qx[row][k] * qw[n][k]          (int32, exact: K <= 32768 keeps it below 2^30)
 //   v[row][n] = float(acc) * sx[row] * sw[n]
 //   gate/up: h = SiLU(v_gate) * v_up in fp32 (quantised per row before the down GEMM, norm.hip: a
-//            row's scale needs all of its d_ff columns, so it cannot be taken inside a tile)
+//            row's scale needs all of its d_ff columns, which no tile has alone)
 //   down, dense: y = bf16(v)
 //
 // The scales are constant along K, so the K loops are MFMAs and loads only, and integer sums do not
@@ -13,9 +13,11 @@
 //  * stream (light experts, small dense products): a workgroup's 4 wavefronts split K over 16 weight
 //    rows (K >= kStreamSplitK) or 32, up to 64 token rows per pass; weights go straight from HBM
 //    into MFMA registers, 1 KB contiguous per load in the tiled layout (moe_fp8_tile).
-//  * mfma (mfma_tile.h): 256 weight rows by 32 to 256 token rows staged through LDS; dense 4096 x 4096 x
-//    14336 222 us (2.17 POP/s, 0.99 of the library's product; the chip's power limit), 8 experts of
-//    4096 x 14336, 8192 rows 930 + 470 us (2.05).
+//  * mfma (mfma_tile.h): 256 weight rows by 32 to 256 token rows staged through LDS; dense, 4096 rows
+//    of K = 4096 by 14336 channels, 217-230 us (2.1-2.2 POP/s, the library's rate), of K = 14336 by 4096 193
+//    (2.49): the clock falls to 1.6-1.7 GHz under this load, and MFMAs fill 0.67 of the CUs' busy cycles at
+//    K = 4096, where an epilogue follows every 32 K-steps, and 0.83 at K = 14336.  8 experts of 4096 x 14336,
+//    8192 rows: 930-945 + 470 us (2.04-2.06).
 #include <algorithm>
 
 #include "common.h"

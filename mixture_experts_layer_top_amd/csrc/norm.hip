@@ -13,7 +13,7 @@
 // squares, then the scaling) run from there, and the 8-bit output costs no second read of y.  The
 // sum of squares is held in fp64 across a row, over fp32 chains of eight; a row whose squares leave
 // fp32's range (row_rstd) is summed again in fp64 from its registers.  Forward with a residual and e4m3 rows: 8192 x 7168 98 us (5.4
-// TB/s, a copy's rate), 1 x 7168 3.3 us.
+// TB/s, a copy's rate), 1 x 7168 3.4 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -278,9 +278,9 @@ __global__ __launch_bounds__(row_block(R)) void quant_i8_kernel(const void* __re
 // Norm gradient: every workgroup takes rows blockIdx.x, + gridDim.x, ... and keeps its share of dw
 // in registers; part [gridDim.x][d] receives it (summed by dw_reduce_kernel, in a fixed order).
 // Up to 4096 channels the next row is loaded while this one is reduced (two rows do not fit the
-// registers beyond that).  Both kernels, T x d: 4096 x 4096 with dh 28.3 us (4.75 TB/s; 30.5 without
-// the second row in flight and with 8 columns a workgroup in the sum), 8192 x 7168 with dh 94.6 (4.97),
-// 777 x 7168 15.2 (21.3), 17 x 4096 5.5.
+// registers beyond that).  Both kernels, T x d: 4096 x 4096 with dh 29.4 us (4.6 TB/s; without
+// the second row in flight and with 8 columns a workgroup in the sum 30.5 where it took 28.3), 8192 x 7168
+// with dh 94.8 (4.96), 777 x 7168 15.3 (21.3 where it took 15.2).
 template <int R, int V>
 __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
     const void* dy, const void* dh, const void* h, const void* __restrict__ w, float eps,

@@ -393,9 +393,10 @@ def gemm_i8(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scale: torch.
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
             eps: float = 1e-6, act_dtype: int = DTYPE_BF16, want_y: bool = True):
     """RMS norm of h = x + residual.  Returns (h, y, q, q_scale): h is x itself without a residual, y is
-    None when not wanted (8-bit outputs only), q and q_scale are the activations that experts of format
-    act_dtype take (DTYPE_FP8: e4m3 uint8 and fp32 [T, d/128]; DTYPE_MXFP4_A8: e4m3 and E8M0 uint8
-    [T, d/32]; DTYPE_INT8: int8 and fp32 [T]; DTYPE_BF16: None)."""
+    None when not wanted (8-bit outputs only), q and q_scale are y in the format act_dtype (DTYPE_FP8: e4m3
+    uint8 and fp32 [T, d/128]; DTYPE_INT8: int8 and fp32 [T]: what permute and grouped_ffn take;
+    DTYPE_MXFP4_A8: e4m3 and E8M0 uint8 [T, d/32], as quant_act_mx writes them, which no call here takes;
+    DTYPE_BF16: None).  The outputs carry no autograd history (rmsnorm_grad is the gradient)."""
     T, d = _rows(x, "x")
     dev = x.get_device()
     _arg(x, "x", (T, d), _BF16, dev)
