@@ -12,8 +12,8 @@
 // All of it is bound by HBM: a row is read once into registers, both passes over it (the sum of
 // squares, then the scaling) run from there, and the 8-bit output costs no second read of y.  The
 // sum of squares is held in fp64 across a row, over fp32 chains of eight; a row whose squares leave
-// fp32's range (row_rstd) is summed again in fp64 from its registers.  Forward with a residual and e4m3 rows: 8192 x 7168 98 us (5.4
-// TB/s, a copy's rate), 1 x 7168 3.4 us.
+// fp32's range (row_in_range) is summed again in fp64 from its registers.  Forward with a residual and e4m3
+// rows: 8192 x 7168 98 us (5.4 TB/s, a copy's rate), 1 x 7168 3.4 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -57,9 +57,10 @@ __device__ __forceinline__ float row_rstd(double sum, double inv_d, float eps) {
 constexpr float kSmallRow = 0x1p32f;
 __device__ __forceinline__ float wide_rstd(double sum, double inv_d, float eps, bool& small) {
   const double m = sum * inv_d + (double)eps;
-  small = m < 1.0;
-  if (!(m < __builtin_inf())) return __uint_as_float(0x7FC00000u);
-  return small ? 0x1p68f / sqrtf(float(m * 0x1p200)) : 0x1p-100f / sqrtf(float(m * 0x1p-200));
+  small = m < 0x1p-100;
+  if (small) return 0x1p68f / sqrtf(float(m * 0x1p200));
+  if (m <= 0x1p100) return 1.0f / sqrtf(float(m));  // (the gradient's products may leave the range alone)
+  return m < __builtin_inf() ? 0x1p-100f / sqrtf(float(m * 0x1p-200)) : __uint_as_float(0x7FC00000u);
 }
 
 // The wide sums of a row out of range, two values at a time in a loop, and its values times kSmallRow

@@ -419,3 +419,26 @@ def test_rmsnorm_grad_of_non_finite_rows(moe):
     assert dx[[1, 3]].isnan().all() and dx[4].isfinite().logical_not().all() and dx[4, 0].isnan()
     assert torch.equal(dx[[0, 2, 5]], want[[0, 2, 5]])
     assert dw[5].isnan() and dw[4103].isnan()
+
+
+@pytest.mark.parametrize("size", [0.9, 6.0])
+@pytest.mark.parametrize("d", [64, 256, 1024, 8192])
+def test_rmsnorm_grad_of_products_past_fp32(moe, d, size):
+    """Ordinary rows whose dy * weight * h passes fp32's range in the sum, with a dx that does not: rows of
+    mean square below and above one."""
+    g = torch.Generator().manual_seed(d)
+    h = (torch.randint(0, 2, (2, d), generator=g) * 2 - 1).to(torch.bfloat16).mul_(size).cuda()
+    dy = (torch.rand(2, d, generator=g) + 1).mul_(8e37 if size < 1 else 5e37).to(torch.bfloat16).cuda()
+    w = (torch.rand(d, generator=g) * 0.5 + 0.5).to(torch.bfloat16).cuda()
+    dx, dw = moe.rmsnorm_grad(dy, h, w, None, EPS)
+    dy64, h64, w64 = f64(dy), f64(h), f64(w)
+    chains = (dy64 * w64 * h64).reshape(2, -1, 8).cumsum(-1)
+    assert np.abs(chains).max() > 3.5e38
+    ref, refw = R.rmsnorm_grad(dy64, h64, w64, EPS)
+    r = 1 / np.sqrt((h64 ** 2).mean(-1, keepdims=True) + EPS)
+    gg, n = dy64 * w64, h64 * r
+    terms = r * (np.abs(gg) + np.abs(n) * np.abs(gg * n).mean(-1, keepdims=True))
+    assert np.abs(ref).max() < 3e38
+    assert (np.abs(f64(dx) - ref) <= np.abs(ref) * 2.0 ** -8 + terms * 2 * Y).all()
+    if np.abs(refw).max() < 3e38:
+        assert (np.abs(f64(dw) - refw) <= (1 + 16 + 32 + 14) * 2.0 ** -24 * np.abs(dy64 * n).sum(0)).all()
