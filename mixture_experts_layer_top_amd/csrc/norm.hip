@@ -349,8 +349,10 @@ __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
     float rstd = row_rstd(sum[0], inv_d, eps);
     float c = float(sum[1] * inv_d) * rstd * rstd;
     float up = 1.0f;
-    if (!row_in_range(sum[0], inv_d, eps) || !(fabs(sum[1]) < __builtin_inf())) {
-      // (the row's sums in fp64, as in the forward kernel; the same in all threads)
+    const double gn = fabs(sum[1]) * inv_d;
+    if (!row_in_range(sum[0], inv_d, eps) || !(gn < __builtin_inf()) || (gn < 0x1p-100 && gn > 0.0)) {
+      // (the row's sums in fp64, as in the forward kernel; the same in all threads.  A sum of 0, which rows
+      // without a gradient have, stays: its products are 0, or below 2^-150 each)
       sum[0] = sum[1] = 0.0;
 #pragma unroll
       for (int s = 0; s < V; ++s) {

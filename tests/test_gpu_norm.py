@@ -442,3 +442,20 @@ def test_rmsnorm_grad_of_products_past_fp32(moe, d, size):
     assert (np.abs(f64(dx) - ref) <= np.abs(ref) * 2.0 ** -8 + terms * 2 * Y).all()
     if np.abs(refw).max() < 3e38:
         assert (np.abs(f64(dw) - refw) <= (1 + 16 + 32 + 14) * 2.0 ** -24 * np.abs(dy64 * n).sum(0)).all()
+
+
+@pytest.mark.parametrize("dy_size,h_size", [(1e-30, 1e-9), (1e-36, 1e-4), (1e-28, 1e-14), (1e-38, 1e-6)])
+@pytest.mark.parametrize("d", [256, 8192])
+def test_rmsnorm_grad_of_products_below_fp32(moe, d, dy_size, h_size):
+    """dy * weight * h below the smallest normal float, of rows in fp32's range: mean(g n) keeps its bits."""
+    h, dy, w = _bf16(3, d, seed=1, std=h_size), _bf16(3, d, seed=2, std=dy_size), _bf16(d, seed=3)
+    dy = (dy.float() + 3 * h.float() * (dy_size / h_size)).to(torch.bfloat16)  # (a mean(g n) that counts)
+    dy[1] = 0
+    dx, _ = moe.rmsnorm_grad(dy, h, w, None, 0.0)
+    dy64, h64, w64 = f64(dy), f64(h), f64(w)
+    ref, _ = R.rmsnorm_grad(dy64, h64, w64, 0.0)
+    r = 1 / np.sqrt((h64 ** 2).mean(-1, keepdims=True))
+    g, n = dy64 * w64, h64 * r
+    terms = r * (np.abs(g) + np.abs(n) * np.abs(g * n).mean(-1, keepdims=True) + 2.0 ** -149)
+    assert (np.abs(f64(dx) - ref) <= np.abs(ref) * 2.0 ** -8 + terms * 2 * Y + r * 2.0 ** -148).all()
+    assert not dx[1].any()
