@@ -363,6 +363,107 @@ int moe_combine_grad(const void* dout, const void* y_perm, const int32_t* slot_d
 int moe_permute_grad(const void* dx_perm, const int32_t* slot_dst, const void* dx_add, int T, int k,
                      int d, void* dx, hipStream_t stream);
 
+/* Routing by scores, for models whose router is not moe_route's softmax over the selected k. */
+enum moe_score {
+  MOE_SCORE_SOFTMAX = 0, /* s_e = exp(l_e) / sum over all E experts */
+  MOE_SCORE_SIGMOID = 1  /* s_e = 1 / (1 + exp(-l_e)) */
+};
+typedef struct moe_scoring {
+  int32_t score;      /* enum moe_score */
+  int32_t groups;     /* the experts lie in this many groups of E / groups consecutive ones (1: no groups) */
+  int32_t top_groups; /* groups that stay, top_groups * (E / groups) >= k */
+  int32_t group_top;  /* 1 or 2 (<= E / groups): how many of its largest c a group is valued by, summed */
+  int32_t renorm;     /* 1: weights renormalised over the selected k */
+  float scale;        /* factor of the weights, > 0 and finite */
+} moe_scoring;
+
+/* Route by scores: c_e = s_e + bias_e (bias, for balance, takes part in the selection only); topk_ids[t] =
+ * the k experts with the largest c among the top_groups best groups, descending, ties to the lower id (of
+ * groups: to the lower group); topk_w[t][j] = scale * s_j, renormalised scale * s_j / sum_i s_i (0 where that
+ * sum is 0).  The selection is that of scores in 64 bits; without a bias experts are compared by their
+ * logits, whose order the scores have.
+ * An expert whose logit is -inf is masked: its score is 0 and it comes behind every expert with a finite c
+ * or c = +inf, whatever its bias; where fewer than k others are left (a row may be masked whole) the lowest
+ * masked ids fill up, with weight 0.  The lowest finite float is a number like others.  A NaN logit or bias, or
+ * softmax over a +inf logit, leaves weights unspecified; the ids of a row are k different experts whatever it holds.
+ *   logits [T][E] fp32, bias [E] fp32 or NULL.  Outputs [T][k].
+ *   1 <= k <= 8, E <= 512, groups <= 64 and a divisor of E, T < 2^25, else MOE_ERR_UNSUPPORTED. */
+int moe_route_scored(const float* logits, const float* bias, int T, int E, int k, const moe_scoring* scoring,
+                     int32_t* topk_ids, float* topk_w, hipStream_t stream);
+
+/* Gradient of moe_route_scored's weights to the logits (the selection and the bias have none), with the
+ * forward call's outputs: dlogits [T][E] fp32, written whole.  With D = sum_i w_i dw_i and the scores s, for
+ * the selected experts
+ *   sigmoid: (1 - s_j) w_j (dw_j - D / scale) renormalised, (1 - s_j) w_j dw_j otherwise;
+ *   softmax: w_j (dw_j - D / scale) renormalised, w_j dw_j - s_j D otherwise;
+ * and 0 for the others, but -s_e D for softmax without renormalisation.  Slots that name the same expert
+ * add up; ids outside [0, E) have no part but in D.  scoring's groups are not looked at. */
+int moe_route_scored_grad(const float* logits, const int32_t* topk_ids, const float* topk_w,
+                          const float* dtopk_w, int T, int E, int k, const moe_scoring* scoring,
+                          float* dlogits, hipStream_t stream);
+
+/* Norms around a block (attention, or the layer itself), its gate and the residual stream, in one pass: with
+ * x the block's output,
+ *   u = x / sqrt(mean(x^2) + eps) * post_weight  (x itself without a norm behind the block)
+ *   h = bf16(residual_scale * residual + branch_scale * gate * u)
+ *   y = h / sqrt(mean(h^2) + eps) * pre_weight   (the norm in front of the next block)
+ * in fp32 (squares that leave fp32's range in fp64); y from the rounded h. */
+typedef struct moe_block {
+  const void* post_weight; /* [d] bf16 or NULL: no norm behind the block */
+  const void* gate;        /* bf16 [d], or [T][d] with gate_per_token; NULL: 1 */
+  const void* pre_weight;  /* [d] bf16 */
+  int32_t gate_per_token;  /* 0 or 1 (0 without a gate) */
+  float residual_scale;    /* finite */
+  float branch_scale;      /* finite */
+  float eps;               /* >= 0, of both norms */
+} moe_block;
+
+/*   x, residual [T][d] bf16; h_out [T][d] bf16 (may be x or residual itself); y, act_dtype, q and q_scale,
+ *   limits and rows that hold an infinity or NaN as in moe_rmsnorm. */
+int moe_block_norm(const moe_block* block, const void* x, const void* residual, int T, int d, int act_dtype,
+                   void* h_out, void* y, void* q, void* q_scale, hipStream_t stream);
+
+/* Gradient of moe_block_norm's y and h: dy [T][d] and dh [T][d] (or NULL) bf16 arrive at them; x is the
+ * forward call's, h its h_out.  With H = dh + the gradient that dy gives h (moe_rmsnorm_grad's):
+ *   dresidual = residual_scale * H, dx = the gradient that branch_scale * gate * H gives x, both [T][d]
+ *   bf16, rounded once (dx may be dy, dh or x, dresidual another of dy, dh and h);
+ *   dpre_weight, dpost_weight [d] fp32 or NULL (dpost_weight only with a post_weight);
+ *   dgate [d] fp32, [T][d] bf16 with gate_per_token, or NULL (only with a gate); it overlaps nothing else.
+ * Sums over rows run in a fixed order.  T = 0 writes zeros to those of [d].
+ *   ws: moe_block_norm_grad_workspace_bytes(T, d) bytes, needed for the outputs of [d] only.
+ *   d % 8 == 0, d <= 16384, else MOE_ERR_UNSUPPORTED (and 0 bytes). */
+int moe_block_norm_grad(const moe_block* block, const void* dy, const void* dh, const void* x, const void* h,
+                        int T, int d, void* dx, void* dresidual, float* dpre_weight, float* dpost_weight,
+                        void* dgate, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t moe_block_norm_grad_workspace_bytes(int T, int d);
+
+/* 4-bit weights [N][K]: value = (code - zero) * scale, two codes 0..15 per byte (element 2j in the low nibble
+ * of byte j), one 16-bit scale and, if zeros is not NULL, one zero point (a whole number 0..255) per `group`
+ * consecutive values of a row: scales, zeros [N][K / group].  Without zeros the zero point is 8. */
+enum moe_scale_dtype { MOE_SCALE_BF16 = 0, MOE_SCALE_FP16 = 1 };
+typedef struct moe_w4 {
+  const void* codes;
+  const void* scales;
+  const uint8_t* zeros;
+  int32_t N, K;        /* N % 16 == 0, K % 128 == 0 */
+  int32_t group;       /* 32, 64 or 128 */
+  int32_t scale_dtype; /* enum moe_scale_dtype */
+  int32_t layout;      /* enum moe_layout of all three: MOE_LAYOUT_TILED for moe_gemm_w4 */
+} moe_w4;
+
+/* Layout of 4-bit weights for moe_gemm_w4 (load time): src row-major -> codes, scales and zeros (NULL without
+ * src->zeros) of the same sizes, overlapping neither src nor each other.  The layout is the library's: per 16 rows, codes in
+ * 1 KB units of 128 columns, scales and zeros [K / group][16].  All pointers 16-byte aligned. */
+int moe_w4_tile(const moe_w4* src, void* codes, void* scales, uint8_t* zeros, hipStream_t stream);
+
+/* Product of bf16 rows with 4-bit weights: y[m][n] = bf16(sum_k x[m][k] * W[n][k]); with `up` (of w's N, K,
+ * group and scale_dtype) the SwiGLU of the pair, bf16(SiLU(x Wt) * (x Upt)): a shared expert's gate and up
+ * step, whose y moe_gemm_w4 takes back to d for moe_combine's shared_y.  Codes less zero points are exact in
+ * the products, sums and scales are fp32, one rounding.
+ *   x [M][K], y [M][N] bf16, not overlapping.  M * K < 2^31, N * K < 2^32, else MOE_ERR_UNSUPPORTED; pointers
+ *   16-byte aligned.  M = 0 is a no-op. */
+int moe_gemm_w4(const void* x, int M, const moe_w4* w, const moe_w4* up, void* y, hipStream_t stream);
+
 /* Static name of a status code. */
 const char* moe_status_string(int status);
 

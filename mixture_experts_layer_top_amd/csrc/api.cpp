@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -551,19 +552,28 @@ int moe_gemm_i8(const int8_t* xq, const float* xs, int M, const int8_t* wq, cons
   return hip_status(launch_gemm_i8(xq, xs, M, wq, ws, N, K, y, cus, stream));
 }
 
-int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int T, int d,
-                int act_dtype, void* h_out, void* y, void* q, void* q_scale, hipStream_t stream) {
-  if (T < 0 || d <= 0 || !(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
-  int fmt, step;
+namespace {
+// The norm kernels' shape and output format (launch_rmsnorm's fmt).
+int norm_format(int T, int d, int act_dtype, int* fmt) {
+  if (T < 0 || d <= 0) return MOE_ERR_INVALID_ARG;
+  int step;
   switch (act_dtype) {
-    case MOE_DTYPE_BF16: fmt = 0; step = 8; break;
-    case MOE_DTYPE_FP8_E4M3: fmt = 1; step = 128; break;
-    case MOE_DTYPE_MXFP4_A8: fmt = 2; step = 32; break;
-    case MOE_DTYPE_INT8: fmt = 3; step = 16; break;
+    case MOE_DTYPE_BF16: *fmt = 0; step = 8; break;
+    case MOE_DTYPE_FP8_E4M3: *fmt = 1; step = 128; break;
+    case MOE_DTYPE_MXFP4_A8: *fmt = 2; step = 32; break;
+    case MOE_DTYPE_INT8: *fmt = 3; step = 16; break;
     default: return MOE_ERR_UNSUPPORTED;
   }
-  if (d % step || d > kMaxRowLen || T >= kMaxRowCount) return MOE_ERR_UNSUPPORTED;
-  if (T == 0) return MOE_OK;
+  return d % step || d > kMaxRowLen || T >= kMaxRowCount ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+}  // namespace
+
+int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int T, int d,
+                int act_dtype, void* h_out, void* y, void* q, void* q_scale, hipStream_t stream) {
+  if (!(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  int fmt = 0;
+  const int st = norm_format(T, d, act_dtype, &fmt);
+  if (st || T == 0) return st;
   if (!x || !weight) return MOE_ERR_INVALID_ARG;
   if (fmt == 0 ? !y : (!q || !q_scale)) return MOE_ERR_INVALID_ARG;
   const void* al[] = {x, residual, weight, h_out, y, q};
@@ -634,6 +644,180 @@ int moe_permute_grad(const void* dx_perm, const int32_t* slot_dst, const void* d
   if (!dx_perm || !slot_dst || !dx) return MOE_ERR_INVALID_ARG;
   if (!aligned16(dx_perm) || !aligned16(dx) || !aligned16(dx_add)) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_combine(dx_perm, slot_dst, nullptr, T, k, d, dx_add, dx, stream));
+}
+
+namespace {
+int check_scoring(const moe_scoring* p, int E, int k, bool selects) {
+  if (!p) return MOE_ERR_INVALID_ARG;
+  if (p->score != MOE_SCORE_SOFTMAX && p->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (p->renorm != 0 && p->renorm != 1) return MOE_ERR_INVALID_ARG;
+  if (!(p->scale > 0.0f) || !std::isfinite(p->scale)) return MOE_ERR_INVALID_ARG;
+  if (!selects) return MOE_OK;
+  if (p->groups <= 0 || p->top_groups <= 0 || p->top_groups > p->groups) return MOE_ERR_INVALID_ARG;
+  if (p->groups > kMaxGroups || E % p->groups) return MOE_ERR_UNSUPPORTED;
+  const int size = E / p->groups;
+  if (p->group_top < 1 || p->group_top > 2 || p->group_top > size) return MOE_ERR_INVALID_ARG;
+  return p->top_groups * size < k ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+Scoring scoring_of(const moe_scoring* p) {
+  return Scoring{p->score == MOE_SCORE_SIGMOID ? kScoreSigmoid : kScoreSoftmax, p->groups, p->top_groups,
+                 p->group_top, p->renorm, p->scale};
+}
+
+int check_block(const moe_block* b, int T) {
+  if (!b || !(b->eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(b->residual_scale) || !std::isfinite(b->branch_scale)) return MOE_ERR_INVALID_ARG;
+  if (b->gate_per_token != 0 && b->gate_per_token != 1) return MOE_ERR_INVALID_ARG;
+  if (b->gate_per_token && !b->gate && T != 0) return MOE_ERR_INVALID_ARG;  // (no rows: no gate either)
+  return MOE_OK;
+}
+BlockIn block_in(const moe_block* b) {
+  return BlockIn{b->post_weight, b->gate, b->gate_per_token, b->residual_scale, b->branch_scale};
+}
+
+int check_w4(const moe_w4* w, int32_t layout) {
+  if (!w || w->N <= 0 || w->K <= 0) return MOE_ERR_INVALID_ARG;
+  if (w->N % 16 || w->K % 128 || (w->group != 32 && w->group != 64 && w->group != 128))
+    return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)w->N * w->K >= kMaxOffsetBytes) return MOE_ERR_UNSUPPORTED;
+  if (w->scale_dtype != MOE_SCALE_BF16 && w->scale_dtype != MOE_SCALE_FP16) return MOE_ERR_UNSUPPORTED;
+  if (w->layout != layout || !w->codes || !w->scales) return MOE_ERR_INVALID_ARG;
+  const void* al[] = {w->codes, w->scales, w->zeros};
+  for (const void* p : al)
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const char* p = static_cast<const char*>(a);
+  const char* q = static_cast<const char*>(b);
+  return p < q + nb && q < p + na;
+}
+}  // namespace
+
+int moe_route_scored(const float* logits, const float* bias, int T, int E, int k, const moe_scoring* scoring,
+                     int32_t* topk_ids, float* topk_w, hipStream_t stream) {
+  int st = check_route_shape(T, E, k);
+  if (!st) st = check_scoring(scoring, E, k, true);
+  if (st) return st;
+  if (T >= kMaxRowCount) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_route_scored(logits, bias, T, E, k, scoring_of(scoring), topk_ids, topk_w, stream));
+}
+
+int moe_route_scored_grad(const float* logits, const int32_t* topk_ids, const float* topk_w,
+                          const float* dtopk_w, int T, int E, int k, const moe_scoring* scoring,
+                          float* dlogits, hipStream_t stream) {
+  int st = check_route_shape(T, E, k);
+  if (!st) st = check_scoring(scoring, E, k, false);
+  if (st) return st;
+  if (T >= kMaxRowCount) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_w || !dtopk_w || !dlogits) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_route_scored_grad(logits, topk_ids, topk_w, dtopk_w, T, E, k, scoring_of(scoring),
+                                             dlogits, stream));
+}
+
+int moe_block_norm(const moe_block* block, const void* x, const void* residual, int T, int d, int act_dtype,
+                   void* h_out, void* y, void* q, void* q_scale, hipStream_t stream) {
+  int st = check_block(block, T);
+  int fmt = 0;
+  if (!st) st = norm_format(T, d, act_dtype, &fmt);
+  if (st || T == 0) return st;
+  if (!x || !residual || !block->pre_weight || !h_out) return MOE_ERR_INVALID_ARG;
+  if (fmt == 0 ? !y : (!q || !q_scale)) return MOE_ERR_INVALID_ARG;
+  const void* al[] = {x, residual, block->post_weight, block->gate, block->pre_weight, h_out, y, q};
+  for (const void* p : al)
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  const BlockIn in = block_in(block);
+  return hip_status(launch_rmsnorm(x, residual, block->pre_weight, block->eps, T, d, fmt, h_out, y, q,
+                                   q_scale, stream, &in));
+}
+
+size_t moe_block_norm_grad_workspace_bytes(int T, int d) {
+  if (T < 0 || d <= 0 || d % 8 || d > kMaxRowLenGrad || T >= kMaxRowCount) return 0;
+  Carver c{nullptr};
+  c.take<float>((size_t)block_grad_parts(T) * 2 * d);
+  return c.used;
+}
+
+int moe_block_norm_grad(const moe_block* block, const void* dy, const void* dh, const void* x, const void* h,
+                        int T, int d, void* dx, void* dresidual, float* dpre_weight, float* dpost_weight,
+                        void* dgate, void* ws, size_t ws_bytes, hipStream_t stream) {
+  int st = check_block(block, T);
+  if (st) return st;
+  if (T < 0 || d <= 0) return MOE_ERR_INVALID_ARG;
+  if (d % 8 || d > kMaxRowLenGrad || T >= kMaxRowCount) return MOE_ERR_UNSUPPORTED;
+  if ((dpost_weight && !block->post_weight) || (dgate && !block->gate)) return MOE_ERR_INVALID_ARG;
+  const bool sums = dpre_weight || dpost_weight || (dgate && !block->gate_per_token);
+  if (T == 0 && !sums) return MOE_OK;
+  if (T > 0 && (!dy || !x || !h || !block->pre_weight || !dx || !dresidual || dx == dresidual))
+    return MOE_ERR_INVALID_ARG;
+  const void* al[] = {dy, dh, x, h, block->post_weight, block->gate, block->pre_weight, dx, dresidual,
+                      dpre_weight, dpost_weight, dgate};
+  for (const void* p : al)
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (sums && T > 0) {
+    if (!ws || ws_bytes < moe_block_norm_grad_workspace_bytes(T, d)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  }
+  BlockGrad a;
+  std::memset(&a, 0, sizeof(a));
+  a.dy = dy; a.dh = dh; a.x = x; a.h = h;
+  a.pre = block->pre_weight;
+  a.in = block_in(block);
+  a.eps = block->eps;
+  a.T = T;
+  a.dx = dx;
+  a.dres = dresidual;
+  a.dpre = dpre_weight;
+  a.dpost = dpost_weight;
+  if (block->gate_per_token) a.dgate_rows = dgate;
+  else a.dgate = static_cast<float*>(dgate);
+  a.part = sums ? static_cast<float*>(ws) : nullptr;
+  return hip_status(launch_block_grad(a, d, stream));
+}
+
+int moe_w4_tile(const moe_w4* src, void* codes, void* scales, uint8_t* zeros, hipStream_t stream) {
+  int st = check_w4(src, MOE_LAYOUT_ROW_MAJOR);
+  if (st) return st;
+  if (!codes || !scales || !src->zeros != !zeros) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(zeros)) return MOE_ERR_INVALID_ARG;
+  const int64_t nc = (int64_t)src->N * src->K / 2, ng = (int64_t)src->N * (src->K / src->group);
+  const struct { const void* p; int64_t n; } in[] = {{src->codes, nc}, {src->scales, 2 * ng}, {src->zeros, ng}},
+                                             out[] = {{codes, nc}, {scales, 2 * ng}, {zeros, ng}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 3; ++j) {
+      if (in[i].p && out[j].p && overlap(in[i].p, in[i].n, out[j].p, out[j].n)) return MOE_ERR_INVALID_ARG;
+      if (i < j && out[j].p && overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return MOE_ERR_INVALID_ARG;
+    }
+  return hip_status(launch_w4_tile(W4Mat{src->codes, src->scales, src->zeros}, src->N, src->K, src->group,
+                                   codes, scales, zeros, stream));
+}
+
+int moe_gemm_w4(const void* x, int M, const moe_w4* w, const moe_w4* up, void* y, hipStream_t stream) {
+  if (M < 0) return MOE_ERR_INVALID_ARG;
+  int st = check_w4(w, MOE_LAYOUT_TILED);
+  if (!st && up) st = check_w4(up, MOE_LAYOUT_TILED);
+  if (st) return st;
+  if (up && (up->N != w->N || up->K != w->K || up->group != w->group || up->scale_dtype != w->scale_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if ((int64_t)M * w->K * 2 >= kMaxOffsetBytes) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !y || !aligned16(x) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  const int cus = device_cus();
+  if (cus == 0) return MOE_ERR_HIP;
+  W4Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.m[0] = W4Mat{w->codes, w->scales, w->zeros};
+  if (up) a.m[1] = W4Mat{up->codes, up->scales, up->zeros};
+  a.y = y;
+  a.M = M;
+  a.N = w->N;
+  a.K = w->K;
+  a.fp16 = w->scale_dtype == MOE_SCALE_FP16;
+  return hip_status(launch_gemm_w4(a, w->group, cus, stream));
 }
 
 // Workspace of the whole layer (see carve_layer for the order).

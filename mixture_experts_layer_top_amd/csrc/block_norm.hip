@@ -1,0 +1,283 @@
+// Gradient of the norms around a block (the forward pass is the norm kernel's, norm.hip).
+//
+//   u = x / sqrt(mean(x^2) + eps) * post,  h = rs * r + bs * gate * u,  y = h / sqrt(mean(h^2) + eps) * pre
+// with dy at y and dh at h:
+//   H = dh + r2 (dy pre - n2 mean(dy pre n2))             n2 = h r2, r2 = 1 / sqrt(mean(h^2) + eps)
+//   dr = rs H,  dgate = bs H u,  g1 = bs gate post H      n1 = x r1, r1 likewise
+//   dx = r1 (g1 - n1 mean(g1 n1))  (without a norm behind the block: bs gate H)
+//   dpre[c] = sum_t dy n2,  dpost[c] = sum_t bs gate H n1,  dgate[c] = sum_t bs H u for a gate per channel
+// A gate per channel is the same in all rows, so both of the last two come from one sum, of H n1.
+//
+// Bound by HBM: x, h, dy and dh are read once and dx, dr written once, 12 bytes a value; H stays in fp32
+// registers between the two norms.
+#include <algorithm>
+#include <type_traits>
+
+#include "kernels.h"
+#include "norm_dev.h"
+
+namespace moe {
+
+namespace {
+
+// 1 / sqrt(mean(v^2) + eps) of a row from its sum of squares, which is summed again in fp64 where it left
+// fp32's range; a small row's values are enlarged (norm_dev.h), `up` is then kSmallRow.
+template <int R, int V>
+__device__ __forceinline__ float rstd_of(uint4 (&v)[V], double sum, double inv_d, float eps, int i, int nvec,
+                                         double* red, float& up) {
+  up = 1.0f;
+  if (row_in_range(sum, inv_d, eps)) return row_rstd(sum, inv_d, eps);
+  double s[1] = {0.0};
+#pragma unroll
+  for (int q = 0; q < V; ++q)
+    if (i + R * q < nvec) add_squares(v[q], s[0]);
+  row_reduce<R>(s, red, SumOp{});
+  bool small;
+  const float r = wide_rstd(s[0], inv_d, eps, small);
+  if (small) {
+    up = kSmallRow;
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[q] = enlarged(v[q]);
+  }
+  return r;
+}
+
+// Whether fp32 products may have left their range on the way to this sum (a sum of 0, which rows without a
+// gradient have, stays).
+__device__ __forceinline__ bool out_of_range(double sum, double inv_d) {
+  const double m = fabs(sum) * inv_d;
+  return !(m < __builtin_inf()) || (m < 0x1p-100 && m > 0.0);
+}
+
+// sum += sum_j n[j] * x[j] in fp64, a value at a time in a loop that turns both (they end as they began): a
+// path that must not cost the other one registers.
+__device__ __forceinline__ void add_row_products(float (&n)[8], uint4 x, double& sum) {
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j) {
+    sum = fma((double)n[0], (double)bf16_lo(x.x), sum);
+    const float f = n[0];
+#pragma unroll
+    for (int c = 0; c < 7; ++c) n[c] = n[c + 1];
+    n[7] = f;
+    x = make_uint4((x.x >> 16) | (x.y << 16), (x.y >> 16) | (x.z << 16), (x.z >> 16) | (x.w << 16),
+                   (x.w >> 16) | (x.x << 16));
+  }
+}
+
+// Value j of a vector.
+__device__ __forceinline__ float value(const uint4& v, int j) {
+  const uint32_t p = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
+  return j & 1 ? bf16_hi(p) : bf16_lo(p);
+}
+
+// ROWS: a gate per token and channel, [T][d].
+template <int R, int V, bool ROWS>
+__global__ __launch_bounds__(R, 4) void block_grad_kernel(BlockGrad a, double inv_d, int nvec) {
+  __shared__ double red[2][7][R / 64];
+  const int i = threadIdx.x;
+  float sA[V][8], sP[V][8];
+#pragma unroll
+  for (int s = 0; s < V; ++s)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sA[s][j] = sP[s][j] = 0.f;
+  const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  int turn = 0;
+  for (int row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
+    // (a uniform address per row and array, and lane offsets that are opaque, since the compiler would keep
+    // their sums with every array's address instead: 20 registers a vector)
+    const size_t base = (size_t)row * nvec * 16;
+    auto rows = [&](const void* p, uint32_t off) { return gload16(static_cast<const char*>(p) + base, off); };
+    uint4 h[V], g[V], x[V], add[V], gt[V], wp[V], wq[V];
+    uint32_t at[V];
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      at[s] = min(i + R * s, nvec - 1) * 16;
+      asm volatile("" : "+v"(at[s]));
+      const uint32_t c = at[s];
+      h[s] = rows(a.h, c);
+      g[s] = rows(a.dy, c);
+      x[s] = rows(a.x, c);
+      // (what is absent is 0 or 1: no branches below)
+      add[s] = a.dh ? rows(a.dh, c) : make_uint4(0, 0, 0, 0);
+      gt[s] = ROWS ? rows(a.in.gate, c) : a.in.gate ? gload16(a.in.gate, c) : ones;
+      wp[s] = gload16(a.pre, c);
+      if (!ROWS) wq[s] = a.in.post ? gload16(a.in.post, c) : ones;
+    }
+    double sum[3] = {0.0, 0.0, 0.0};
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      float p = 0.f, c = 0.f, q = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float hv = value(h[s], j), xv = value(x[s], j);
+        p = fmaf(hv, hv, p);
+        c = fmaf(value(g[s], j) * value(wp[s], j), hv, c);
+        q = fmaf(xv, xv, q);
+        if (j & 1) __builtin_amdgcn_sched_barrier(0);  // (few unpacked values at a time)
+      }
+      if (i + R * s < nvec) {
+        sum[0] += (double)p;
+        sum[1] += (double)c;
+        sum[2] += (double)q;
+      }
+    }
+    // (two buffers in turn: a wavefront that is a row ahead writes the other one)
+    row_reduce<R>(sum, red[turn][0], SumOp{});
+    if (!row_in_range(sum[0], inv_d, a.eps) || out_of_range(sum[1], inv_d)) {
+      double c[1] = {0.0};
+#pragma unroll
+      for (int s = 0; s < V; ++s)
+        if (i + R * s < nvec) add_products(h[s], g[s], wp[s], c[0]);
+      row_reduce<R>(c, red[turn][3], SumOp{});
+      sum[1] = c[0];
+    }
+    float up2, up1 = 1.0f, r1 = 1.0f;
+    const float r2 = rstd_of<R, V>(h, sum[0], inv_d, a.eps, i, nvec, red[turn][4], up2);
+    const float c2 = float(sum[1] * inv_d * (double)up2 * (double)r2 * (double)r2);
+    if (a.in.post) r1 = rstd_of<R, V>(x, sum[2], inv_d, a.eps, i, nvec, red[turn][5], up1);
+    // (unpacked anew behind the sums: values kept across the branches would not fit the registers)
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      h[s] = opaque(h[s]);
+      g[s] = opaque(g[s]);
+      x[s] = opaque(x[s]);
+      if (!ROWS) wp[s] = opaque(wp[s]);
+    }
+    float n[V][8];  // the gradient that reaches the first norm (or x)
+    double back[1] = {0.0};
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      const bool in = i + R * s < nvec;
+      if (ROWS) {  // (no registers for them before)
+        __builtin_amdgcn_sched_barrier(0);
+        wp[s] = gload16(a.pre, at[s]);
+        wq[s] = a.in.post ? gload16(a.in.post, at[s]) : ones;
+      }
+      uint32_t dr[4], dg[4];
+      float q = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {  // (two values at a time: few live ones)
+        float r[2], t[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = 2 * w + e;
+          const float hv = value(h[s], j), gv = value(g[s], j), gate = value(gt[s], j), post = value(wq[s], j);
+          sP[s][j] = fmaf(gv, hv * r2, sP[s][j]);
+          const float H = fmaf(r2 * fmaf(-c2, hv, gv * value(wp[s], j)), up2, value(add[s], j));
+          const float n1 = value(x[s], j) * r1, bH = a.in.bs * H;
+          r[e] = a.in.rs * H;
+          if (ROWS) t[e] = bH * n1 * post;
+          sA[s][j] = fmaf(ROWS ? gate * H : H, n1, sA[s][j]);
+          n[s][j] = bH * gate * post;
+          q = fmaf(n[s][j], value(x[s], j), q);
+        }
+        // (the sums are taken here: moved to the row's end they would keep all their operands)
+        asm volatile("" : "+v"(sA[s][2 * w]), "+v"(sA[s][2 * w + 1]), "+v"(sP[s][2 * w]), "+v"(sP[s][2 * w + 1]));
+        dr[w] = pack_bf16x2(r[0], r[1]);
+        if (ROWS) dg[w] = pack_bf16x2(t[0], t[1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (in) {
+        const uint32_t c = at[s];
+        gstore16(static_cast<char*>(a.dres) + base, c, make_uint4(dr[0], dr[1], dr[2], dr[3]));
+        if (ROWS && a.dgate_rows)
+          gstore16(static_cast<char*>(a.dgate_rows) + base, c, make_uint4(dg[0], dg[1], dg[2], dg[3]));
+        back[0] += (double)q;
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < V; ++s) x[s] = opaque(x[s]);
+    float c1 = 0.f;
+    if (a.in.post) {
+      row_reduce<R>(back, red[turn][6], SumOp{});
+      if (out_of_range(back[0], inv_d)) {
+        back[0] = 0.0;
+#pragma unroll
+        for (int s = 0; s < V; ++s)
+          if (i + R * s < nvec) add_row_products(n[s], x[s], back[0]);
+        row_reduce<R>(back, red[turn][3], SumOp{});
+      }
+      // (of a small row, x and the sum hold `up` once, r1 its inverse)
+      c1 = float(back[0] * inv_d * (double)r1 * (double)r1);
+    }
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      float xv[8], o[8];
+      unpack8(x[s], xv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = a.in.post ? r1 * fmaf(-c1, xv[j], n[s][j]) * up1 : n[s][j];
+      if (i + R * s < nvec) gstore16(static_cast<char*>(a.dx) + base, at[s], pack8(o));
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int s = 0; s < V; ++s) {
+    const int idx = i + R * s;
+    if (idx >= nvec) continue;
+    float* p = a.part + ((size_t)blockIdx.x * 2 * nvec + idx) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      gstore16(p + j, 0, make_uint4(__float_as_uint(sA[s][j]), __float_as_uint(sA[s][j + 1]),
+                                    __float_as_uint(sA[s][j + 2]), __float_as_uint(sA[s][j + 3])));
+      gstore16(p + (size_t)nvec * 8 + j, 0,
+               make_uint4(__float_as_uint(sP[s][j]), __float_as_uint(sP[s][j + 1]),
+                          __float_as_uint(sP[s][j + 2]), __float_as_uint(sP[s][j + 3])));
+    }
+  }
+}
+
+// The workgroups' sums [nb][2][d] in a fixed order: 32 columns per workgroup, as dw_reduce_kernel in
+// norm.hip, then the factors that all rows share.
+__global__ __launch_bounds__(256) void block_grad_sum_kernel(BlockGrad a, int nb, int d) {
+  __shared__ float red[32][33];
+  const int c = threadIdx.x & 7, r = threadIdx.x >> 3, col = blockIdx.x * 32 + c * 4;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (col < 2 * d) {  // (d % 8 == 0)
+#pragma unroll 4
+    for (int b = r; b < nb; b += 32) {
+      const uint4 v = ld16(a.part, ((size_t)b * 2 * d + col) / 4);
+      s[0] += __uint_as_float(v.x);
+      s[1] += __uint_as_float(v.y);
+      s[2] += __uint_as_float(v.z);
+      s[3] += __uint_as_float(v.w);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) red[r][c * 4 + j] = s[j];
+  __syncthreads();
+  const int at = blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x >= 32 || at >= 2 * d) return;
+  float v = 0.f;
+  for (int b = 0; b < 32; ++b) v += red[b][threadIdx.x];
+  if (at >= d) {
+    if (a.dpre) a.dpre[at - d] = v;
+    return;
+  }
+  auto channel = [&](const void* p) { return bf16_to_f32(static_cast<const uint16_t*>(p)[at]); };
+  if (a.dpost) a.dpost[at] = a.in.bs * (a.in.gate && !a.in.gate_rows ? channel(a.in.gate) * v : v);
+  if (a.dgate) a.dgate[at] = a.in.bs * (a.in.post ? channel(a.in.post) * v : v);
+}
+
+}  // namespace
+
+int block_grad_parts(int T) { return rmsnorm_grad_parts(T); }
+
+hipError_t launch_block_grad(const BlockGrad& a, int d, hipStream_t s) {
+  const int nvec = d / 8, nb = block_grad_parts(a.T);
+  if (a.T > 0) {
+    auto go = [&](auto Rc, auto Vc) {
+      constexpr int R = decltype(Rc)::value, V = decltype(Vc)::value;
+      auto* kernel = a.in.gate_rows ? &block_grad_kernel<R, V, true> : &block_grad_kernel<R, V, false>;
+      kernel<<<nb, R, 0, s>>>(a, 1.0 / d, nvec);
+    };
+    if (nvec <= 64) go(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 128) go(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
+    else if (nvec <= 512) with_steps<256, 1, 2>((nvec + 255) / 256, go);
+    else if (nvec <= 1024) go(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  }
+  if (a.dpre || a.dpost || a.dgate) block_grad_sum_kernel<<<(2 * d + 31) / 32, 256, 0, s>>>(a, nb, d);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -256,8 +256,17 @@ hipError_t launch_quant_i8(const void* x, bool f32, int T, int d, uint8_t* q, fl
 
 // RMS norm (fmt: 0 bf16 only, 1 e4m3 per 128, 2 e4m3 with E8M0 per 32, 3 int8 rows) and its gradient
 // (part: rmsnorm_grad_parts(T) rows of d partial sums, unused when dw is null).
+// What a block's output passes before the residual is added (null pointers: no such step).
+struct BlockIn {
+  const void* post;  // weight of the norm behind the block, [d]
+  const void* gate;  // [d], or [T][d] with gate_rows
+  int gate_rows;
+  float rs, bs;
+};
+// b: a block norm (x is the block's output, res the residual, which it needs), else null.
 hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float eps, int T, int d,
-                          int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s);
+                          int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s,
+                          const BlockIn* b = nullptr);
 constexpr int kNormGradBlocks = 512;
 constexpr int kNormGradRows = 3;  // per workgroup, until there are that many
 int rmsnorm_grad_parts(int T);
@@ -271,5 +280,49 @@ hipError_t launch_combine_grad(const void* dout, const void* y, const int32_t* s
                                hipStream_t s);
 hipError_t launch_route_grad(const int32_t* ids, const float* w, const float* dw, int T, int E,
                              int k, float* dl, hipStream_t s);
+
+// Gradient of the block norm: in.gate_rows as in the forward call, dgate_rows [T][d] bf16 then (else dgate
+// [d]); part: block_grad_parts(T) rows of 2 d partial sums, null when dpre, dpost and dgate are.
+struct BlockGrad {
+  const void* dy; const void* dh; const void* x; const void* h;
+  const void* pre;
+  BlockIn in;
+  float eps;
+  int T;
+  void* dx; void* dres; void* dgate_rows;
+  float* dpre; float* dpost; float* dgate;
+  float* part;
+};
+int block_grad_parts(int T);
+hipError_t launch_block_grad(const BlockGrad& a, int d, hipStream_t s);
+
+// Routing by scores.
+enum ScoreFn { kScoreSoftmax = 0, kScoreSigmoid = 1 };
+constexpr int kMaxGroups = 64;
+struct Scoring {
+  int score, groups, top, group_top, renorm;
+  float scale;
+};
+hipError_t launch_route_scored(const float* logits, const float* bias, int T, int E, int k,
+                               const Scoring& p, int32_t* ids, float* w, hipStream_t s);
+hipError_t launch_route_scored_grad(const float* logits, const int32_t* ids, const float* w,
+                                    const float* dw, int T, int E, int k, const Scoring& p, float* dl,
+                                    hipStream_t s);
+
+// 4-bit weights: x [M][K] bf16 by one matrix, or by the gate and up pair (m[1].codes not null), tiled.
+struct W4Mat {
+  const void* codes; const void* scales; const uint8_t* zeros;  // (zeros null: 8)
+};
+struct W4Args {
+  const void* x;
+  W4Mat m[2];
+  void* y;
+  int M, N, K;
+  int fp16;    // the scales' type (else bf16)
+  int mtiles;  // (the launch's)
+};
+hipError_t launch_gemm_w4(const W4Args& a, int group, int num_cus, hipStream_t s);
+hipError_t launch_w4_tile(const W4Mat& src, int N, int K, int group, void* codes, void* scales, uint8_t* zeros,
+                          hipStream_t s);
 
 }  // namespace moe

@@ -19,81 +19,83 @@
 
 #include "kernels.h"
 #include "mx_codec.h"
-#include "rows_dev.h"
+#include "norm_dev.h"
 
 namespace moe {
 
 namespace {
 
-enum NormFormat { kNormBf16 = 0, kNormFp8 = 1, kNormMx = 2, kNormI8 = 3 };
-
-// Four e4m3 codes in a dword, by the conversion instruction: to nearest, ties to even, the sign kept.
-// It equals e4m3_encode on values up to 448 in magnitude and does not saturate above 464, so the caller
-// limits its values.
-__device__ __forceinline__ uint32_t e4m3_pack4(const float* v) {
-  int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], p, true);
-}
-
-// A vector through an opaque move (computations on it stay where they are written).
-__device__ __forceinline__ uint4 opaque(uint4 v) {
-  asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
-  return v;
-}
-
-// Whether fp32 held the squares of a row: its mean square (with eps) is finite and so far above
-// the smallest float that what underflowed does not count (2^-149 a term against 2^-100).
-__device__ __forceinline__ bool row_in_range(double sum, double inv_d, float eps) {
-  const float m = float(sum * inv_d) + eps;
-  return m >= 0x1p-100f && m < __uint_as_float(kInfBits);
-}
-// 1 / sqrt(sum / d + eps) of a row in range.
-__device__ __forceinline__ float row_rstd(double sum, double inv_d, float eps) {
-  return 1.0f / sqrtf(float(sum * inv_d) + eps);
-}
-// The same of any row, from squares summed in fp64 (which bf16's never leave): for a small row the value
-// over 2^32, which kSmallRow times the row's values make good; NaN for a row that holds an infinity or
-// NaN, so that the whole row shows it (and for a zero row without eps, 0 / 0).
-constexpr float kSmallRow = 0x1p32f;
-__device__ __forceinline__ float wide_rstd(double sum, double inv_d, float eps, bool& small) {
-  const double m = sum * inv_d + (double)eps;
-  small = m < 0x1p-100;
-  if (small) return 0x1p68f / sqrtf(float(m * 0x1p200));
-  if (m <= 0x1p100) return 1.0f / sqrtf(float(m));  // (the gradient's products may leave the range alone)
-  return m < __builtin_inf() ? 0x1p-100f / sqrtf(float(m * 0x1p-200)) : __uint_as_float(0x7FC00000u);
-}
-
-// The wide sums of a row out of range, two values at a time in a loop, and its values times kSmallRow
-// (exact: a small row's are below 2^-42): a path that must not cost the other one registers.
-__device__ __forceinline__ float bf16_lo(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
-__device__ __forceinline__ uint4 turned(const uint4& v) { return make_uint4(v.y, v.z, v.w, v.x); }
-__device__ __forceinline__ void add_squares(uint4 h, double& sum) {
-#pragma unroll 1
-  for (int j = 0; j < 4; ++j, h = turned(h)) {
-    const double a = bf16_lo(h.x), b = bf16_hi(h.x);
-    sum = fma(b, b, fma(a, a, sum));
+// hv: the block's output x in, the new residual stream h out; rv: the residual.
+template <int R, int V>
+__device__ __forceinline__ void block_stream(uint4 (&hv)[V], const uint4 (&rv)[V], const BlockIn& b, float eps,
+                                             double inv_d, int i, int nvec, size_t base,
+                                             double (*red)[R / 64]) {
+  uint4 gv[V], pv[V];
+  if (b.gate) {
+#pragma unroll
+    for (int s = 0; s < V; ++s) gv[s] = ld16(b.gate, (b.gate_rows ? base : 0) + min(i + R * s, nvec - 1));
+  }
+  float rstd = 1.0f;
+  if (b.post) {
+#pragma unroll
+    for (int s = 0; s < V; ++s) pv[s] = ld16(b.post, min(i + R * s, nvec - 1));
+    double sum[1] = {0.0};
+#pragma unroll
+    for (int s = 0; s < V; ++s) {
+      float v[8];
+      unpack8(hv[s], v);
+      float p = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p = fmaf(v[j], v[j], p);
+      if (i + R * s < nvec) sum[0] += (double)p;
+    }
+    row_reduce<R>(sum, red[0], SumOp{});
+    rstd = row_rstd(sum[0], inv_d, eps);
+    if (!row_in_range(sum[0], inv_d, eps)) {  // (the same in all threads of the row)
+      sum[0] = 0.0;
+#pragma unroll
+      for (int s = 0; s < V; ++s)
+        if (i + R * s < nvec) add_squares(hv[s], sum[0]);
+      row_reduce<R>(sum, red[1], SumOp{});
+      bool small;
+      rstd = wide_rstd(sum[0], inv_d, eps, small);
+      if (small) {
+#pragma unroll
+        for (int s = 0; s < V; ++s) hv[s] = enlarged(hv[s]);
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < V; ++s) {
+    float v[8], r[8];
+    unpack8(hv[s], v);
+    unpack8(rv[s], r);
+    if (b.post) {
+      float p[8];
+      unpack8(pv[s], p);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * p[j];
+    }
+    if (b.gate) {
+      float g[8];
+      unpack8(gv[s], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= g[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = fmaf(b.bs, v[j], b.rs * r[j]);
+    hv[s] = pack8(v);
   }
 }
-__device__ __forceinline__ void add_products(uint4 h, uint4 g, uint4 w, double& sum) {
-#pragma unroll 1
-  for (int j = 0; j < 4; ++j, h = turned(h), g = turned(g), w = turned(w)) {
-    sum = fma((double)bf16_lo(g.x) * (double)bf16_lo(w.x), (double)bf16_lo(h.x), sum);
-    sum = fma((double)bf16_hi(g.x) * (double)bf16_hi(w.x), (double)bf16_hi(h.x), sum);
-  }
-}
-__device__ __forceinline__ uint4 enlarged(uint4 h) {
-#pragma unroll 1
-  for (int j = 0; j < 4; ++j, h = turned(h))
-    h.x = pack_bf16x2(bf16_lo(h.x) * kSmallRow, bf16_hi(h.x) * kSmallRow);
-  return h;
-}
 
-template <int FMT, int R, int V>
+// BLOCK (moe_block_norm): x is a block's output and h = bf16(rs * residual + bs * gate * u), u = x, or
+// x / sqrt(mean(x^2) + eps) * post where there is a norm behind the block.  All of it stays in fp32 up to
+// the one rounding of h; the rest of the row's way is the same.
+template <int FMT, int R, int V, bool BLOCK>
 __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
     const void* x, const void* res, const void* __restrict__ w, float eps, double inv_d, int T,
-    int nvec, void* h_out, void* y, uint8_t* q, void* qs) {
-  __shared__ double red[2][R / 64];
+    int nvec, void* h_out, void* y, uint8_t* q, void* qs, BlockIn b) {
+  __shared__ double red[BLOCK ? 4 : 2][R / 64];
   __shared__ uint32_t redm[R / 64];
   const int row = R == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (R == 64 && row >= T) return;  // (whole wavefronts; no barrier in this form)
@@ -106,6 +108,7 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
 #pragma unroll
     for (int s = 0; s < V; ++s) rv[s] = ld16(res, base + min(i + R * s, nvec - 1));
   }
+  if constexpr (BLOCK) block_stream<R, V>(hv, rv, b, eps, inv_d, i, nvec, base, red + 2);
 #pragma unroll
   for (int s = 0; s < V; ++s) wr[s] = ld16(w, min(i + R * s, nvec - 1));
   double sum[1] = {0.0};
@@ -114,7 +117,7 @@ __global__ __launch_bounds__(row_block(R)) void rmsnorm_kernel(
     const bool in = i + R * s < nvec;
     float h[8];
     unpack8(hv[s], h);
-    if (res) {
+    if (!BLOCK && res) {
       float r[8];
       unpack8(rv[s], r);
 #pragma unroll
@@ -430,15 +433,18 @@ __global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict_
 }  // namespace
 
 hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float eps, int T, int d,
-                          int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s) {
+                          int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s,
+                          const BlockIn* b) {
   if (T == 0) return hipSuccess;
   const int nvec = d / 8;
   with_row_shape(nvec, T <= kFewRows, [&](auto Rc, auto Vc) {
     constexpr int R = decltype(Rc)::value, V = decltype(Vc)::value;
     const unsigned grid = R == 64 ? ((unsigned)T + 3) / 4 : (unsigned)T;
     auto go = [&](auto F) {
-      rmsnorm_kernel<decltype(F)::value, R, V><<<grid, row_block(R), 0, s>>>(
-          x, res, w, eps, 1.0 / d, T, nvec, h_out, y, static_cast<uint8_t*>(q), qs);
+      auto* kernel = b ? &rmsnorm_kernel<decltype(F)::value, R, V, true>
+                       : &rmsnorm_kernel<decltype(F)::value, R, V, false>;
+      kernel<<<grid, row_block(R), 0, s>>>(x, res, w, eps, 1.0 / d, T, nvec, h_out, y,
+                                           static_cast<uint8_t*>(q), qs, b ? *b : BlockIn{});
     };
     if (fmt == kNormFp8) go(std::integral_constant<int, kNormFp8>{});
     else if (fmt == kNormMx) go(std::integral_constant<int, kNormMx>{});

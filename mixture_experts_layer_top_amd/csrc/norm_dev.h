@@ -1,0 +1,73 @@
+// Pieces of the norm kernels (norm.hip, block_norm.hip): a row's reciprocal root in and out of fp32's
+// range, and conversions.
+#pragma once
+
+#include "rows_dev.h"
+
+namespace moe {
+
+enum NormFormat { kNormBf16 = 0, kNormFp8 = 1, kNormMx = 2, kNormI8 = 3 };
+
+// Four e4m3 codes in a dword, by the conversion instruction: to nearest, ties to even, the sign kept.
+// It equals e4m3_encode on values up to 448 in magnitude and does not saturate above 464, so the caller
+// limits its values.
+__device__ __forceinline__ uint32_t e4m3_pack4(const float* v) {
+  int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], p, true);
+}
+
+// A vector through an opaque move (computations on it stay where they are written).
+__device__ __forceinline__ uint4 opaque(uint4 v) {
+  asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+  return v;
+}
+
+// Whether fp32 held the squares of a row: its mean square (with eps) is finite and so far above
+// the smallest float that what underflowed does not count (2^-149 a term against 2^-100).
+__device__ __forceinline__ bool row_in_range(double sum, double inv_d, float eps) {
+  const float m = float(sum * inv_d) + eps;
+  return m >= 0x1p-100f && m < __uint_as_float(kInfBits);
+}
+// 1 / sqrt(sum / d + eps) of a row in range.
+__device__ __forceinline__ float row_rstd(double sum, double inv_d, float eps) {
+  return 1.0f / sqrtf(float(sum * inv_d) + eps);
+}
+// The same of any row, from squares summed in fp64 (which bf16's never leave): for a small row the value
+// over 2^32, which kSmallRow times the row's values make good; NaN for a row that holds an infinity or
+// NaN, so that the whole row shows it (and for a zero row without eps, 0 / 0).
+constexpr float kSmallRow = 0x1p32f;
+__device__ __forceinline__ float wide_rstd(double sum, double inv_d, float eps, bool& small) {
+  const double m = sum * inv_d + (double)eps;
+  small = m < 0x1p-100;
+  if (small) return 0x1p68f / sqrtf(float(m * 0x1p200));
+  if (m <= 0x1p100) return 1.0f / sqrtf(float(m));  // (the gradient's products may leave the range alone)
+  return m < __builtin_inf() ? 0x1p-100f / sqrtf(float(m * 0x1p-200)) : __uint_as_float(0x7FC00000u);
+}
+
+// The wide sums of a row out of range, two values at a time in a loop, and its values times kSmallRow
+// (exact: a small row's are below 2^-42): a path that must not cost the other one registers.
+__device__ __forceinline__ float bf16_lo(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
+__device__ __forceinline__ uint4 turned(const uint4& v) { return make_uint4(v.y, v.z, v.w, v.x); }
+__device__ __forceinline__ void add_squares(uint4 h, double& sum) {
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j, h = turned(h)) {
+    const double a = bf16_lo(h.x), b = bf16_hi(h.x);
+    sum = fma(b, b, fma(a, a, sum));
+  }
+}
+__device__ __forceinline__ void add_products(uint4 h, uint4 g, uint4 w, double& sum) {
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j, h = turned(h), g = turned(g), w = turned(w)) {
+    sum = fma((double)bf16_lo(g.x) * (double)bf16_lo(w.x), (double)bf16_lo(h.x), sum);
+    sum = fma((double)bf16_hi(g.x) * (double)bf16_hi(w.x), (double)bf16_hi(h.x), sum);
+  }
+}
+__device__ __forceinline__ uint4 enlarged(uint4 h) {
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j, h = turned(h))
+    h.x = pack_bf16x2(bf16_lo(h.x) * kSmallRow, bf16_hi(h.x) * kSmallRow);
+  return h;
+}
+
+}  // namespace moe

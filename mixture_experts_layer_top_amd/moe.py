@@ -22,6 +22,8 @@ CONFIG_AUTO, CONFIG_STREAM, CONFIG_MFMA, CONFIG_FUSED = -1, 0, 1, 2
 FUSED_SYNC_BYTES = 36864    # the fused single-token launch's counters at the workspace's start
 CONFIG_POLICY0, NUM_POLICIES = 16, 8  # config = 16 + i forces selection policy i (bf16)
 LAYOUT_ROW_MAJOR, LAYOUT_TILED = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCALE_BF16, SCALE_FP16 = 0, 1
 
 _vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 
@@ -40,6 +42,22 @@ WEIGHT_POINTERS = ("w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down",
 
 class Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in WEIGHT_POINTERS] + [("layout", ctypes.c_int32)]
+
+
+class Scoring(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "groups", "top_groups", "group_top", "renorm")] + [
+        ("scale", ctypes.c_float)]
+
+
+class Block(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("post_weight", "gate", "pre_weight")] + [
+        ("gate_per_token", ctypes.c_int32)] + [
+        (n, ctypes.c_float) for n in ("residual_scale", "branch_scale", "eps")]
+
+
+class W4(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "zeros")] + [
+        (n, ctypes.c_int32) for n in ("N", "K", "group", "scale_dtype", "layout")]
 
 
 class Routing(ctypes.Structure):
@@ -90,6 +108,14 @@ def lib() -> ctypes.CDLL:
             "moe_route_grad": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
             "moe_combine_grad": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp]),
             "moe_permute_grad": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
+            "moe_route_scored": (_i, [_vp, _vp, _i, _i, _i, ctypes.POINTER(Scoring), _vp, _vp, _vp]),
+            "moe_route_scored_grad": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, ctypes.POINTER(Scoring), _vp, _vp]),
+            "moe_block_norm": (_i, [ctypes.POINTER(Block), _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+            "moe_block_norm_grad": (_i, [ctypes.POINTER(Block), _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp,
+                                         _vp, _vp, _sz, _vp]),
+            "moe_block_norm_grad_workspace_bytes": (_sz, [_i, _i]),
+            "moe_w4_tile": (_i, [ctypes.POINTER(W4), _vp, _vp, _vp, _vp]),
+            "moe_gemm_w4": (_i, [_vp, _i, ctypes.POINTER(W4), ctypes.POINTER(W4), _vp, _vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -104,7 +130,9 @@ EXPORTED = ("moe_route", "moe_permute", "moe_permute_workspace_bytes", "moe_quan
             "moe_layer_workspace_bytes", "moe_layer_traced", "moe_status_string", "moe_mxfp4_tile",
             "moe_fp8_tile", "moe_layer_noalloc", "moe_quant_act_i8", "moe_gemm_i8", "moe_rmsnorm",
             "moe_rmsnorm_grad", "moe_rmsnorm_grad_workspace_bytes", "moe_route_grad",
-            "moe_combine_grad", "moe_permute_grad")
+            "moe_combine_grad", "moe_permute_grad", "moe_route_scored", "moe_route_scored_grad",
+            "moe_block_norm", "moe_block_norm_grad", "moe_block_norm_grad_workspace_bytes", "moe_w4_tile",
+            "moe_gemm_w4")
 
 NOALLOC_SCRATCH_BYTES = 128 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -304,7 +332,7 @@ def combine(y_perm, slot_dst, topk_w, shared_y=None):
 
 
 # ------------------------------------------------------------------------------------------------
-# int8 products, RMS norm, gradients
+# int8 and 4-bit products, RMS norms, routing by scores, gradients
 #
 # bf16 tensors are torch.bfloat16 or their bits as torch.int16, like the rest of this module's; outputs
 # take the input's choice.  Tensors must be contiguous and on one GPU, which need not be the current
@@ -390,23 +418,9 @@ def gemm_i8(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_scale: torch.
     return y
 
 
-def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
-            eps: float = 1e-6, act_dtype: int = DTYPE_BF16, want_y: bool = True):
-    """RMS norm of h = x + residual.  Returns (h, y, q, q_scale): h is x itself without a residual, y is
-    None when not wanted (8-bit outputs only), q and q_scale are y in the format act_dtype (DTYPE_FP8: e4m3
-    uint8 and fp32 [T, d/128]; DTYPE_INT8: int8 and fp32 [T]: what permute and grouped_ffn take;
-    DTYPE_MXFP4_A8: e4m3 and E8M0 uint8 [T, d/32], as quant_act_mx writes them, which no call here takes;
-    DTYPE_BF16: None).  The outputs carry no autograd history (rmsnorm_grad is the gradient)."""
-    T, d = _rows(x, "x")
-    dev = x.get_device()
-    _arg(x, "x", (T, d), _BF16, dev)
-    _arg(weight, "weight", (d,), _BF16, dev)
-    h, y, q, qs = x, None, None, None
-    rp = hp = yp = qp = sp = None
-    if residual is not None:
-        _arg(residual, "residual", (T, d), _BF16, dev)
-        h = torch.empty_like(x)
-        rp, hp = residual.data_ptr(), h.data_ptr()
+def _norm_outputs(x, T, d, act_dtype, want_y):
+    """A norm call's (y, q, q_scale), None where not wanted, and their addresses."""
+    y = q = qs = yp = qp = sp = None
     if want_y or act_dtype == DTYPE_BF16:
         y = torch.empty_like(x)
         yp = y.data_ptr()
@@ -420,6 +434,26 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None
             q = torch.empty_like(x, dtype=torch.uint8)
             qs = x.new_empty((T, d // 32), dtype=torch.uint8)
         qp, sp = q.data_ptr(), qs.data_ptr()
+    return y, q, qs, yp, qp, sp
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+            eps: float = 1e-6, act_dtype: int = DTYPE_BF16, want_y: bool = True):
+    """RMS norm of h = x + residual.  Returns (h, y, q, q_scale): h is x itself without a residual, y is
+    None when not wanted (8-bit outputs only), q and q_scale are y in the format act_dtype (DTYPE_FP8: e4m3
+    uint8 and fp32 [T, d/128]; DTYPE_INT8: int8 and fp32 [T]: what permute and grouped_ffn take;
+    DTYPE_MXFP4_A8: e4m3 and E8M0 uint8 [T, d/32], as quant_act_mx writes them, which no call here takes;
+    DTYPE_BF16: None).  The outputs carry no autograd history (rmsnorm_grad is the gradient)."""
+    T, d = _rows(x, "x")
+    dev = x.get_device()
+    _arg(x, "x", (T, d), _BF16, dev)
+    _arg(weight, "weight", (d,), _BF16, dev)
+    h, rp, hp = x, None, None
+    if residual is not None:
+        _arg(residual, "residual", (T, d), _BF16, dev)
+        h = torch.empty_like(x)
+        rp, hp = residual.data_ptr(), h.data_ptr()
+    y, q, qs, yp, qp, sp = _norm_outputs(x, T, d, act_dtype, want_y)
     _run("moe_rmsnorm", dev, x.data_ptr(), rp, weight.data_ptr(), eps, T, d, act_dtype, hp, yp, qp, sp)
     return h, y, q, qs
 
@@ -490,6 +524,156 @@ def permute_grad(dx_perm: torch.Tensor, slot_dst: torch.Tensor, k: int, add: tor
     _run("moe_permute_grad", dev, dx_perm.data_ptr(), slot_dst.data_ptr(), _ptr(add), T, k, d,
          dx.data_ptr())
     return dx
+
+
+def _scoring(score, renorm, scale, groups=1, top_groups=1, group_top=1):
+    return Scoring(score, groups, top_groups, group_top, 1 if renorm else 0, scale)
+
+
+def route_scored(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: int = SCORE_SIGMOID,
+                 groups: int = 1, top_groups: int = 1, group_top: int = 1, renorm: bool = True,
+                 scale: float = 1.0):
+    """Routing by scores (SCORE_SIGMOID, or SCORE_SOFTMAX over all experts): fp32 logits [T, E] and bias [E]
+    -> ids int32 [T, k], the experts with the largest score + bias among the top_groups best of `groups`
+    groups (valued by the sum of their group_top largest), and w fp32 [T, k], scale times their scores,
+    renormalised over the k if wanted.  Experts with a logit of -inf are masked."""
+    T, E = _rows(logits, "logits")
+    dev = logits.get_device()
+    _arg(logits, "logits", (T, E), _F32, dev)
+    bp = None
+    if bias is not None:
+        _arg(bias, "bias", (E,), _F32, dev)
+        bp = bias.data_ptr()
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    w = logits.new_empty((T, k))
+    _run("moe_route_scored", dev, logits.data_ptr(), bp, T, E, k,
+         _scoring(score, renorm, scale, groups, top_groups, group_top), ids.data_ptr(), w.data_ptr())
+    return ids, w
+
+
+def route_scored_grad(logits: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, dw: torch.Tensor,
+                      score: int = SCORE_SIGMOID, renorm: bool = True, scale: float = 1.0):
+    """Gradient of route_scored's weights: its logits [T, E], ids and w, and dw [T, k] -> dlogits fp32 [T, E]."""
+    T, E = _rows(logits, "logits")
+    k = _rows(ids, "ids")[1]
+    dev = logits.get_device()
+    _arg(logits, "logits", (T, E), _F32, dev)
+    _arg(ids, "ids", (T, k), _I32, dev)
+    _arg(w, "w", (T, k), _F32, dev)
+    _arg(dw, "dw", (T, k), _F32, dev)
+    dl = torch.empty_like(logits)
+    _run("moe_route_scored_grad", dev, logits.data_ptr(), ids.data_ptr(), w.data_ptr(), dw.data_ptr(), T, E, k,
+         _scoring(score, renorm, scale), dl.data_ptr())
+    return dl
+
+
+def _block(T, d, dev, pre_weight, post_weight, gate, residual_scale, branch_scale, eps):
+    """The Block of a call and whether its gate has a row per token."""
+    _arg(pre_weight, "pre_weight", (d,), _BF16, dev)
+    if post_weight is not None:
+        _arg(post_weight, "post_weight", (d,), _BF16, dev)
+    rows = gate is not None and gate.dim() == 2
+    if gate is not None:
+        _arg(gate, "gate", (T, d) if rows else (d,), _BF16, dev)
+    return Block(_ptr(post_weight), _ptr(gate), pre_weight.data_ptr(), 1 if rows else 0, residual_scale,
+                 branch_scale, eps), rows
+
+
+def block_norm(x: torch.Tensor, residual: torch.Tensor, pre_weight: torch.Tensor,
+               post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+               residual_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-6,
+               act_dtype: int = DTYPE_BF16, want_y: bool = True):
+    """From a block's output x to the next block's input: h = residual_scale * residual + branch_scale * gate
+    * (the RMS norm of x with post_weight, or x), y = the RMS norm of h with pre_weight.  gate: [d], or
+    [T, d].  Returns (h, y, q, q_scale) as rmsnorm does."""
+    T, d = _rows(x, "x")
+    dev = x.get_device()
+    _arg(x, "x", (T, d), _BF16, dev)
+    _arg(residual, "residual", (T, d), _BF16, dev)
+    b, _ = _block(T, d, dev, pre_weight, post_weight, gate, residual_scale, branch_scale, eps)
+    h = torch.empty_like(x)
+    y, q, qs, yp, qp, sp = _norm_outputs(x, T, d, act_dtype, want_y)
+    _run("moe_block_norm", dev, b, x.data_ptr(), residual.data_ptr(), T, d, act_dtype, h.data_ptr(), yp, qp, sp)
+    return h, y, q, qs
+
+
+def block_norm_grad(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, pre_weight: torch.Tensor,
+                    dh: torch.Tensor | None = None, post_weight: torch.Tensor | None = None,
+                    gate: torch.Tensor | None = None, residual_scale: float = 1.0, branch_scale: float = 1.0,
+                    eps: float = 1e-6, want_sums: bool = True):
+    """Gradient of block_norm's y (and of its h, dh), with the forward call's x and h.  Returns (dx,
+    dresidual, dpre_weight, dpost_weight, dgate): [T, d] the first two, fp32 [d] the next two (None without a
+    post_weight), dgate fp32 [d], [T, d] in the gate's type, or None without one.  Without want_sums those of
+    [d] are None."""
+    T, d = _rows(dy, "dy")
+    dev = dy.get_device()
+    for name, t in (("dy", dy), ("x", x), ("h", h)) + (() if dh is None else (("dh", dh),)):
+        _arg(t, name, (T, d), _BF16, dev)
+    b, rows = _block(T, d, dev, pre_weight, post_weight, gate, residual_scale, branch_scale, eps)
+    dx, dres = torch.empty_like(dy), torch.empty_like(dy)
+    dpre = dpost = dgate = ws = None
+    nws = 0
+    if rows:
+        dgate = torch.empty_like(gate)
+    if want_sums:
+        dpre = dy.new_empty(d, dtype=torch.float32)
+        if post_weight is not None:
+            dpost = torch.empty_like(dpre)
+        if gate is not None and not rows:
+            dgate = torch.empty_like(dpre)
+        nws = lib().moe_block_norm_grad_workspace_bytes(T, d)
+        ws = dy.new_empty(nws, dtype=torch.uint8) if nws else None
+    _run("moe_block_norm_grad", dev, b, dy.data_ptr(), _ptr(dh), x.data_ptr(), h.data_ptr(), T, d, dx.data_ptr(),
+         dres.data_ptr(), _ptr(dpre), _ptr(dpost), _ptr(dgate), _ptr(ws), nws)
+    return dx, dres, dpre, dpost, dgate
+
+
+@dataclass
+class W4Weights:
+    """4-bit weights [N, K] in the library's layout, from w4_tile."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    zeros: torch.Tensor | None
+    N: int
+    K: int
+    group: int
+
+    def struct(self, layout: int = LAYOUT_TILED) -> W4:
+        fmt = SCALE_FP16 if self.scales.dtype == torch.float16 else SCALE_BF16
+        return W4(_ptr(self.codes), _ptr(self.scales), _ptr(self.zeros), self.N, self.K, self.group, fmt, layout)
+
+
+def w4_tile(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None) -> W4Weights:
+    """4-bit weights for gemm_w4, laid out once at load time: codes uint8 [N, K/2] (0..15, the even element in
+    the low half of a byte), scales bf16 or fp16 [N, K/group], zeros uint8 [N, K/group] (None: 8)."""
+    N, half = _rows(codes, "codes")
+    K, G = 2 * half, _rows(scales, "scales")[1]
+    dev = codes.get_device()
+    _arg(codes, "codes", (N, half), (torch.uint8,), dev)
+    _arg(scales, "scales", (N, G), (torch.bfloat16, torch.float16), dev)
+    if G < 1 or K % G:
+        raise MoEError(f"scales has {G} columns, not a divisor of K = {K}")
+    if zeros is not None:
+        _arg(zeros, "zeros", (N, G), (torch.uint8,), dev)
+    out = W4Weights(torch.empty_like(codes), torch.empty_like(scales),
+                    None if zeros is None else torch.empty_like(zeros), N, K, K // G)
+    src = W4Weights(codes, scales, zeros, N, K, K // G)
+    _run("moe_w4_tile", dev, src.struct(LAYOUT_ROW_MAJOR), out.codes.data_ptr(), out.scales.data_ptr(),
+         _ptr(out.zeros))
+    return out
+
+
+def gemm_w4(x: torch.Tensor, w: W4Weights, up: W4Weights | None = None):
+    """bf16 [M, N] = x [M, K] w^T with 4-bit weights from w4_tile; with `up`, SiLU(x w^T) * (x up^T)."""
+    M, K = _rows(x, "x")
+    dev = x.get_device()
+    _arg(x, "x", (M, w.K), _BF16, dev)
+    for m in (w, up):
+        if m is not None and m.codes.get_device() != dev:
+            raise MoEError(f"w must live on GPU {dev}, not on {m.codes.device}")
+    y = x.new_empty((M, w.N))
+    _run("moe_gemm_w4", dev, x.data_ptr(), M, w.struct(), None if up is None else up.struct(), y.data_ptr())
+    return y
 
 
 class Layer:

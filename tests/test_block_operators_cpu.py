@@ -1,0 +1,182 @@
+"""Refusals of routing by scores, the block norms and the 4-bit products: on the host, before any GPU work."""
+import ctypes
+
+import pytest
+import torch
+
+from mixture_experts_layer_top_amd import moe
+
+OK, INV, UNS, WS = moe.MOE_OK, moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED, moe.MOE_ERR_WORKSPACE
+A = 4096  # stands for an aligned device pointer; no call here gets as far as using it
+
+
+@pytest.fixture(scope="module")
+def L():
+    return moe.lib()
+
+
+def scoring(score=moe.SCORE_SIGMOID, groups=1, top_groups=1, group_top=1, renorm=1, scale=1.0):
+    return moe.Scoring(score, groups, top_groups, group_top, renorm, scale)
+
+
+def test_route_scored_refusals(L):
+    def call(l=A, b=None, T=2, E=16, k=4, ids=A, w=A, sc=None, **kw):
+        return L.moe_route_scored(l, b, T, E, k, scoring(**kw) if sc is None else sc, ids, w, None)
+
+    assert call(T=0) == OK
+    assert call(T=-1) == INV and call(E=0) == INV and call(k=0) == INV
+    assert call(k=9) == UNS and call(E=513) == UNS and call(E=3) == UNS and call(T=1 << 25) == UNS
+    for name in ("l", "ids", "w"):
+        assert call(**{name: None}) == INV
+    assert L.moe_route_scored(A, None, 2, 16, 4, None, A, A, None) == INV
+    assert call(score=2) == INV and call(score=-1) == INV and call(renorm=2) == INV
+    for bad in (0.0, -1.0, float("nan"), float("inf")):
+        assert call(scale=bad) == INV
+    assert call(groups=0) == INV and call(groups=4, top_groups=0) == INV and call(groups=4, top_groups=5) == INV
+    assert call(groups=3) == UNS and call(groups=128, E=512, top_groups=8) == UNS
+    assert call(group_top=0) == INV and call(group_top=3) == INV
+    assert call(groups=16, top_groups=4, group_top=2) == INV  # groups of one expert
+    assert call(groups=8, top_groups=1) == INV  # two experts for four slots
+    assert call(T=0, groups=8, top_groups=2) == OK
+
+
+def test_route_scored_grad_refusals(L):
+    def call(l=A, ids=A, w=A, dw=A, T=2, E=16, k=4, dl=A, **kw):
+        return L.moe_route_scored_grad(l, ids, w, dw, T, E, k, scoring(**kw), dl, None)
+
+    assert call(T=0) == OK and call(T=0, groups=7) == OK  # the groups are the forward call's
+    assert call(T=-1) == INV and call(k=9) == UNS and call(E=513) == UNS and call(T=1 << 25) == UNS
+    for name in ("l", "ids", "w", "dw", "dl"):
+        assert call(**{name: None}) == INV
+    assert call(score=7) == INV and call(scale=0.0) == INV and call(renorm=-1) == INV
+
+
+def block(post=A, gate=None, pre=A, rows=0, rs=1.0, bs=1.0, eps=1e-6):
+    return moe.Block(post, gate, pre, rows, rs, bs, eps)
+
+
+def test_block_norm_refusals(L):
+    def call(x=A, r=A, T=2, d=256, act=moe.DTYPE_BF16, h=A, y=A, q=None, qs=None, **kw):
+        return L.moe_block_norm(block(**kw), x, r, T, d, act, h, y, q, qs, None)
+
+    assert call(T=0) == OK
+    assert L.moe_block_norm(None, A, A, 2, 256, 0, A, A, None, None, None) == INV
+    assert call(T=-1) == INV and call(d=0) == INV and call(eps=-1.0) == INV and call(eps=float("nan")) == INV
+    for bad in (float("nan"), float("inf")):
+        assert call(rs=bad) == INV and call(bs=bad) == INV
+    assert call(rows=1) == INV and call(rows=2, gate=A) == INV
+    for name in ("x", "r", "h", "y", "pre"):
+        assert call(**{name: None}) == INV
+    for name in ("x", "r", "h", "y", "pre", "post", "gate"):
+        assert call(**{name: A + 8}) == INV
+    assert call(act=moe.DTYPE_INT8, q=A + 8, qs=A) == INV and call(act=moe.DTYPE_FP8, q=A) == INV
+    assert call(d=252) == UNS and call(d=32776) == UNS and call(T=1 << 25) == UNS
+    assert call(d=264, act=moe.DTYPE_INT8, q=A, qs=A) == UNS
+    assert call(d=192, act=moe.DTYPE_FP8, q=A, qs=A) == UNS and call(act=moe.DTYPE_MXFP4, q=A, qs=A) == UNS
+
+
+def test_block_norm_grad_refusals(L):
+    B = 1 << 20
+
+    def call(dy=A, dh=None, x=A, h=A, T=2, d=256, dx=A, dr=B, dpre=A, dpost=A, dgate=None, ws=A, n=1 << 30, **kw):
+        return L.moe_block_norm_grad(block(**kw), dy, dh, x, h, T, d, dx, dr, dpre, dpost, dgate, ws, n, None)
+
+    need = L.moe_block_norm_grad_workspace_bytes
+    assert need(2, 256) >= 2 * 2 * 256 * 4 and need(0, 256) == 0
+    assert need(2, 252) == 0 and need(2, 16392) == 0 and need(-1, 256) == 0 and need(1 << 25, 8) == 0
+    assert call(T=0, dpre=None, dpost=None) == OK
+    assert call(T=-1) == INV and call(d=-8) == INV and call(eps=-1.0) == INV and call(bs=float("inf")) == INV
+    assert call(d=252) == UNS and call(d=16392) == UNS and call(T=1 << 25, d=8) == UNS
+    for name in ("dy", "x", "h", "dx", "dr", "pre"):
+        assert call(**{name: None}) == INV
+    for name in ("dy", "dh", "x", "h", "dx", "dr", "dpre", "dpost", "pre", "post", "ws"):
+        assert call(**{name: A + 8}) == INV
+    assert call(gate=A, dgate=A + 8) == INV and call(gate=A + 8) == INV
+    assert call(post=None) == INV and call(dgate=A) == INV and call(rows=1) == INV  # gradients of what is not there
+    assert call(dr=A) == INV  # dx and dresidual in one place
+    assert call(ws=None) == WS and call(n=need(2, 256) - 1) == WS
+    assert call(gate=A, dgate=B, dpre=None, dpost=None, ws=None) == WS
+
+
+def w4(codes=A, scales=2 * A, zeros=None, N=16, K=128, group=32, fmt=moe.SCALE_BF16, layout=moe.LAYOUT_TILED):
+    return moe.W4(codes, scales, zeros, N, K, group, fmt, layout)
+
+
+def test_gemm_w4_refusals(L):
+    def call(x=A, M=2, up=None, y=A, **kw):
+        return L.moe_gemm_w4(x, M, w4(**kw), up, y, None)
+
+    assert call(M=0) == OK and call(M=0, up=w4()) == OK
+    assert call(M=-1) == INV and L.moe_gemm_w4(A, 1, None, None, A, None) == INV
+    assert call(N=0) == INV and call(K=0) == INV and call(N=-16) == INV
+    assert call(N=24) == UNS and call(K=192) == UNS and call(group=256) == UNS and call(group=0) == UNS
+    assert call(fmt=2) == UNS and call(N=1 << 16, K=1 << 16) == UNS and call(M=1 << 24) == UNS
+    assert call(layout=moe.LAYOUT_ROW_MAJOR) == INV
+    for name in ("x", "y", "codes", "scales"):
+        assert call(**{name: None}) == INV
+    for name in ("x", "y", "codes", "scales", "zeros"):
+        assert call(**{name: A + 8}) == INV
+    for bad in (dict(N=32), dict(K=256), dict(group=64), dict(fmt=moe.SCALE_FP16), dict(codes=None),
+                dict(layout=moe.LAYOUT_ROW_MAJOR)):
+        assert call(M=0, up=w4(**bad)) == INV
+
+
+def test_w4_tile_refusals(L):
+    def call(codes=1 << 16, scales=1 << 17, zeros=None, **kw):
+        return L.moe_w4_tile(w4(**dict(dict(layout=moe.LAYOUT_ROW_MAJOR), **kw)), codes, scales, zeros, None)
+
+    src = dict(codes=A, scales=2 * A, zeros=3 * A)
+    row = moe.LAYOUT_ROW_MAJOR
+    assert L.moe_w4_tile(None, 1 << 16, 1 << 17, None, None) == INV
+    assert L.moe_w4_tile(w4(layout=moe.LAYOUT_TILED), 1 << 16, 1 << 17, None, None) == INV
+    assert call(codes=None) == INV and call(scales=None) == INV and call(zeros=1 << 18) == INV
+    assert L.moe_w4_tile(w4(layout=row, **src), 1 << 16, 1 << 17, None, None) == INV  # zeros without a place
+    for bad in (dict(codes=(1 << 16) + 8), dict(scales=(1 << 17) + 8)):
+        assert call(**bad) == INV
+    for bad in (dict(N=24), dict(K=64), dict(group=48)):
+        assert L.moe_w4_tile(w4(**dict(dict(layout=row), **bad)), 1 << 16, 1 << 17, None, None) == UNS
+    # overlaps: codes are 1 KB, scales 128 bytes, zeros 64
+    assert call(codes=A) == INV and call(codes=A + 1008) == INV and call(scales=A + 512) == INV
+    assert call(codes=2 * A - 512) == INV and call(scales=(1 << 16) + 1008) == INV
+    assert L.moe_w4_tile(w4(layout=row, **src), 1 << 16, 1 << 17, (1 << 17) + 112, None) == INV
+    assert L.moe_w4_tile(w4(layout=row, **src), 1 << 16, 1 << 17, 3 * A + 48, None) == INV
+
+
+def test_binding_refusals():
+    """The binding checks types, shapes, contiguity and device before the library sees a pointer."""
+    bf = torch.bfloat16
+    x, w, l = torch.zeros(4, 256, dtype=bf), torch.zeros(256, dtype=bf), torch.zeros(4, 16)
+    ids, g = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+
+    def refused(match, f, *a, **kw):
+        with pytest.raises(moe.MoEError, match=match):
+            f(*a, **kw)
+
+    refused("GPU", moe.route_scored, l, 2)
+    refused("logits must be", moe.route_scored, l.double(), 2)
+    refused("two dimensions", moe.route_scored, l[0], 2)
+    refused("contiguous", moe.route_scored, torch.zeros(16, 4).t(), 2)
+    refused("bias must have shape", moe.route_scored, l, 2, bias=torch.zeros(15))
+    refused("bias must be", moe.route_scored, l, 2, bias=torch.zeros(16, dtype=bf))
+    refused("GPU", moe.route_scored_grad, l, ids, g, g)
+    refused("ids must be", moe.route_scored_grad, l, ids.long(), g, g)
+    refused("dw must have shape", moe.route_scored_grad, l, ids, g, g[:3])
+    refused("GPU", moe.block_norm, x, x, w)
+    refused("residual must have shape", moe.block_norm, x, x[:2], w)
+    refused("post_weight must have", moe.block_norm, x, x, w, post_weight=w[:8])
+    refused("gate must have shape", moe.block_norm, x, x, w, gate=x[:3])
+    refused("gate must be", moe.block_norm, x, x, w, gate=w.float())
+    refused("GPU", moe.block_norm_grad, x, x, x, w)
+    refused("dh must have shape", moe.block_norm_grad, x, x, x, w, dh=w)
+    refused("h must be", moe.block_norm_grad, x, x, x.float(), w)
+    q, s, z = torch.zeros(16, 64, dtype=torch.uint8), torch.zeros(16, 4, dtype=bf), torch.zeros(16, 4, dtype=torch.uint8)
+    refused("GPU", moe.w4_tile, q, s)
+    refused("scales must be", moe.w4_tile, q, s.float())
+    refused("scales must have shape", moe.w4_tile, q, s[:8])
+    refused("not a divisor", moe.w4_tile, q, torch.zeros(16, 3, dtype=bf))
+    refused("zeros must have shape", moe.w4_tile, q, s, z[:, :2])
+    refused("codes must be", moe.w4_tile, q.to(torch.int8), s)
+    t = moe.W4Weights(q, s, z, 16, 128, 32)
+    refused("GPU", moe.gemm_w4, torch.zeros(2, 128, dtype=bf), t)
+    refused("x must have shape", moe.gemm_w4, x, t)
+    assert t.struct().layout == moe.LAYOUT_TILED and ctypes.sizeof(t.struct()) == 48
