@@ -438,7 +438,7 @@ int moe_block_norm_grad(const moe_block* block, const void* dy, const void* dh, 
 size_t moe_block_norm_grad_workspace_bytes(int T, int d);
 
 /* 4-bit weights [N][K]: value = (code - zero) * scale, two codes 0..15 per byte (element 2j in the low nibble
- * of byte j), one 16-bit scale and, if zeros is not NULL, one zero point (a whole number 0..255) per `group`
+ * of byte j), one 16-bit scale and, if zeros is not NULL, one zero point (0..127, not checked) per `group`
  * consecutive values of a row: scales, zeros [N][K / group].  Without zeros the zero point is 8. */
 enum moe_scale_dtype { MOE_SCALE_BF16 = 0, MOE_SCALE_FP16 = 1 };
 typedef struct moe_w4 {

@@ -7,6 +7,7 @@
 // themselves and the output.  (Weights scaled before the product would be rounded to bf16, 2^-9 each.)
 #include "common.h"
 #include "kernels.h"
+#include "mfma_dev.h"
 #include "rows_dev.h"
 
 namespace moe {
@@ -36,14 +37,31 @@ __global__ __launch_bounds__(256) void w4_scale_tile_kernel(const T* __restrict_
   dst[at] = src[(blk * 16 + row) * groups + unit % groups];
 }
 
-// Eight codes -> bf16 of code - z, in K order.
-__device__ __forceinline__ bf16x8 decode8(uint32_t c, float z) {
-  const uint32_t lo = c & 0x0F0F0F0Fu, hi = (c >> 4) & 0x0F0F0F0Fu;
+// Four codes, one per byte in the low half (or the high half, HI), as signed bytes code - z: 128 + code - z
+// never leaves a byte (z <= 127), and turning its top bit makes it two's complement.  zc = zero_bytes(z).
+__device__ __forceinline__ uint32_t zero_bytes(uint32_t z) { return 0x80808080u - z * 0x01010101u; }
+
+// Eight codes -> bf16 of code - z, in K order, exactly.  Without zero points (z = 8) the sign sits in the
+// nibble's own top bit: the high half of a byte then is 16 (code - 8), and the 16 is left to the scale
+// (kSymScale).  Either way a signed byte converts in one instruction and a pair packs in another.
+constexpr float kSymScale = 0.0625f;
+__device__ __forceinline__ float byte_f32(uint32_t w, int b) { return (float)(int8_t)(w >> (8 * b)); }
+template <bool ZERO>
+__device__ __forceinline__ bf16x8 decode8(uint32_t c, uint32_t zc) {
+  uint32_t lo, hi;
+  if (ZERO) {
+    lo = ((c & 0x0F0F0F0Fu) + zc) ^ 0x80808080u;
+    hi = (((c >> 4) & 0x0F0F0F0Fu) + zc) ^ 0x80808080u;
+  } else {
+    c ^= 0x88888888u;
+    lo = (c << 4) & 0xF0F0F0F0u;
+    hi = c & 0xF0F0F0F0u;
+  }
   uint4 o;
-  o.x = pack_bf16x2(float(lo & 255) - z, float(hi & 255) - z);
-  o.y = pack_bf16x2(float((lo >> 8) & 255) - z, float((hi >> 8) & 255) - z);
-  o.z = pack_bf16x2(float((lo >> 16) & 255) - z, float((hi >> 16) & 255) - z);
-  o.w = pack_bf16x2(float(lo >> 24) - z, float(hi >> 24) - z);
+  o.x = pack_bf16x2(byte_f32(lo, 0), byte_f32(hi, 0));
+  o.y = pack_bf16x2(byte_f32(lo, 1), byte_f32(hi, 1));
+  o.z = pack_bf16x2(byte_f32(lo, 2), byte_f32(hi, 2));
+  o.w = pack_bf16x2(byte_f32(lo, 3), byte_f32(hi, 3));
   return as_bf16x8(o);
 }
 
@@ -54,7 +72,7 @@ __device__ __forceinline__ float scale_f32(uint32_t bits, bool fp16) {
 
 // 16 * NR weight rows (PAIR: 8 * NR of either matrix) by 16 * MQ rows of x per workgroup, whose 4
 // wavefronts split K (interleaved chunks of 128; the sums meet in LDS in a fixed order).
-template <int MQ, int NR, int GROUP, bool PAIR>
+template <int MQ, int NR, int GROUP, bool PAIR, bool ZERO>
 __global__ __launch_bounds__(256) void gemm_stream_w4(W4Args a) {
   constexpr int S = 128 / GROUP, F = GROUP / 32;  // groups per chunk, MFMAs per group
   constexpr int U = MQ * NR <= 2 ? 2 : 1;         // chunks per batch
@@ -81,7 +99,7 @@ __global__ __launch_bounds__(256) void gemm_stream_w4(W4Args a) {
   struct Batch {
     uint4 w[U][NR], x[U][MQ][4];
     uint2 s[U][NR][S];
-    uint32_t z[U][NR][S];
+    uint32_t z[ZERO ? U : 1][NR][S];
   };
   const int nc = (nkb - kw + 3) / 4;  // this wavefront's chunks: kw, kw + 4, ...
   auto load = [&](Batch& bt, int i) {
@@ -96,7 +114,7 @@ __global__ __launch_bounds__(256) void gemm_stream_w4(W4Args a) {
 #pragma unroll
         for (int g = 0; g < S; ++g) {
           bt.s[u][j][g] = gload8(m.scales, ((unit * S + g) * 16 + kg * 4) * 2);
-          bt.z[u][j][g] = m.zeros ? gload_u8(m.zeros, (unit * S + g) * 16 + r16) : 8u;
+          if (ZERO) bt.z[u][j][g] = m.zeros ? gload_u8(m.zeros, (unit * S + g) * 16 + r16) : 8u;
         }
       }
 #pragma unroll
@@ -114,16 +132,17 @@ __global__ __launch_bounds__(256) void gemm_stream_w4(W4Args a) {
         const uint32_t c[4] = {bt.w[u][j].x, bt.w[u][j].y, bt.w[u][j].z, bt.w[u][j].w};
 #pragma unroll
         for (int g = 0; g < S; ++g) {
-          const float z = float(bt.z[u][j][g]);
+          const uint32_t z = ZERO ? zero_bytes(bt.z[ZERO ? u : 0][j][g]) : 0u;
           const uint2 sb = bt.s[u][j][g];
-          const float sc[4] = {scale_f32(sb.x & 0xFFFF, a.fp16), scale_f32(sb.x >> 16, a.fp16),
-                               scale_f32(sb.y & 0xFFFF, a.fp16), scale_f32(sb.y >> 16, a.fp16)};
+          constexpr float one = ZERO ? 1.0f : kSymScale;
+          const float sc[4] = {scale_f32(sb.x & 0xFFFF, a.fp16) * one, scale_f32(sb.x >> 16, a.fp16) * one,
+                               scale_f32(sb.y & 0xFFFF, a.fp16) * one, scale_f32(sb.y >> 16, a.fp16) * one};
           f32x4 acc[MQ];
 #pragma unroll
           for (int q = 0; q < MQ; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int f = 0; f < F; ++f) {
-            const bf16x8 wf = decode8(c[g * F + f], z);
+            const bf16x8 wf = decode8<ZERO>(c[g * F + f], z);
 #pragma unroll
             for (int q = 0; q < MQ; ++q) acc[q] = mfma16(wf, as_bf16x8(bt.x[u][q][g * F + f]), acc[q]);
           }
@@ -180,26 +199,198 @@ __global__ __launch_bounds__(256) void gemm_stream_w4(W4Args a) {
   }
 }
 
-template <int GROUP, bool PAIR>
-hipError_t launch_group(W4Args a, hipStream_t s) {
+// ------------------------------------------------------------------------------------------------
+// many rows: 256 weight rows (PAIR: 128 of either matrix) by 128 rows of x per workgroup
+//
+// Each of the 4 wavefronts holds 64 weight rows and all 128 rows of x: a weight is decoded by one wavefront,
+// from registers, once for 128 rows, and only x goes through LDS as operands (global_load_lds, two stages of
+// 128 columns).  A group's sums are four chained MFMAs from zero (one per 32 columns); the scale takes them to
+// the totals while the next ones run.  Here x is the MFMA's first operand: a lane then holds one weight row per
+// fragment, and one scale.
+// ------------------------------------------------------------------------------------------------
+constexpr int kTileM = 128;
+constexpr int kXStage = kTileM * 256;  // bytes: rows of 16 pieces of 16 bytes, swizzled by the row
+
+template <int GROUP, bool PAIR, bool ZERO>
+__global__ __launch_bounds__(256, 2) void gemm_tile_w4(W4Args a) {
+  constexpr int S = 128 / GROUP, F = GROUP / 32;
+  constexpr int C = PAIR ? 2 : 4;  // consecutive weight rows of a lane
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[2 * kXStage + 4 * 4096];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, kg = lane >> 4;
+  const int K = a.K, nkb = K / 128;
+  const int m0 = (blockIdx.x % a.mtiles) * kTileM;
+  const int n0 = (blockIdx.x / a.mtiles) * (64 * C) + wv * (16 * C);
+  // Row r of fragment j is weight row n0 + C r + j % C (of matrix j / 2 of a pair): a lane's results are
+  // consecutive columns of y.  (Rows past N re-read the last ones; never stored.)
+  const int nl = min(n0 + C * r16, a.N - C);
+  // of the lane's 16 bytes of fragment 0 in the first unit; the next rows' follow
+  const uint32_t woff = (uint32_t)(nl >> 4) * (uint32_t)(nkb * 1024) + kg * 256 + (nl & 15) * 16;
+  f32x4 tot[4][8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int t = 0; t < 8; ++t) tot[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // 8 of the stage's 32 kilobytes: rows 32 wv + 4 q .. + 3 in load q
+  auto load_x = [&](int kb, int stage) {
+    const char* base = static_cast<const char*>(a.x) + (size_t)kb * 256;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int row = 32 * wv + 4 * q + (tid_here() >> 4 & 3);
+      const int piece = (tid_here() & 15) ^ (row & 15);
+      const uint32_t off = (uint32_t)min(m0 + row, a.M - 1) * (uint32_t)(K * 2) + piece * 16;
+      dma16(base, off, (lds_void*)(ring + stage * kXStage + (32 * wv + 4 * q) * 256));
+    }
+  };
+  // A wavefront's codes of a chunk, one kilobyte per fragment, as its lanes hold them.
+  uint8_t* const codes = ring + 2 * kXStage + wv * 4096;
+  auto load_codes = [&](int kb) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      dma16(static_cast<const char*>(a.m[PAIR ? j >> 1 : 0].codes) + (size_t)kb * 1024 + (j % C) * 16, woff,
+            (lds_void*)(codes + j * 1024));
+  };
+  // Scales (16 bits per row) and zero points (8) of a chunk wait in registers.
+  uint32_t sc[S][2], zb[S][PAIR ? 2 : 1];
+  auto load_scales = [&](int kb) {
+    // (opaque: the compiler would keep a 64-bit address for each of these loads)
+    uint32_t at = woff;
+    asm volatile("" : "+v"(at));
+    at = (at >> 10) * (16 * S) + (nl & 15);  // (16 rows of every group)
+#pragma unroll
+    for (int g = 0; g < S; ++g) {
+      const uint32_t e = (kb * S + g) * 16 + at;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        sc[g][c] = gload4(a.m[PAIR ? c : 0].scales, (e + (PAIR ? 0 : 2 * c)) * 2);
+        if (ZERO && PAIR) {
+          const uint8_t* z = a.m[c].zeros;
+          zb[g][PAIR ? c : 0] = z ? gload_u8(z, e) | gload_u8(z, e + 1) << 8 : 0x0808u;
+        }
+      }
+      if (ZERO && !PAIR) zb[g][0] = gload4(a.m[0].zeros, e);
+    }
+  };
+  load_x(0, 0);
+  load_codes(0);
+  load_scales(0);
+  for (int kb = 0; kb < nkb; ++kb) {
+    const int st = kb & 1;
+    MOE_WAITCNT(0, 15);  // this chunk has landed
+    __syncthreads();     // for every wavefront; and all have read the other stage
+    // (the last chunk loads itself again: without a branch the loop's body is one block)
+    const int next = min(kb + 1, nkb - 1);
+    load_x(next, st ^ 1);
+    uint4 code[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) code[j] = *reinterpret_cast<const uint4*>(codes + j * 1024 + lane * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)  // (in registers before the next chunk's take their place)
+      asm volatile("" : "+v"(code[j].x), "+v"(code[j].y), "+v"(code[j].z), "+v"(code[j].w));
+    load_codes(next);
+    uint32_t xa = st * kXStage + r16 * 256 + (kg ^ (r16 & 3)) * 16 + (r16 >> 2) * 64;
+    asm volatile("" : "+v"(xa));
+#pragma unroll
+    for (int g = 0; g < S; ++g) {
+      float s[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t b = PAIR ? sc[g][j >> 1] >> (16 * (j & 1)) : sc[g][j >> 1] >> (16 * (j & 1));
+        s[j] = (a.fp16 ? scale_f32(b & 0xFFFF, true) : scale_f32(b & 0xFFFF, false)) * (ZERO ? 1.0f : kSymScale);
+      }
+      bf16x8 wf[4][F];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t c[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+        const uint32_t z = !ZERO ? 0u : PAIR ? zb[g][PAIR ? j >> 1 : 0] >> (8 * (j & 1)) : zb[g][0] >> (8 * j);
+#pragma unroll
+        for (int f = 0; f < F; ++f) wf[j][f] = decode8<ZERO>(c[g * F + f], ZERO ? zero_bytes(z & 255) : 0u);
+      }
+      // (behind the last use of this chunk's; the loop's head waits for them)
+      if (g == S - 1) load_scales(next);
+      // row r16 of tile t, piece 4 f' + kg (f' = g F + f) at place (4 f' + kg) ^ r16
+      auto read_x = [&](int t, int f) {
+        return as_bf16x8(*reinterpret_cast<const uint4*>(ring + ((xa ^ ((g * F + f) * 64)) + t * 4096)));
+      };
+      // Operand f of tile t lies in slot (F t + f) mod X: half of a tile's are read ahead of its use, the rest as
+      // the tile before has used its own up (with a whole second tile's the registers do not suffice).
+      constexpr int H = F / 2, X = F + (H ? H : 1);
+      bf16x8 xf[X];
+#pragma unroll
+      for (int f = 0; f < F; ++f) xf[f] = read_x(0, f);
+      f32x4 acc[2];
+#pragma unroll
+      for (int i = 0; i <= 32; ++i) {  // fragment i % 4 of tile i / 4, and the totals of the one before
+        const int t = i >> 2, j = i & 3;
+        if (i < 32) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (j == 0 && t < 7) {
+#pragma unroll
+            for (int f = 0; f < X - F; ++f) xf[(F * (t + 1) + f) % X] = read_x(t + 1, f);
+          }
+          acc[i & 1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int f = 0; f < F; ++f) {
+            acc[i & 1] = mfma16(xf[(F * t + f) % X], wf[j][f], acc[i & 1]);
+            if (j == 3 && t < 7 && f + X - F < F) xf[(F * (t + 1) + f + X - F) % X] = read_x(t + 1, f + X - F);
+          }
+        }
+        if (i > 0) {
+          const int u = (i - 1) >> 2, v = (i - 1) & 3;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) tot[v][u][r] = fmaf(s[v], acc[(i - 1) & 1][r], tot[v][u][r]);
+          // (the sums are taken here: moved behind the chunk's other MFMAs they would keep every acc)
+          asm volatile("" : "+v"(tot[v][u]));
+        }
+      }
+    }
+  }
+  MOE_WAITCNT(0, 15);  // (no load may still be on its way to LDS when the workgroup ends)
+  // lane holds rows 4 kg + r of tile t, columns nl .. + C - 1
+  if (n0 + C * r16 >= a.N) return;
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = m0 + t * 16 + kg * 4 + r;
+      if (row >= a.M) continue;
+      const size_t at = ((size_t)row * a.N + nl) * 2;
+      if (PAIR)
+        gstore4(a.y, at, pack_bf16x2(swiglu(tot[0][t][r], tot[2][t][r]), swiglu(tot[1][t][r], tot[3][t][r])));
+      else
+        gstore8(a.y, at, uint2{pack_bf16x2(tot[0][t][r], tot[1][t][r]), pack_bf16x2(tot[2][t][r], tot[3][t][r])});
+    }
+}
+
+template <int GROUP, bool PAIR, bool ZERO>
+hipError_t launch_tiles(W4Args a, hipStream_t s) {
+  if (a.M > 64) {
+    a.mtiles = (a.M + kTileM - 1) / kTileM;
+    const unsigned grid = (unsigned)a.mtiles * ((a.N + (PAIR ? 127 : 255)) / (PAIR ? 128 : 256));
+    gemm_tile_w4<GROUP, PAIR, ZERO><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+  }
   constexpr int NR = 2;
   const int mq = a.M <= 16 ? 1 : 2;
   a.mtiles = (a.M + 16 * mq - 1) / (16 * mq);
   const int per = PAIR ? NR / 2 : NR;
   const unsigned grid = (unsigned)a.mtiles * ((a.N / 16 + per - 1) / per);
-  auto* kernel = mq == 1 ? &gemm_stream_w4<1, NR, GROUP, PAIR> : &gemm_stream_w4<2, NR, GROUP, PAIR>;
+  auto* kernel = mq == 1 ? &gemm_stream_w4<1, NR, GROUP, PAIR, ZERO> : &gemm_stream_w4<2, NR, GROUP, PAIR, ZERO>;
   kernel<<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
+}
+template <int GROUP>
+hipError_t launch_group(const W4Args& a, hipStream_t s) {
+  const bool zero = a.m[0].zeros || a.m[1].zeros;
+  if (a.m[1].codes) return zero ? launch_tiles<GROUP, true, true>(a, s) : launch_tiles<GROUP, true, false>(a, s);
+  return zero ? launch_tiles<GROUP, false, true>(a, s) : launch_tiles<GROUP, false, false>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_w4(const W4Args& a, int group, int num_cus, hipStream_t s) {
   (void)num_cus;
-  const bool pair = a.m[1].codes != nullptr;
-  if (group == 32) return pair ? launch_group<32, true>(a, s) : launch_group<32, false>(a, s);
-  if (group == 64) return pair ? launch_group<64, true>(a, s) : launch_group<64, false>(a, s);
-  return pair ? launch_group<128, true>(a, s) : launch_group<128, false>(a, s);
+  return group == 32 ? launch_group<32>(a, s) : group == 64 ? launch_group<64>(a, s) : launch_group<128>(a, s);
 }
 
 hipError_t launch_w4_tile(const W4Mat& src, int N, int K, int group, void* codes, void* scales, uint8_t* zeros,

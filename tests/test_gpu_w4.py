@@ -91,7 +91,7 @@ def test_gemm_w4_every_code(moe, M, group):
     N, K = 64, 256
     codes, s, _ = _w(N, K, group, False, 3)
     codes[:, :128] = torch.arange(N * 128, device="cuda").reshape(N, 128).to(torch.uint8)
-    z = torch.randint(0, 256, (N, K // group), generator=torch.Generator().manual_seed(1), dtype=torch.uint8).cuda()
+    z = torch.randint(0, 128, (N, K // group), generator=torch.Generator().manual_seed(1), dtype=torch.uint8).cuda()
     for zeros in (None, z):
         w = (codes, s, zeros)
         t = moe.w4_tile(*w)
