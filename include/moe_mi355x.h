@@ -460,7 +460,7 @@ int moe_w4_tile(const moe_w4* src, void* codes, void* scales, uint8_t* zeros, hi
  * group and scale_dtype) the SwiGLU of the pair, bf16(SiLU(x Wt) * (x Upt)): a shared expert's gate and up
  * step, whose y moe_gemm_w4 takes back to d for moe_combine's shared_y.  Codes less zero points are exact in
  * the products, sums and scales are fp32, one rounding.
- *   x [M][K], y [M][N] bf16, not overlapping.  M * K < 2^31, N * K < 2^32, else MOE_ERR_UNSUPPORTED; pointers
+ *   x [M][K], y [M][N] bf16, not overlapping.  M * K < 2^31, N * K < 2^32, M * N < 2^37, else MOE_ERR_UNSUPPORTED; pointers
  *   16-byte aligned.  M = 0 is a no-op. */
 int moe_gemm_w4(const void* x, int M, const moe_w4* w, const moe_w4* up, void* y, hipStream_t stream);
 

@@ -791,7 +791,7 @@ int moe_w4_tile(const moe_w4* src, void* codes, void* scales, uint8_t* zeros, hi
       if (in[i].p && out[j].p && overlap(in[i].p, in[i].n, out[j].p, out[j].n)) return MOE_ERR_INVALID_ARG;
       if (i < j && out[j].p && overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return MOE_ERR_INVALID_ARG;
     }
-  return hip_status(launch_w4_tile(W4Mat{src->codes, src->scales, src->zeros}, src->N, src->K, src->group,
+  return hip_status(launch_w4_tile(W4Mat{src->codes, src->scales, src->zeros, 0, 0}, src->N, src->K, src->group,
                                    codes, scales, zeros, stream));
 }
 
@@ -803,6 +803,7 @@ int moe_gemm_w4(const void* x, int M, const moe_w4* w, const moe_w4* up, void* y
   if (up && (up->N != w->N || up->K != w->K || up->group != w->group || up->scale_dtype != w->scale_dtype))
     return MOE_ERR_INVALID_ARG;
   if ((int64_t)M * w->K * 2 >= kMaxOffsetBytes) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)M * w->N >= (int64_t(1) << 37)) return MOE_ERR_UNSUPPORTED;  // (a launch's threads)
   if (M == 0) return MOE_OK;
   if (!x || !y || !aligned16(x) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
   const int cus = device_cus();
@@ -810,8 +811,12 @@ int moe_gemm_w4(const void* x, int M, const moe_w4* w, const moe_w4* up, void* y
   W4Args a;
   std::memset(&a, 0, sizeof(a));
   a.x = x;
-  a.m[0] = W4Mat{w->codes, w->scales, w->zeros};
-  if (up) a.m[1] = W4Mat{up->codes, up->scales, up->zeros};
+  const uint8_t* zeros = w->zeros ? w->zeros : up ? up->zeros : nullptr;
+  auto mat = [&](const moe_w4* m) {
+    return W4Mat{m->codes, m->scales, m->zeros ? m->zeros : zeros, m->zeros ? 0xFFu : 0u, m->zeros ? 0u : 8u};
+  };
+  a.m[0] = mat(w);
+  if (up) a.m[1] = mat(up);
   a.y = y;
   a.M = M;
   a.N = w->N;

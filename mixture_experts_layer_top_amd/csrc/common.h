@@ -88,6 +88,9 @@ __device__ __forceinline__ uint32_t gload4(const void* base, uint32_t off) {
 __device__ __forceinline__ uint32_t gload_u8(const uint8_t* p, uint32_t i) {
   return reinterpret_cast<__attribute__((address_space(1))) const uint8_t*>((gchar*)p)[i];
 }
+__device__ __forceinline__ uint32_t gload_u16(const void* base, uint32_t off) {
+  return *reinterpret_cast<__attribute__((address_space(1))) const uint16_t*>((gchar*)base + off);
+}
 __device__ __forceinline__ int32_t gload_i32(const int32_t* p, int i) {
   return reinterpret_cast<__attribute__((address_space(1))) const int32_t*>((gchar*)p)[i];
 }

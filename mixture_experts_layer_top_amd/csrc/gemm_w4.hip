@@ -14,10 +14,12 @@ namespace moe {
 
 namespace {
 
-// Tiled layout: per 16 weight rows and 128 values of K, 1 KB ordered [lane group 0..3][row][part 0..3] of
-// dwords, part i of lane group g being values 32 i + 8 g .. + 7 (in the order of the row-major bytes): one
-// 16-byte load gives a lane its operand of four MFMAs, each of which covers 32 consecutive values, so that a
-// group of 32 is one MFMA.  Scales and zeros [block][group][row].
+// Tiled layout, per 16 weight rows and unit of 128 columns (S = 128 / group groups):
+//  codes   1 KB ordered [lane group 0..3][row][part 0..3] of dwords, part i of lane group g being values
+//          32 i + 8 g .. + 7 (in the order of the row-major bytes): one 16-byte load gives a lane its operand of
+//          four MFMAs, each of which covers 32 consecutive values, so that a group of 32 is one MFMA;
+//  scales  [row / 4][group][row % 4]: the four rows of a lane's results, all groups, in one piece;
+//  zeros   [row][group].
 __global__ __launch_bounds__(256) void w4_tile_kernel(const uint32_t* __restrict__ src,
                                                       uint32_t* __restrict__ dst, int64_t n, int nkb) {
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -27,14 +29,19 @@ __global__ __launch_bounds__(256) void w4_tile_kernel(const uint32_t* __restrict
   const int kb = (int)(unit % nkb);
   dst[at] = src[((blk * 16 + row) * nkb + kb) * 16 + i * 4 + g];
 }
-template <class T>
-__global__ __launch_bounds__(256) void w4_scale_tile_kernel(const T* __restrict__ src, T* __restrict__ dst,
-                                                            int64_t n, int groups) {
+// A thread per scale: groups = K / group of a row, S of them per unit.
+__global__ __launch_bounds__(256) void w4_scale_tile_kernel(const uint16_t* __restrict__ src,
+                                                            const uint8_t* __restrict__ zsrc,
+                                                            uint16_t* __restrict__ dst,
+                                                            uint8_t* __restrict__ zdst, int64_t n, int groups,
+                                                            int S) {
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= n) return;
-  const int row = (int)(at & 15);
-  const int64_t unit = at >> 4, blk = unit / groups;
-  dst[at] = src[(blk * 16 + row) * groups + unit % groups];
+  const int64_t blk = at / (16 * groups);
+  const int row = (int)(at / groups % 16), g = (int)(at % groups);
+  const int64_t unit = (blk * (groups / S) + g / S) * (16 * S);
+  dst[unit + (row >> 2) * (4 * S) + (g % S) * 4 + (row & 3)] = src[at];
+  if (zsrc) zdst[unit + row * S + g % S] = zsrc[at];
 }
 
 // Four codes, one per byte in the low half (or the high half, HI), as signed bytes code - z: 128 + code - z
@@ -70,73 +77,102 @@ __device__ __forceinline__ float scale_f32(uint32_t bits, bool fp16) {
   return fp16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)bits) : __uint_as_float(bits << 16);
 }
 
-// 16 * NR weight rows (PAIR: 8 * NR of either matrix) by 16 * MQ rows of x per workgroup, whose 4
-// wavefronts split K (interleaved chunks of 128; the sums meet in LDS in a fixed order).
-template <int MQ, int NR, int GROUP, bool PAIR, bool ZERO>
-__global__ __launch_bounds__(256) void gemm_stream_w4(W4Args a) {
-  constexpr int S = 128 / GROUP, F = GROUP / 32;  // groups per chunk, MFMAs per group
-  constexpr int U = MQ * NR <= 2 ? 2 : 1;         // chunks per batch
+// ------------------------------------------------------------------------------------------------
+// few rows: 16 * NR weight rows (PAIR: 8 * NR of either matrix) by 16 * MQ rows of x per workgroup, whose W
+// wavefronts split K (interleaved units; the sums meet in LDS in a fixed order)
+//
+// Weights go straight from HBM into registers, 1 KB per load, are decoded there and multiplied.  XL: all of x
+// lies in LDS (few short rows): a wavefront then keeps nothing but weights in flight.
+// ------------------------------------------------------------------------------------------------
+constexpr int kXlBytes = 64 << 10;
+constexpr int xl_stride(int K) { return K * 2 + 64; }  // (rows start in different banks)
+
+template <int MQ, int NR, int GROUP, bool PAIR, bool ZERO, int W, bool XL, bool FP16>
+__device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
+  constexpr int S = 128 / GROUP, F = GROUP / 32;  // groups per unit, MFMAs per group
+  constexpr int U = MQ == 1 ? 2 : 1;              // units per batch (by registers)
   constexpr int PC = PAIR ? 2 : 1;                // accumulators per output
   constexpr int P = MQ * NR / PC;                 // outputs (16 x 16) per wavefront
-  __shared__ float red[P * 3 * PC * 4 * 64];
+  float* const red = reinterpret_cast<float*>(lds);  // [P][W - 1][PC * 4][64]
+  uint8_t* const xl = lds + P * (W - 1) * PC * 1024;
   const int lane = threadIdx.x & 63, kw = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kg = lane >> 4;
   const int K = a.K, nkb = K / 128, nblk = a.N / 16;
   const int m0 = (blockIdx.x % a.mtiles) * (16 * MQ), rows = min(16 * MQ, a.M - m0);
   const int b0 = (blockIdx.x / a.mtiles) * (NR / PC);  // first 16-row block
-  uint32_t blk[NR], xoff[MQ];
+  uint32_t unit0[NR], xoff[MQ];
 #pragma unroll
   for (int j = 0; j < NR; ++j)  // (a block past N re-reads the last one; never stored)
-    blk[j] = (uint32_t)min(b0 + j / PC, nblk - 1);
+    unit0[j] = (uint32_t)min(b0 + j / PC, nblk - 1) * (uint32_t)nkb;
 #pragma unroll
-  for (int q = 0; q < MQ; ++q)  // (a row past the last re-reads it; never stored)
-    xoff[q] = ((uint32_t)(m0 + min(q * 16 + r16, rows - 1)) * (uint32_t)K + kg * 8) * 2;
+  for (int q = 0; q < MQ; ++q) {  // (a row past the last re-reads it; never stored)
+    const int r = min(q * 16 + r16, rows - 1);
+    xoff[q] = XL ? (uint32_t)(r * xl_stride(K) + kg * 16) : ((uint32_t)(m0 + r) * (uint32_t)K + kg * 8) * 2;
+  }
   f32x4 tot[NR][MQ];
 #pragma unroll
   for (int j = 0; j < NR; ++j)
 #pragma unroll
     for (int q = 0; q < MQ; ++q) tot[j][q] = f32x4{0.f, 0.f, 0.f, 0.f};
   struct Batch {
-    uint4 w[U][NR], x[U][MQ][4];
-    uint2 s[U][NR][S];
-    uint32_t z[ZERO ? U : 1][NR][S];
+    uint4 w[U][NR], x[XL ? 1 : U][MQ][4];
+    uint32_t s[U][NR][2 * S], z[ZERO ? U : 1][NR];
   };
-  const int nc = (nkb - kw + 3) / 4;  // this wavefront's chunks: kw, kw + 4, ...
+  const int nc = (nkb - kw + W - 1) / W;  // this wavefront's units: kw, kw + W, ...
   auto load = [&](Batch& bt, int i) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t kb = (uint32_t)min(kw + 4 * (i + u), nkb - 1);
+      const uint32_t kb = (uint32_t)min(kw + W * (i + u), nkb - 1);
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
         const W4Mat& m = a.m[PAIR ? j & 1 : 0];
-        const uint32_t unit = blk[j] * (uint32_t)nkb + kb;
-        bt.w[u][j] = gload16(static_cast<const char*>(m.codes) + (size_t)unit * 1024, lane * 16);
+        const size_t unit = unit0[j] + kb;
+        const char* codes = static_cast<const char*>(m.codes) + unit * 1024;
+        bt.w[u][j] = a.mtiles == 1 ? gload16_nt(codes, lane * 16) : gload16(codes, lane * 16);
+        const char* sc = static_cast<const char*>(m.scales) + unit * (32 * S);
+        if (S == 1) {
+          const uint2 v = gload8(sc, kg * 8);
+          bt.s[u][j][0] = v.x;
+          bt.s[u][j][1] = v.y;
+        } else {
 #pragma unroll
-        for (int g = 0; g < S; ++g) {
-          bt.s[u][j][g] = gload8(m.scales, ((unit * S + g) * 16 + kg * 4) * 2);
-          if (ZERO) bt.z[u][j][g] = m.zeros ? gload_u8(m.zeros, (unit * S + g) * 16 + r16) : 8u;
+          for (int g = 0; g < S / 2; ++g) {
+            const uint4 v = gload16(sc, kg * (8 * S) + g * 16);
+            bt.s[u][j][4 * g] = v.x;
+            bt.s[u][j][4 * g + 1] = v.y;
+            bt.s[u][j][4 * g + 2] = v.z;
+            bt.s[u][j][4 * g + 3] = v.w;
+          }
+        }
+        if (ZERO) {
+          const uint8_t* z = m.zeros + unit * (16 * S);
+          bt.z[ZERO ? u : 0][j] = S == 1 ? gload_u8(z, r16) : S == 2 ? gload_u16(z, r16 * 2) : gload4(z, r16 * 4);
         }
       }
+      if (!XL) {
 #pragma unroll
-      for (int q = 0; q < MQ; ++q)
+        for (int q = 0; q < MQ; ++q)
 #pragma unroll
-        for (int f = 0; f < 4; ++f) bt.x[u][q][f] = gload16(a.x, xoff[q] + (kb * 128 + f * 32) * 2);
+          for (int f = 0; f < 4; ++f) bt.x[XL ? 0 : u][q][f] = gload16(a.x, xoff[q] + (kb * 128 + f * 32) * 2);
+      }
     }
   };
   auto compute = [&](const Batch& bt, int i) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i + u >= nc) break;
+      const uint32_t kb = kw + W * (i + u);
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
         const uint32_t c[4] = {bt.w[u][j].x, bt.w[u][j].y, bt.w[u][j].z, bt.w[u][j].w};
 #pragma unroll
         for (int g = 0; g < S; ++g) {
-          const uint32_t z = ZERO ? zero_bytes(bt.z[ZERO ? u : 0][j][g]) : 0u;
-          const uint2 sb = bt.s[u][j][g];
-          constexpr float one = ZERO ? 1.0f : kSymScale;
-          const float sc[4] = {scale_f32(sb.x & 0xFFFF, a.fp16) * one, scale_f32(sb.x >> 16, a.fp16) * one,
-                               scale_f32(sb.y & 0xFFFF, a.fp16) * one, scale_f32(sb.y >> 16, a.fp16) * one};
+          const uint32_t z = ZERO ? zero_bytes(a.m[PAIR ? j & 1 : 0].zero(bt.z[ZERO ? u : 0][j] >> (8 * g))) : 0u;
+          float sc[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            sc[r] = scale_f32(bt.s[u][j][2 * g + (r >> 1)] >> (16 * (r & 1)) & 0xFFFF, FP16) *
+                    (ZERO ? 1.0f : kSymScale);
           f32x4 acc[MQ];
 #pragma unroll
           for (int q = 0; q < MQ; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -144,7 +180,11 @@ __global__ __launch_bounds__(256) void gemm_stream_w4(W4Args a) {
           for (int f = 0; f < F; ++f) {
             const bf16x8 wf = decode8<ZERO>(c[g * F + f], z);
 #pragma unroll
-            for (int q = 0; q < MQ; ++q) acc[q] = mfma16(wf, as_bf16x8(bt.x[u][q][g * F + f]), acc[q]);
+            for (int q = 0; q < MQ; ++q) {
+              const uint4 xv = XL ? *reinterpret_cast<const uint4*>(xl + xoff[q] + kb * 256 + (g * F + f) * 64)
+                                  : bt.x[XL ? 0 : u][q][g * F + f];
+              acc[q] = mfma16(wf, as_bf16x8(xv), acc[q]);
+            }
           }
 #pragma unroll
           for (int q = 0; q < MQ; ++q)
@@ -155,19 +195,39 @@ __global__ __launch_bounds__(256) void gemm_stream_w4(W4Args a) {
     }
   };
   Batch c0, c1;
-  if (nc > 0) load(c0, 0);
+  if constexpr (XL) {  // (one tile of rows: m0 = 0)
+    // the first pieces of x, then both batches of weights behind them; the barrier waits for LDS alone
+    constexpr int A = 2;
+    const int per = K / 8, n = rows * per;  // 16-byte pieces of a row, of x
+    auto place = [&](int i) { return reinterpret_cast<uint4*>(xl + (i / per) * xl_stride(K) + (i % per) * 16); };
+    uint4 v[A];
+#pragma unroll
+    for (int q = 0; q < A; ++q) v[q] = gload16(a.x, (uint32_t)min((int)threadIdx.x + q * 64 * W, n - 1) * 16);
+    if (nc > 0) load(c0, 0);
+    if (U < nc) load(c1, U);
+#pragma unroll
+    for (int q = 0; q < A; ++q)
+      if ((int)threadIdx.x + q * 64 * W < n) *place(threadIdx.x + q * 64 * W) = v[q];
+    for (int i = threadIdx.x + A * 64 * W; i < n; i += 64 * W) *place(i) = gload16(a.x, (uint32_t)i * 16);
+    asm volatile("" ::: "memory");
+    MOE_WAITCNT(63, 0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  } else {
+    if (nc > 0) load(c0, 0);
+  }
   for (int i = 0; i < nc; i += 2 * U) {
-    if (i + U < nc) load(c1, i + U);
+    if (i + U < nc && !(XL && i == 0)) load(c1, i + U);
     compute(c0, i);
     if (i + 2 * U < nc) load(c0, i + 2 * U);
     if (i + U < nc) compute(c1, i + U);
   }
   // every wavefront parks its sums but those of the outputs it finishes itself: output p goes to wavefront
-  // p % 4, slot order (p, wavefront)
+  // p % W, slot order (p, wavefront)
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    if (p % 4 == kw) continue;
-    float* dst = red + (p * 3 + (kw < p % 4 ? kw : kw - 1)) * (PC * 256) + lane;
+    if (p % W == kw) continue;
+    float* dst = red + (p * (W - 1) + (kw < p % W ? kw : kw - 1)) * (PC * 256) + lane;
 #pragma unroll
     for (int c = 0; c < PC; ++c)
 #pragma unroll
@@ -176,8 +236,8 @@ __global__ __launch_bounds__(256) void gemm_stream_w4(W4Args a) {
   __syncthreads();
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    if (p % 4 != kw) continue;
-    const float* src = red + p * 3 * (PC * 256) + lane;
+    if (p % W != kw) continue;
+    const float* src = red + p * (W - 1) * (PC * 256) + lane;
     float v[PC][4];
 #pragma unroll
     for (int c = 0; c < PC; ++c)
@@ -185,7 +245,7 @@ __global__ __launch_bounds__(256) void gemm_stream_w4(W4Args a) {
       for (int r = 0; r < 4; ++r) {
         v[c][r] = tot[p / MQ * PC + c][p % MQ][r];
 #pragma unroll
-        for (int w = 0; w < 3; ++w) v[c][r] += src[w * (PC * 256) + (c * 4 + r) * 64];
+        for (int w = 0; w < W - 1; ++w) v[c][r] += src[w * (PC * 256) + (c * 4 + r) * 64];
       }
     // lane holds weight rows 4 kg + r of row r16 of x
     const int r = p % MQ * 16 + r16, b = b0 + p / MQ;
@@ -251,24 +311,35 @@ __global__ __launch_bounds__(256, 2) void gemm_tile_w4(W4Args a) {
             (lds_void*)(codes + j * 1024));
   };
   // Scales (16 bits per row) and zero points (8) of a chunk wait in registers.
-  uint32_t sc[S][2], zb[S][PAIR ? 2 : 1];
+  uint32_t sc[S][2], zb[C * S / 4 ? C * S / 4 : 1][PAIR ? 2 : 1];
   auto load_scales = [&](int kb) {
     // (opaque: the compiler would keep a 64-bit address for each of these loads)
     uint32_t at = woff;
     asm volatile("" : "+v"(at));
-    at = (at >> 10) * (16 * S) + (nl & 15);  // (16 rows of every group)
+    at = (at >> 10) * (16 * S);  // (16 rows of every group)
+    const uint32_t e = at + ((nl & 15) >> 2) * (4 * S) + (nl & 3), ze = at + (nl & 15) * S;
 #pragma unroll
-    for (int g = 0; g < S; ++g) {
-      const uint32_t e = (kb * S + g) * 16 + at;
+    for (int c = 0; c < (PAIR ? 2 : 1); ++c) {
+      const char* s = static_cast<const char*>(a.m[c].scales) + (size_t)kb * (32 * S);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        sc[g][c] = gload4(a.m[PAIR ? c : 0].scales, (e + (PAIR ? 0 : 2 * c)) * 2);
-        if (ZERO && PAIR) {
-          const uint8_t* z = a.m[c].zeros;
-          zb[g][PAIR ? c : 0] = z ? gload_u8(z, e) | gload_u8(z, e + 1) << 8 : 0x0808u;
+      for (int g = 0; g < S; ++g) {
+        if (PAIR) {
+          sc[g][c] = gload4(s, (e + g * 4) * 2);
+        } else {
+          const uint2 v = gload8(s, (e + g * 4) * 2);
+          sc[g][0] = v.x;
+          sc[g][1] = v.y;
         }
       }
-      if (ZERO && !PAIR) zb[g][0] = gload4(a.m[0].zeros, e);
+      if (ZERO) {
+        const uint8_t* z = a.m[c].zeros + (size_t)kb * (16 * S);
+        if (C * S == 2) {
+          zb[0][c] = gload_u16(z, ze);
+        } else {
+#pragma unroll
+          for (int i = 0; i < C * S / 4; ++i) zb[i][c] = gload4(z, ze + 4 * i);
+        }
+      }
     }
   };
   load_x(0, 0);
@@ -295,16 +366,17 @@ __global__ __launch_bounds__(256, 2) void gemm_tile_w4(W4Args a) {
       float s[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t b = PAIR ? sc[g][j >> 1] >> (16 * (j & 1)) : sc[g][j >> 1] >> (16 * (j & 1));
+        const uint32_t b = sc[g][j >> 1] >> (16 * (j & 1));
         s[j] = (a.fp16 ? scale_f32(b & 0xFFFF, true) : scale_f32(b & 0xFFFF, false)) * (ZERO ? 1.0f : kSymScale);
       }
       bf16x8 wf[4][F];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t c[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
-        const uint32_t z = !ZERO ? 0u : PAIR ? zb[g][PAIR ? j >> 1 : 0] >> (8 * (j & 1)) : zb[g][0] >> (8 * j);
+        const int zi = (j % C) * S + g;  // (row by row, its groups)
+        const uint32_t z = ZERO ? zb[zi / 4][PAIR ? j >> 1 : 0] >> (8 * (zi % 4)) : 0u;
 #pragma unroll
-        for (int f = 0; f < F; ++f) wf[j][f] = decode8<ZERO>(c[g * F + f], ZERO ? zero_bytes(z & 255) : 0u);
+        for (int f = 0; f < F; ++f) wf[j][f] = decode8<ZERO>(c[g * F + f], ZERO ? zero_bytes(a.m[PAIR ? j >> 1 : 0].zero(z)) : 0u);
       }
       // (behind the last use of this chunk's; the loop's head waits for them)
       if (g == S - 1) load_scales(next);
@@ -312,35 +384,49 @@ __global__ __launch_bounds__(256, 2) void gemm_tile_w4(W4Args a) {
       auto read_x = [&](int t, int f) {
         return as_bf16x8(*reinterpret_cast<const uint4*>(ring + ((xa ^ ((g * F + f) * 64)) + t * 4096)));
       };
-      // Operand f of tile t lies in slot (F t + f) mod X: half of a tile's are read ahead of its use, the rest as
-      // the tile before has used its own up (with a whole second tile's the registers do not suffice).
-      constexpr int H = F / 2, X = F + (H ? H : 1);
+      // Operand f of tile t lies in slot (F t + f) mod X: a tile's first is read ahead, the rest as the tile before
+      // has used its own up (with a whole second tile's the registers do not suffice).
+      constexpr int X = F + 1;
       bf16x8 xf[X];
 #pragma unroll
       for (int f = 0; f < F; ++f) xf[f] = read_x(0, f);
-      f32x4 acc[2];
+      f32x4 acc[2][2];
 #pragma unroll
-      for (int i = 0; i <= 32; ++i) {  // fragment i % 4 of tile i / 4, and the totals of the one before
-        const int t = i >> 2, j = i & 3;
-        if (i < 32) {
+      for (int i = 0; i <= 16; ++i) {  // fragments 2 (i % 2) and + 1 of tile i / 2, and the totals of the ones before
+        const int t = i >> 1, j = (i & 1) * 2;
+        if (i < 16) {
           __builtin_amdgcn_sched_barrier(0);
           if (j == 0 && t < 7) {
 #pragma unroll
             for (int f = 0; f < X - F; ++f) xf[(F * (t + 1) + f) % X] = read_x(t + 1, f);
           }
-          acc[i & 1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) acc[i & 1][e] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int f = 0; f < F; ++f) {
-            acc[i & 1] = mfma16(xf[(F * t + f) % X], wf[j][f], acc[i & 1]);
-            if (j == 3 && t < 7 && f + X - F < F) xf[(F * (t + 1) + f + X - F) % X] = read_x(t + 1, f + X - F);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) acc[i & 1][e] = mfma16(xf[(F * t + f) % X], wf[j + e][f], acc[i & 1][e]);
+            if (j == 2 && t < 7 && f + X - F < F) xf[(F * (t + 1) + f + X - F) % X] = read_x(t + 1, f + X - F);
           }
         }
         if (i > 0) {
-          const int u = (i - 1) >> 2, v = (i - 1) & 3;
+          const int u = (i - 1) >> 1, v = ((i - 1) & 1) * 2;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) tot[v][u][r] = fmaf(s[v], acc[(i - 1) & 1][r], tot[v][u][r]);
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) tot[v + e][u][r] = fmaf(s[v + e], acc[(i - 1) & 1][e][r], tot[v + e][u][r]);
+          }
+          if (i < 16) {
+#pragma unroll
+            for (int q = 0; q < 2 * F; ++q) {
+              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x002, 8 / (2 * F) ? 8 / (2 * F) : 1, 0);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
           // (the sums are taken here: moved behind the chunk's other MFMAs they would keep every acc)
           asm volatile("" : "+v"(tot[v][u]));
+          asm volatile("" : "+v"(tot[v + 1][u]));
         }
       }
     }
@@ -362,35 +448,63 @@ __global__ __launch_bounds__(256, 2) void gemm_tile_w4(W4Args a) {
     }
 }
 
-template <int GROUP, bool PAIR, bool ZERO>
-hipError_t launch_tiles(W4Args a, hipStream_t s) {
-  if (a.M > 64) {
-    a.mtiles = (a.M + kTileM - 1) / kTileM;
-    const unsigned grid = (unsigned)a.mtiles * ((a.N + (PAIR ? 127 : 255)) / (PAIR ? 128 : 256));
-    gemm_tile_w4<GROUP, PAIR, ZERO><<<grid, 256, 0, s>>>(a);
-    return hipGetLastError();
-  }
-  constexpr int NR = 2;
-  const int mq = a.M <= 16 ? 1 : 2;
-  a.mtiles = (a.M + 16 * mq - 1) / (16 * mq);
-  const int per = PAIR ? NR / 2 : NR;
+// (One loop per type of scale: with the choice inside it the sums would be taken behind a branch, where every
+// accumulator has to be kept.)
+template <int MQ, int NR, int GROUP, bool PAIR, bool ZERO, int W, bool XL>
+__global__ __launch_bounds__(64 * W) void gemm_stream_w4(W4Args a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  if (a.fp16) stream_w4<MQ, NR, GROUP, PAIR, ZERO, W, XL, true>(a, lds);
+  else stream_w4<MQ, NR, GROUP, PAIR, ZERO, W, XL, false>(a, lds);
+}
+
+template <int MQ, int NR, int GROUP, bool PAIR, bool ZERO, int W, bool XL>
+hipError_t launch_stream(W4Args a, hipStream_t s) {
+  constexpr int PC = PAIR ? 2 : 1, per = NR / PC;
+  a.mtiles = (a.M + 16 * MQ - 1) / (16 * MQ);
   const unsigned grid = (unsigned)a.mtiles * ((a.N / 16 + per - 1) / per);
-  auto* kernel = mq == 1 ? &gemm_stream_w4<1, NR, GROUP, PAIR, ZERO> : &gemm_stream_w4<2, NR, GROUP, PAIR, ZERO>;
-  kernel<<<grid, 256, 0, s>>>(a);
+  const int lds = MQ * NR * (W - 1) * 1024 + (XL ? a.M * xl_stride(a.K) : 0);
+  gemm_stream_w4<MQ, NR, GROUP, PAIR, ZERO, W, XL><<<grid, 64 * W, lds, s>>>(a);
   return hipGetLastError();
 }
+// The streaming tiles, unless there are so many (16 weight rows by 32 rows of x each, a unit of work per 128
+// columns) that the MFMA tiles, which need as long for one as for 128 rows, take less.  Microseconds, streaming and
+// MFMA tiles, at rows x weight rows x columns (tiles per CU): group 128, 256 x 7168 x 7168 (14) 79 and 122, 512
+// (28) 135 and 123, 1024 x 2048 x 2048 (16) 31 and 38, 2048 (32) 59 and 39; group 32 pair, 512 x 2048 x 7168
+// (16) 135 and 193, 1024 (32) 266 and 193.
+constexpr int kStreamTilesPerCu = 24;
+template <int GROUP, bool PAIR, bool ZERO>
+hipError_t launch_tiles(W4Args a, int num_cus, hipStream_t s) {
+  const int64_t blocks = a.N / 16 * (PAIR ? 2 : 1), mtiles = (a.M + 31) / 32;
+  if (a.M > 32 && mtiles * blocks > (int64_t)kStreamTilesPerCu * num_cus) {
+    a.mtiles = (a.M + kTileM - 1) / kTileM;
+    const int64_t grid = (int64_t)a.mtiles * ((a.N + (PAIR ? 127 : 255)) / (PAIR ? 128 : 256));
+    gemm_tile_w4<GROUP, PAIR, ZERO><<<(unsigned)grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  if (a.M <= 16) {
+    // x in LDS where it fits (1 x 7168 x 7168 11.2 us, 12.3 with x from L2; 16 rows of 7168 do not)
+    if (a.M * xl_stride(a.K) <= kXlBytes) return launch_stream<1, PAIR ? 2 : 1, GROUP, PAIR, ZERO, 8, true>(a, s);
+    return launch_stream<1, 2, GROUP, PAIR, ZERO, 8, false>(a, s);
+  }
+  // 64 weight rows a workgroup halve what is read of x, where there are workgroups for half the CUs (64 x 7168 x
+  // 7168 23 us, 33 with 32; 64 x 2048 x 2048 8.9 and 7.4).  Groups of 128 only: the registers hold no more scales.
+  if constexpr (GROUP == 128) {
+    if (2 * mtiles * ((blocks + 3) / 4) >= num_cus) return launch_stream<2, 4, GROUP, PAIR, ZERO, 8, false>(a, s);
+  }
+  return launch_stream<2, 2, GROUP, PAIR, ZERO, 8, false>(a, s);
+}
 template <int GROUP>
-hipError_t launch_group(const W4Args& a, hipStream_t s) {
-  const bool zero = a.m[0].zeros || a.m[1].zeros;
-  if (a.m[1].codes) return zero ? launch_tiles<GROUP, true, true>(a, s) : launch_tiles<GROUP, true, false>(a, s);
-  return zero ? launch_tiles<GROUP, false, true>(a, s) : launch_tiles<GROUP, false, false>(a, s);
+hipError_t launch_group(const W4Args& a, int cus, hipStream_t s) {
+  const bool zero = a.m[0].zeros;  // (of either matrix, kernels.h)
+  if (a.m[1].codes) return zero ? launch_tiles<GROUP, true, true>(a, cus, s) : launch_tiles<GROUP, true, false>(a, cus, s);
+  return zero ? launch_tiles<GROUP, false, true>(a, cus, s) : launch_tiles<GROUP, false, false>(a, cus, s);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_w4(const W4Args& a, int group, int num_cus, hipStream_t s) {
-  (void)num_cus;
-  return group == 32 ? launch_group<32>(a, s) : group == 64 ? launch_group<64>(a, s) : launch_group<128>(a, s);
+  return group == 32   ? launch_group<32>(a, num_cus, s)
+         : group == 64 ? launch_group<64>(a, num_cus, s) : launch_group<128>(a, num_cus, s);
 }
 
 hipError_t launch_w4_tile(const W4Mat& src, int N, int K, int group, void* codes, void* scales, uint8_t* zeros,
@@ -398,10 +512,9 @@ hipError_t launch_w4_tile(const W4Mat& src, int N, int K, int group, void* codes
   const int64_t nw = (int64_t)N * K / 8, ns = (int64_t)N * (K / group);
   w4_tile_kernel<<<(unsigned)((nw + 255) / 256), 256, 0, s>>>(static_cast<const uint32_t*>(src.codes),
                                                               static_cast<uint32_t*>(codes), nw, K / 128);
-  const unsigned grid = (unsigned)((ns + 255) / 256);
-  w4_scale_tile_kernel<uint16_t><<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(src.scales),
-                                                      static_cast<uint16_t*>(scales), ns, K / group);
-  if (src.zeros) w4_scale_tile_kernel<uint8_t><<<grid, 256, 0, s>>>(src.zeros, zeros, ns, K / group);
+  w4_scale_tile_kernel<<<(unsigned)((ns + 255) / 256), 256, 0, s>>>(
+      static_cast<const uint16_t*>(src.scales), src.zeros, static_cast<uint16_t*>(scales), zeros, ns, K / group,
+      128 / group);
   return hipGetLastError();
 }
 

@@ -310,8 +310,12 @@ hipError_t launch_route_scored_grad(const float* logits, const int32_t* ids, con
                                     hipStream_t s);
 
 // 4-bit weights: x [M][K] bf16 by one matrix, or by the gate and up pair (m[1].codes not null), tiled.
+// A kernel that takes zero points takes them of both matrices: one without them has the other's pointer, read but
+// not looked at, and all_zero (its zero point, 8) in their place.
 struct W4Mat {
-  const void* codes; const void* scales; const uint8_t* zeros;  // (zeros null: 8)
+  const void* codes; const void* scales; const uint8_t* zeros;
+  uint32_t zero_mask, all_zero;  // (0xFF and 0, or 0 and 8)
+  __device__ uint32_t zero(uint32_t z) const { return (z & zero_mask) | all_zero; }
 };
 struct W4Args {
   const void* x;

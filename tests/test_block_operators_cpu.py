@@ -111,6 +111,7 @@ def test_gemm_w4_refusals(L):
     assert call(N=0) == INV and call(K=0) == INV and call(N=-16) == INV
     assert call(N=24) == UNS and call(K=192) == UNS and call(group=256) == UNS and call(group=0) == UNS
     assert call(fmt=2) == UNS and call(N=1 << 16, K=1 << 16) == UNS and call(M=1 << 24) == UNS
+    assert call(M=1 << 14, N=1 << 23) == UNS  # 2^37 outputs
     assert call(layout=moe.LAYOUT_ROW_MAJOR) == INV
     for name in ("x", "y", "codes", "scales"):
         assert call(**{name: None}) == INV
