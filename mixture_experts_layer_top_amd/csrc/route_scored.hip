@@ -73,15 +73,12 @@ __device__ __forceinline__ void scores64(const float (&l)[VPL], int E, int score
   for (int i = 0; i < VPL; ++i) s[i] = sum == 0.0 ? 0.0 : s[i] / sum;
 }
 
+// One token by the whole wavefront, compared in 64 bits.  s_key: 64 * VPL keys of LDS of its own (groups).
 template <int VPL>
-__global__ __launch_bounds__(256) void route_scored_kernel(const float* __restrict__ logits,
-                                                           const float* __restrict__ bias, int T, int E,
-                                                           int k, Scoring p, int32_t* __restrict__ ids,
-                                                           float* __restrict__ w) {
-  __shared__ uint64_t s_key[4][64 * VPL];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int t = blockIdx.x * 4 + wv;
-  if (t >= T) return;  // (whole wavefronts; no barrier below)
+__device__ __forceinline__ void route_exact(const float* __restrict__ logits, const float* __restrict__ bias,
+                                            int t, int E, int k, const Scoring& p, uint64_t* s_key,
+                                            int32_t* __restrict__ ids, float* __restrict__ w) {
+  const int lane = threadIdx.x & 63;
   float l[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -102,21 +99,26 @@ __global__ __launch_bounds__(256) void route_scored_kernel(const float* __restri
   if (p.groups > 1) {
     const int size = E / p.groups;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) s_key[wv][lane + 64 * i] = __builtin_bit_cast(uint64_t, c[i]);
+    for (int i = 0; i < VPL; ++i) s_key[lane + 64 * i] = __builtin_bit_cast(uint64_t, c[i]);
     __builtin_amdgcn_wave_barrier();
     uint64_t gk = 0;
     if (lane < p.groups) {
       // (by keys, so that a NaN stays at the bottom)
       uint64_t k0 = 0, k1 = 0;
       double a = 0.0, b = 0.0;
-      for (int j = 0; j < size; ++j) {
-        const double v = __builtin_bit_cast(double, s_key[wv][lane * size + j]);
-        const uint64_t kv = key64(v);
-        if (kv > k0) {
-          k1 = k0; b = a;
-          k0 = kv; a = v;
-        } else if (kv > k1) {
-          k1 = kv; b = v;
+      for (int j = 0; j < size; j += 4) {
+        double v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = __builtin_bit_cast(double, s_key[lane * size + min(j + q, size - 1)]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint64_t kv = j + q < size ? key64(v[q]) : 0;
+          if (kv > k0) {
+            k1 = k0; b = a;
+            k0 = kv; a = v[q];
+          } else if (kv > k1) {
+            k1 = kv; b = v[q];
+          }
         }
       }
       gk = key64(p.group_top > 1 ? a + b : a);
@@ -172,6 +174,290 @@ __global__ __launch_bounds__(256) void route_scored_kernel(const float* __restri
   if (lane < k) {
     ids[(size_t)t * k + lane] = my_id;
     w[(size_t)t * k + lane] = float(my_s * (double)p.scale);
+  }
+}
+
+template <int VPL>
+__global__ __launch_bounds__(64) void route_exact_kernel(const float* __restrict__ logits,
+                                                         const float* __restrict__ bias, int E, int k,
+                                                         Scoring p, int32_t* __restrict__ ids,
+                                                         float* __restrict__ w) {
+  __shared__ uint64_t s_key[64 * VPL];
+  route_exact<VPL>(logits, bias, blockIdx.x, E, k, p, s_key, ids, w);
+}
+
+// ------------------------------------------------------------------------------------------------
+// 16 lanes per token
+//
+// Lane i of a token holds experts i v .. i v + v - 1 (v = ceil(E / 16)) and their c in fp32.  A key is c's
+// place below the row's largest, in 23 bits, above the expert's complement in 9: unsigned order is c's order
+// and ties go to the lower id, so one register carries an expert through the sort.  Each lane keeps its eight
+// largest keys in order (one med3 per place and key), then four exchanges with other lanes merge the lists
+// (the larger of each with the other's reversed, and a bitonic sort of eight).
+//
+// fp32 and 23 bits do not decide everything.  Where two of the first k + 1 keys are nearer than their errors (a row
+// in some hundred), the first nine are compared again in 64 bits, a lane each.  Where that cannot help (the
+// ninth and tenth are near too, or the last group that stays and the first that does not), and where anything
+// infinite, masked or NaN is among them, the token is routed again by route_exact.
+// ------------------------------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ uint32_t from(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float from(float v) { return __uint_as_float(from<CTRL>(__float_as_uint(v))); }
+
+__device__ __forceinline__ uint32_t med3(uint32_t a, uint32_t b, uint32_t c) {
+  return max(min(a, b), min(max(a, b), c));
+}
+// Descending order: larger first.
+__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
+  const uint32_t m = max(a, b);
+  b = min(a, b);
+  a = m;
+}
+// The eight largest of two lanes' lists, in order, in both lanes.
+template <int CTRL>
+__device__ __forceinline__ void merge8(uint32_t (&v)[8]) {
+  uint32_t m[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m[j] = max(v[j], from<CTRL>(v[7 - j]));
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!(j & d)) order(m[j], m[j + d]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = m[j];
+}
+// The two largest of two lanes' pairs a >= b.
+template <int CTRL>
+__device__ __forceinline__ void merge2(float& a, float& b) {
+  const float x = from<CTRL>(a), y = from<CTRL>(b);
+  b = fmaxf(fminf(a, x), fmaxf(b, y));
+  a = fmaxf(a, x);
+}
+__device__ __forceinline__ float max16(float v) {
+  return reduce16(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+constexpr float kPlaces = 0x1p23f;  // of a key
+
+template <int V, bool VEC>
+__global__ __launch_bounds__(64) void route_scored_kernel(const float* __restrict__ logits,
+                                                          const float* __restrict__ bias, int T, int E,
+                                                          int k, Scoring p, int32_t* __restrict__ ids,
+                                                          float* __restrict__ w) {
+  constexpr int VPL = V <= 4 ? 1 : V <= 8 ? 2 : V <= 16 ? 4 : 8;
+  __shared__ uint64_t s_key[64 * VPL];
+  const int lane = threadIdx.x, li = lane & 15;
+  const int tok = blockIdx.x * 4 + (lane >> 4);
+  const int t = min(tok, T - 1);  // (a token past the last is the last again, and not written)
+  const int v = VEC ? V : (E + 15) >> 4, e0 = li * v;
+  const size_t row = (size_t)t * E;
+  float l[V], c[V];
+  auto load4 = [&](const float* from, float* to) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const uint4 q = gload16(from, (e0 + i) * 4);
+      to[i] = __uint_as_float(q.x);
+      to[i + 1] = __uint_as_float(q.y);
+      to[i + 2] = __uint_as_float(q.z);
+      to[i + 3] = __uint_as_float(q.w);
+    }
+  };
+  if (VEC) {
+    load4(logits + row, l);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = e0 + i;
+      l[i] = i < v && e < E ? logits[row + min(e, E - 1)] : -kInf;
+    }
+  }
+  // scores, and a softmax's largest logit and 1 / sum
+  float top = -kInf, inv = 1.0f;
+  if (p.score == kScoreSoftmax) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+    top = max16(top);
+    if (p.renorm) {  // (for the selection only)
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += __expf(l[i] - top);
+      inv = 1.0f / reduce16(sum, SumOp{});
+    } else {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += (double)expf(l[i] - top);
+      inv = 1.0f / (float)reduce16(sum, SumOp{});
+    }
+  }
+  const bool scored = bias || (p.groups > 1 && p.group_top > 1);
+  if (!scored) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = l[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float s = p.score == kScoreSoftmax ? __expf(l[i] - top) * inv
+                                               : __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
+      c[i] = l[i] == -kInf ? -kInf : s;
+    }
+    if (bias) {
+      float b[V];
+      if (VEC) {
+        load4(bias, b);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) b[i] = bias[min(e0 + i, E - 1)];
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] += b[i];
+    }
+  }
+  // a sigmoid's fp32 value is within 2^-22 (its slope makes up for the exponential's argument), a softmax's within
+  // 2^-18 of the largest one, 1 / sum (its exponentials and up to 36 additions); c adds |c| 2^-24
+  const float tol_s = !scored ? 0.f : p.score == kScoreSoftmax ? inv * 0x1p-18f : 0x1p-21f;
+  bool kept = true, unsure = false;
+  if (p.groups > 1) {  // (16 / groups lanes hold a group)
+    const int lg = 16 / p.groups;
+    float a = -kInf, b = -kInf;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      b = fmaxf(b, fminf(a, c[i]));
+      a = fmaxf(a, c[i]);
+    }
+    if (lg >= 2) merge2<0xb1>(a, b);
+    if (lg >= 4) merge2<0x4e>(a, b);
+    if (lg >= 8) merge2<0x141>(a, b);
+    const float g = p.group_top > 1 ? a + b : a;
+    const float size = fabsf(a) + (p.group_top > 1 ? fabsf(b) : 0.f);
+    const float far = 2.0f * tol_s + max16(size < kInf ? size : 0.f) * (scored ? 0x1p-22f : 0.f);
+    int above = 0, near = 0;
+    auto against = [&](float o) {
+      const float d = o - g;
+      above += d > far ? 1 : 0;
+      near += !(fabsf(d) > far) ? 1 : 0;  // (or not to be compared: two groups masked whole)
+    };
+#define MOE_ROT(n) if (p.groups == 16 || (n) % lg == 0) against(from<0x120 + (n)>(g));
+    MOE_ROT(1) MOE_ROT(2) MOE_ROT(3) MOE_ROT(4) MOE_ROT(5) MOE_ROT(6) MOE_ROT(7) MOE_ROT(8)
+    MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
+#undef MOE_ROT
+    kept = above + near < p.top;
+    unsure = !kept && above < p.top;
+    if (!bias) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = l[i];
+    }
+  }
+  // keys: places below the largest c that stays
+  float high = -kInf;
+#pragma unroll
+  for (int i = 0; i < V; ++i) high = fmaxf(high, c[i]);
+  high = max16(kept ? high : -kInf);
+  // (values further below the largest than the span have place 0.  A place is off by half a step of c - base,
+  // its rounding down and the id's carry into it: 3 between two without errors of their own)
+  const float span = bias ? 2.0f : 16.0f, scale = kPlaces / span, base = high - span * (1.0f - 0x1p-20f);
+  const int apart = 2 + (int)fminf((bias ? 2.0f * tol_s + fabsf(high) * 0x1p-22f : 0.f) * scale + 1.0f, 1e6f);
+  uint32_t best[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) best[j] = 0u;
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = e0 + i;
+    const uint32_t place = (uint32_t)fminf(fmaxf((c[i] - base) * scale, 0.0f), kPlaces - 1.0f);  // (NaN: 0)
+    key[i] = kept && (VEC || (i < v && e < E)) ? (place << 9) + (uint32_t)(512 - e) : 0u;
+#pragma unroll
+    for (int j = 7; j > 0; --j)
+      if (j <= i) best[j] = med3(key[i], best[j - 1], best[j]);
+    best[0] = max(best[0], key[i]);
+  }
+  merge8<0xb1>(best);
+  merge8<0x4e>(best);
+  merge8<0x141>(best);
+  merge8<0x140>(best);
+  uint32_t next = 0u;  // the largest that is not among them
+#pragma unroll
+  for (int i = 0; i < V; ++i) next = max(next, key[i] < best[7] ? key[i] : 0u);
+  next = max(next, from<0xb1>(next));
+  next = max(next, from<0x4e>(next));
+  next = max(next, from<0x141>(next));
+  next = max(next, from<0x140>(next));
+  // lane j keeps the j-th, lane 8 the one behind them
+  uint32_t mine = li == 8 ? next : 0u;
+  bool gap = false, close = false;  // a gap at or behind the k-th; two of the first k + 1 too near to tell
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t after = j < 7 ? best[j + 1] : next;
+    const bool apart_here = after == 0u || (int)(best[j] >> 9) - (int)(after >> 9) >= apart;
+    if (j < k) {
+      unsure |= best[j] < 2u << 9;  // (place 0: clamped, masked or NaN)
+      close |= !apart_here;
+    }
+    if (j >= k - 1) gap |= apart_here;
+    if (j == li) mine = best[j];
+  }
+  int id = (mine & 511u) ? 512 - (int)(mine & 511u) : 0, rank = li < 8 ? li : 16;
+  if (__ballot(close)) {
+    // candidates again, in 64 bits: right among them if a gap divides them from the rest
+    uint32_t last = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) last = max(last, key[i] < next ? key[i] : 0u);
+    last = max(last, from<0xb1>(last));
+    last = max(last, from<0x4e>(last));
+    last = max(last, from<0x141>(last));
+    last = max(last, from<0x140>(last));
+    gap |= last == 0u || (int)(next >> 9) - (int)(last >> 9) >= apart;
+    unsure |= close && !gap;
+    const bool in = mine >= 2u << 9;
+    double v64 = logits[row + min(id, E - 1)];
+    if (bias) {
+      if (p.score == kScoreSoftmax) {
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += exp((double)l[i] - (double)top);  // (-inf past E)
+        v64 = exp(v64 - (double)top) / reduce16(sum, SumOp{});
+      } else {
+        v64 = 1.0 / (1.0 + exp(-v64));
+      }
+      v64 += (double)bias[min(id, E - 1)];
+    }
+    if (!in) v64 = -__builtin_inf();
+    const int no = in ? id : 1024 + li;
+    int above = 0;
+    auto against = [&](double o, int n) { above += o > v64 || (o == v64 && n < no) ? 1 : 0; };
+#define MOE_ROT(n) against(dpp16<0x120 + (n)>(v64), dpp16<0x120 + (n)>(no));
+    MOE_ROT(1) MOE_ROT(2) MOE_ROT(3) MOE_ROT(4) MOE_ROT(5) MOE_ROT(6) MOE_ROT(7) MOE_ROT(8)
+    MOE_ROT(9) MOE_ROT(10) MOE_ROT(11) MOE_ROT(12) MOE_ROT(13) MOE_ROT(14) MOE_ROT(15)
+#undef MOE_ROT
+    if (close) rank = above;
+  }
+  const bool chosen = rank < k;
+  float lj = logits[row + min(id, E - 1)];
+  float s;
+  if (p.score == kScoreSoftmax) {
+    const float m = p.renorm ? max16(chosen ? lj : -kInf) : top;
+    s = expf(lj - m) * (p.renorm ? 1.0f : inv);
+    unsure |= !(fabsf(m) < kInf);
+  } else {
+    const float e = expf(-fabsf(lj));
+    s = (lj > 0.f ? 1.0f : e) / (1.0f + e);
+    if (p.renorm) unsure |= !(max16(chosen ? lj : -kInf) > -60.0f);  // (sums of the smallest floats)
+  }
+  if (p.renorm) s = s / reduce16(chosen ? s : 0.f, SumOp{});
+  // (unsure is a group's, a token's: any of its lanes)
+  const uint64_t ask = __ballot(unsure);
+  const bool redo = (ask >> (lane & 48)) & 0xFFFF;
+  if (tok < T && chosen && !redo) {
+    ids[(size_t)t * k + rank] = id;
+    w[(size_t)t * k + rank] = s * p.scale;
+  }
+  if (ask) {
+    for (int q = 0; q < 4; ++q)
+      if (((ask >> (16 * q)) & 0xFFFF) && (int)blockIdx.x * 4 + q < T)
+        route_exact<VPL>(logits, bias, blockIdx.x * 4 + q, E, k, p, s_key, ids, w);
   }
 }
 
@@ -249,10 +535,22 @@ __global__ __launch_bounds__(256) void route_scored_grad_kernel(
 hipError_t launch_route_scored(const float* logits, const float* bias, int T, int E, int k,
                                const Scoring& p, int32_t* ids, float* w, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const unsigned grid = ((unsigned)T + 3) / 4;
-  auto* kernel = E <= 64 ? &route_scored_kernel<1> : E <= 128 ? &route_scored_kernel<2>
-                 : E <= 256 ? &route_scored_kernel<4> : &route_scored_kernel<8>;
-  kernel<<<grid, 256, 0, s>>>(logits, bias, T, E, k, p, ids, w);
+  if (p.groups > 1 && (E % 16 || 16 % p.groups)) {  // (groups that lanes do not share out)
+    auto* kernel = E <= 64 ? &route_exact_kernel<1> : E <= 128 ? &route_exact_kernel<2>
+                   : E <= 256 ? &route_exact_kernel<4> : &route_exact_kernel<8>;
+    kernel<<<(unsigned)T, 64, 0, s>>>(logits, bias, E, k, p, ids, w);
+    return hipGetLastError();
+  }
+  const bool vec = E % 64 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
+  auto* kernel = vec && E == 64    ? &route_scored_kernel<4, true>
+                 : vec && E == 128 ? &route_scored_kernel<8, true>
+                 : vec && E == 256 ? &route_scored_kernel<16, true>
+                 : vec && E == 384 ? &route_scored_kernel<24, true>
+                 : vec && E == 512 ? &route_scored_kernel<32, true>
+                 : E <= 64         ? &route_scored_kernel<4, false>
+                 : E <= 128        ? &route_scored_kernel<8, false>
+                 : E <= 256        ? &route_scored_kernel<16, false> : &route_scored_kernel<32, false>;
+  kernel<<<((unsigned)T + 3) / 4, 64, 0, s>>>(logits, bias, T, E, k, p, ids, w);
   return hipGetLastError();
 }
 
