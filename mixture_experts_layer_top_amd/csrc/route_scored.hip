@@ -461,72 +461,84 @@ __global__ __launch_bounds__(64) void route_scored_kernel(const float* __restric
   }
 }
 
-// 2^lg lanes per token, as the softmax's gradient in grad.hip; WHOLE: a wavefront per token, since
-// every expert's score takes part.
-template <bool WHOLE>
+// Gradient, 16 lanes per token: lane j works out slot j's, and every lane then has all slots' (id, value) by
+// row broadcasts and writes its share of the row.  V > 0: every expert's score takes part (a softmax over
+// all), the logits of a lane's V experts stay in registers.  VEC: a lane has experts 64 c + 4 li .. + 3 (whole 16-byte
+// vectors, E % 4 == 0), else 16 c + li.
+template <int V, bool VEC>
 __global__ __launch_bounds__(256) void route_scored_grad_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ w,
-    const float* __restrict__ dw, int T, int E, int k, int lg, Scoring p, float* __restrict__ dl) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t t = at >> lg;
-  if (t >= T) return;
-  int id[kMaxTopK];
-  float v[kMaxTopK], u[kMaxTopK];
-  float dot = 0.f;
+    const float* __restrict__ dw, int T, int E, int k, Scoring p, float* __restrict__ dl) {
+  const int li = threadIdx.x & 15;
+  const int tok = (int)(((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4);
+  const int t = min(tok, T - 1);  // (all lanes of a wavefront take part in the sums)
+  const size_t row = (size_t)t * E, slot = (size_t)t * k + min(li, k - 1);
+  constexpr int N = VEC ? 4 : 1, C = V / N;  // experts per step, steps
+  auto at = [&](int c) { return VEC ? 64 * c + 4 * li : 16 * c + li; };
+  float l[V ? V : 1], top = -kInf;
 #pragma unroll
-  for (int j = 0; j < kMaxTopK; ++j) {
-    id[j] = -1;
-    v[j] = u[j] = 0.f;
-    if (j < k) {
-      id[j] = ids[t * k + j];
-      v[j] = w[t * k + j];
-      u[j] = dw[t * k + j];
-      dot = fmaf(v[j], u[j], dot);
+  for (int c = 0; c < C; ++c) {
+    if (VEC) {
+      const uint4 q = gload16(logits + row, min(at(c), E - 4) * 4);
+      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < N; ++i) l[V ? c * N + i : 0] = at(c) < E ? __uint_as_float(u[i]) : -kInf;
+    } else {
+      l[V ? c : 0] = at(c) < E ? logits[row + min(at(c), E - 1)] : -kInf;
     }
   }
-  const float off = p.renorm ? dot / p.scale : 0.f;
-#pragma unroll
-  for (int j = 0; j < kMaxTopK; ++j) {
-    v[j] *= u[j] - off;
-    if (p.score == kScoreSigmoid && j < k) {
-      const float l = (unsigned)id[j] < (unsigned)E ? logits[t * E + id[j]] : 0.f;
-      const float e = expf(-fabsf(l));  // (at most 1, whatever l)
-      v[j] *= (l > 0.f ? e : 1.0f) / (1.0f + e);  // 1 - s
-    }
+  const int id = ids[slot];
+  const float u = dw[slot];
+  float v = li < k ? w[slot] : 0.f;
+  const float dot = reduce16(li < k ? v * u : 0.f, SumOp{});
+  v *= li < k ? u - (p.renorm ? dot / p.scale : 0.f) : 0.f;
+  if (!V && p.score == kScoreSigmoid) {
+    const float lj = (unsigned)id < (unsigned)E ? logits[row + id] : 0.f;
+    const float e = expf(-fabsf(lj));  // (at most 1, whatever the logit)
+    v *= (lj > 0.f ? e : 1.0f) / (1.0f + e);  // 1 - s
   }
-  const int e0 = (int)(at & ((1 << lg) - 1));
-  if constexpr (WHOLE) {
-    float l[8], m = -kInf, sum = 0.f;
+  float f = 0.f;  // of all experts: - s_e * dot
+  if (V) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      l[i] = e0 + 64 * i < E ? logits[t * E + e0 + 64 * i] : -kInf;
-      m = fmaxf(m, l[i]);
-    }
-    m = wave_max(m);
+    for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+    top = max16(top);
+    double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      l[i] = m == -kInf ? 0.f : expf(l[i] - m);
-      sum += l[i];
+    for (int i = 0; i < V; ++i) {
+      l[i] = top == -kInf ? 0.f : expf(l[i] - top);
+      sum += (double)l[i];
     }
     sum = reduce16(sum, SumOp{});
-    sum = (read_lane(sum, 0) + read_lane(sum, 16)) + (read_lane(sum, 32) + read_lane(sum, 48));
-    const float f = sum == 0.f ? 0.f : dot / sum;
+    f = sum == 0.0 ? 0.f : -dot / (float)sum;
+  }
+  int sid[kMaxTopK];
+  float sv[kMaxTopK];
+#define MOE_SLOT(j)                                                                                  \
+  sid[j] = __builtin_amdgcn_update_dpp(0, id, 0x150 + j, 0xf, 0xf, false);                           \
+  sv[j] = from<0x150 + j>(v);                                                                        \
+  if (j >= k) sid[j] = -1;
+  MOE_SLOT(0) MOE_SLOT(1) MOE_SLOT(2) MOE_SLOT(3) MOE_SLOT(4) MOE_SLOT(5) MOE_SLOT(6) MOE_SLOT(7)
+#undef MOE_SLOT
+  if (tok >= T) return;
+  auto step = [&](int c, const float* mine) {
+    float o[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = e0 + 64 * i;
-      if (e >= E) continue;
-      float o = -l[i] * f;
+    for (int i = 0; i < N; ++i) {
+      o[i] = V ? mine[i] * f : 0.f;
 #pragma unroll
-      for (int j = 0; j < kMaxTopK; ++j) o += id[j] == e ? v[j] : 0.f;
-      dl[t * E + e] = o;
+      for (int j = 0; j < kMaxTopK; ++j) o[i] += sid[j] == at(c) + i ? sv[j] : 0.f;
     }
+    if (at(c) >= E) return;
+    if constexpr (VEC)
+      gstore16(dl + row, at(c) * 4, make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
+                                               __float_as_uint(o[3])));
+    else dl[row + at(c)] = o[0];
+  };
+  if constexpr (V > 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) step(c, l + c * N);
   } else {
-    for (int e = e0; e < E; e += 1 << lg) {
-      float o = 0.f;
-#pragma unroll
-      for (int j = 0; j < kMaxTopK; ++j) o += id[j] == e ? v[j] : 0.f;
-      dl[t * E + e] = o;
-    }
+    for (int c = 0; 16 * N * c < E; ++c) step(c, nullptr);
   }
 }
 
@@ -559,11 +571,12 @@ hipError_t launch_route_scored_grad(const float* logits, const int32_t* ids, con
                                     hipStream_t s) {
   if (T == 0) return hipSuccess;
   const bool whole = p.score == kScoreSoftmax && !p.renorm;
-  int lg = whole ? 6 : 0;
-  while (lg < 6 && (1 << lg) < E) ++lg;
-  const int64_t blocks = (((int64_t)T << lg) + 255) / 256;
-  auto* kernel = whole ? &route_scored_grad_kernel<true> : &route_scored_grad_kernel<false>;
-  kernel<<<(unsigned)blocks, 256, 0, s>>>(logits, ids, w, dw, T, E, k, lg, p, dl);
+  const bool vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dl)) % 16 == 0;
+  auto* kernel = !whole     ? vec ? &route_scored_grad_kernel<0, true> : &route_scored_grad_kernel<0, false>
+                 : E <= 128 ? vec ? &route_scored_grad_kernel<8, true> : &route_scored_grad_kernel<8, false>
+                 : E <= 256 ? vec ? &route_scored_grad_kernel<16, true> : &route_scored_grad_kernel<16, false>
+                            : vec ? &route_scored_grad_kernel<32, true> : &route_scored_grad_kernel<32, false>;
+  kernel<<<((unsigned)T + 15) / 16, 256, 0, s>>>(logits, ids, w, dw, T, E, k, p, dl);
   return hipGetLastError();
 }
 
