@@ -9,7 +9,10 @@
 // A gate per channel is the same in all rows, so both of the last two come from one sum, of H n1.
 //
 // Bound by HBM: x, h, dy and dh are read once and dx, dr written once, 12 bytes a value; H stays in fp32
-// registers between the two norms.
+// registers between the two norms. 8192 x 7168 takes 156 us (4.5 TB/s; a copy runs at 5.1), with a gate per token
+// 190 us (16 bytes a value, 4.9 TB/s). Few rows are bound by their chain of loads and two reductions instead:
+// 7.6 us for one row of 7168. Loading the next row ahead, loads past the caches and more or fewer workgroups than
+// four wavefronts per SIMD gave nothing.
 #include <algorithm>
 #include <type_traits>
 
@@ -70,16 +73,36 @@ __device__ __forceinline__ float value(const uint4& v, int j) {
   return j & 1 ? bf16_hi(p) : bf16_lo(p);
 }
 
+// sum + the squares of a vector's values, two at a time from their packed form.
+__device__ __forceinline__ float squares(const uint4& v, float sum) {
+  const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bf16x2_t b = __builtin_bit_cast(bf16x2_t, p[i]);
+    sum = __builtin_amdgcn_fdot2_f32_bf16(b, b, sum, false);
+  }
+  return sum;
+}
+
 // ROWS: a gate per token and channel, [T][d].
 template <int R, int V, bool ROWS>
 __global__ __launch_bounds__(R, 4) void block_grad_kernel(BlockGrad a, double inv_d, int nvec) {
-  __shared__ double red[2][7][R / 64];
+  __shared__ float red[2][4][R / 64];  // a row's four sums
+  __shared__ double wide[2][3][R / 64];
   const int i = threadIdx.x;
-  float sA[V][8], sP[V][8];
+  // Sums over the thread's rows, of H n1 and of dy n2. Beside two vectors of a row and of its gate the registers do
+  // not hold the latter: they take 64 KB of LDS per CU at every R, which four wavefronts per SIMD leave free.
+  constexpr bool kLds = ROWS && V == 2;
+  __shared__ float lds_sum[kLds ? V * 8 * R : 1];
+  float sA[V][8], sP[kLds ? 1 : V][8];
+  auto pre_sum = [&](int s, int j) -> float& {
+    if constexpr (kLds) return lds_sum[(s * 8 + j) * R + i];
+    else return sP[s][j];
+  };
 #pragma unroll
   for (int s = 0; s < V; ++s)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sA[s][j] = sP[s][j] = 0.f;
+    for (int j = 0; j < 8; ++j) sA[s][j] = pre_sum(s, j) = 0.f;
   const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
   int turn = 0;
   for (int row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
@@ -87,6 +110,10 @@ __global__ __launch_bounds__(R, 4) void block_grad_kernel(BlockGrad a, double in
     // their sums with every array's address instead: 20 registers a vector)
     const size_t base = (size_t)row * nvec * 16;
     auto rows = [&](const void* p, uint32_t off) { return gload16(static_cast<const char*>(p) + base, off); };
+    auto put = [&](char* p, uint32_t off, const uint4& v) {
+      if (a.once) gstore16_nt(p, off, v);
+      else gstore16(p, off, v);
+    };
     uint4 h[V], g[V], x[V], add[V], gt[V], wp[V], wq[V];
     uint32_t at[V];
 #pragma unroll
@@ -103,38 +130,36 @@ __global__ __launch_bounds__(R, 4) void block_grad_kernel(BlockGrad a, double in
       wp[s] = gload16(a.pre, c);
       if (!ROWS) wq[s] = a.in.post ? gload16(a.in.post, c) : ones;
     }
-    double sum[3] = {0.0, 0.0, 0.0};
+    float sum[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < V; ++s) {
-      float p = 0.f, c = 0.f, q = 0.f;
+      float c = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float hv = value(h[s], j), xv = value(x[s], j);
-        p = fmaf(hv, hv, p);
-        c = fmaf(value(g[s], j) * value(wp[s], j), hv, c);
-        q = fmaf(xv, xv, q);
+        c = fmaf(value(g[s], j) * value(wp[s], j), value(h[s], j), c);
         if (j & 1) __builtin_amdgcn_sched_barrier(0);  // (few unpacked values at a time)
       }
       if (i + R * s < nvec) {
-        sum[0] += (double)p;
-        sum[1] += (double)c;
-        sum[2] += (double)q;
+        sum[0] = squares(h[s], sum[0]);
+        sum[1] += c;
+        sum[2] = squares(x[s], sum[2]);
       }
     }
     // (two buffers in turn: a wavefront that is a row ahead writes the other one)
     row_reduce<R>(sum, red[turn][0], SumOp{});
-    if (!row_in_range(sum[0], inv_d, a.eps) || out_of_range(sum[1], inv_d)) {
+    double gh = (double)sum[1];
+    if (!row_in_range(sum[0], inv_d, a.eps) || out_of_range(gh, inv_d)) {
       double c[1] = {0.0};
 #pragma unroll
       for (int s = 0; s < V; ++s)
         if (i + R * s < nvec) add_products(h[s], g[s], wp[s], c[0]);
-      row_reduce<R>(c, red[turn][3], SumOp{});
-      sum[1] = c[0];
+      row_reduce<R>(c, wide[turn][0], SumOp{});
+      gh = c[0];
     }
     float up2, up1 = 1.0f, r1 = 1.0f;
-    const float r2 = rstd_of<R, V>(h, sum[0], inv_d, a.eps, i, nvec, red[turn][4], up2);
-    const float c2 = float(sum[1] * inv_d * (double)up2 * (double)r2 * (double)r2);
-    if (a.in.post) r1 = rstd_of<R, V>(x, sum[2], inv_d, a.eps, i, nvec, red[turn][5], up1);
+    const float r2 = rstd_of<R, V>(h, sum[0], inv_d, a.eps, i, nvec, wide[turn][1], up2);
+    const float c2 = float(gh * inv_d * (double)up2 * (double)r2 * (double)r2);
+    if (a.in.post) r1 = rstd_of<R, V>(x, sum[2], inv_d, a.eps, i, nvec, wide[turn][2], up1);
     // (unpacked anew behind the sums: values kept across the branches would not fit the registers)
 #pragma unroll
     for (int s = 0; s < V; ++s) {
@@ -144,7 +169,7 @@ __global__ __launch_bounds__(R, 4) void block_grad_kernel(BlockGrad a, double in
       if (!ROWS) wp[s] = opaque(wp[s]);
     }
     float n[V][8];  // the gradient that reaches the first norm (or x)
-    double back[1] = {0.0};
+    float back[1] = {0.f};
 #pragma unroll
     for (int s = 0; s < V; ++s) {
       const bool in = i + R * s < nvec;
@@ -162,7 +187,7 @@ __global__ __launch_bounds__(R, 4) void block_grad_kernel(BlockGrad a, double in
         for (int e = 0; e < 2; ++e) {
           const int j = 2 * w + e;
           const float hv = value(h[s], j), gv = value(g[s], j), gate = value(gt[s], j), post = value(wq[s], j);
-          sP[s][j] = fmaf(gv, hv * r2, sP[s][j]);
+          pre_sum(s, j) = fmaf(gv, hv * r2, pre_sum(s, j));
           const float H = fmaf(r2 * fmaf(-c2, hv, gv * value(wp[s], j)), up2, value(add[s], j));
           const float n1 = value(x[s], j) * r1, bH = a.in.bs * H;
           r[e] = a.in.rs * H;
@@ -172,33 +197,35 @@ __global__ __launch_bounds__(R, 4) void block_grad_kernel(BlockGrad a, double in
           q = fmaf(n[s][j], value(x[s], j), q);
         }
         // (the sums are taken here: moved to the row's end they would keep all their operands)
-        asm volatile("" : "+v"(sA[s][2 * w]), "+v"(sA[s][2 * w + 1]), "+v"(sP[s][2 * w]), "+v"(sP[s][2 * w + 1]));
+        asm volatile("" : "+v"(sA[s][2 * w]), "+v"(sA[s][2 * w + 1]));
+        if (!kLds) asm volatile("" : "+v"(pre_sum(s, 2 * w)), "+v"(pre_sum(s, 2 * w + 1)));
         dr[w] = pack_bf16x2(r[0], r[1]);
         if (ROWS) dg[w] = pack_bf16x2(t[0], t[1]);
         __builtin_amdgcn_sched_barrier(0);
       }
       if (in) {
         const uint32_t c = at[s];
-        gstore16(static_cast<char*>(a.dres) + base, c, make_uint4(dr[0], dr[1], dr[2], dr[3]));
+        put(static_cast<char*>(a.dres) + base, c, make_uint4(dr[0], dr[1], dr[2], dr[3]));
         if (ROWS && a.dgate_rows)
-          gstore16(static_cast<char*>(a.dgate_rows) + base, c, make_uint4(dg[0], dg[1], dg[2], dg[3]));
-        back[0] += (double)q;
+          put(static_cast<char*>(a.dgate_rows) + base, c, make_uint4(dg[0], dg[1], dg[2], dg[3]));
+        back[0] += q;
       }
     }
 #pragma unroll
     for (int s = 0; s < V; ++s) x[s] = opaque(x[s]);
     float c1 = 0.f;
     if (a.in.post) {
-      row_reduce<R>(back, red[turn][6], SumOp{});
-      if (out_of_range(back[0], inv_d)) {
-        back[0] = 0.0;
+      row_reduce<R>(back, red[turn][3], SumOp{});
+      double gx[1] = {(double)back[0]};
+      if (out_of_range(gx[0], inv_d)) {
+        gx[0] = 0.0;
 #pragma unroll
         for (int s = 0; s < V; ++s)
-          if (i + R * s < nvec) add_row_products(n[s], x[s], back[0]);
-        row_reduce<R>(back, red[turn][3], SumOp{});
+          if (i + R * s < nvec) add_row_products(n[s], x[s], gx[0]);
+        row_reduce<R>(gx, wide[turn][0], SumOp{});
       }
       // (of a small row, x and the sum hold `up` once, r1 its inverse)
-      c1 = float(back[0] * inv_d * (double)r1 * (double)r1);
+      c1 = float(gx[0] * inv_d * (double)r1 * (double)r1);
     }
 #pragma unroll
     for (int s = 0; s < V; ++s) {
@@ -206,7 +233,7 @@ __global__ __launch_bounds__(R, 4) void block_grad_kernel(BlockGrad a, double in
       unpack8(x[s], xv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = a.in.post ? r1 * fmaf(-c1, xv[j], n[s][j]) * up1 : n[s][j];
-      if (i + R * s < nvec) gstore16(static_cast<char*>(a.dx) + base, at[s], pack8(o));
+      if (i + R * s < nvec) put(static_cast<char*>(a.dx) + base, at[s], pack8(o));
     }
   }
   if (!a.part) return;
@@ -220,8 +247,8 @@ __global__ __launch_bounds__(R, 4) void block_grad_kernel(BlockGrad a, double in
       gstore16(p + j, 0, make_uint4(__float_as_uint(sA[s][j]), __float_as_uint(sA[s][j + 1]),
                                     __float_as_uint(sA[s][j + 2]), __float_as_uint(sA[s][j + 3])));
       gstore16(p + (size_t)nvec * 8 + j, 0,
-               make_uint4(__float_as_uint(sP[s][j]), __float_as_uint(sP[s][j + 1]),
-                          __float_as_uint(sP[s][j + 2]), __float_as_uint(sP[s][j + 3])));
+               make_uint4(__float_as_uint(pre_sum(s, j)), __float_as_uint(pre_sum(s, j + 1)),
+                          __float_as_uint(pre_sum(s, j + 2)), __float_as_uint(pre_sum(s, j + 3))));
     }
   }
 }
@@ -262,7 +289,10 @@ __global__ __launch_bounds__(256) void block_grad_sum_kernel(BlockGrad a, int nb
 
 int block_grad_parts(int T) { return rmsnorm_grad_parts(T); }
 
-hipError_t launch_block_grad(const BlockGrad& a, int d, hipStream_t s) {
+hipError_t launch_block_grad(BlockGrad a, int d, hipStream_t s) {
+  // Outputs pass the caches by when a call's rows are more than the 256 MB last-level cache holds (8192 x 7168 154
+  // us, 158 kept).
+  a.once = (int64_t)a.T * d * (a.in.gate_rows ? 16 : 12) > (int64_t)256 << 20;
   const int nvec = d / 8, nb = block_grad_parts(a.T);
   if (a.T > 0) {
     auto go = [&](auto Rc, auto Vc) {

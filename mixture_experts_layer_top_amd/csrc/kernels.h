@@ -292,9 +292,10 @@ struct BlockGrad {
   void* dx; void* dres; void* dgate_rows;
   float* dpre; float* dpost; float* dgate;
   float* part;
+  int once;  // (the launch's)
 };
 int block_grad_parts(int T);
-hipError_t launch_block_grad(const BlockGrad& a, int d, hipStream_t s);
+hipError_t launch_block_grad(BlockGrad a, int d, hipStream_t s);
 
 // Routing by scores.
 enum ScoreFn { kScoreSoftmax = 0, kScoreSigmoid = 1 };
