@@ -11,9 +11,15 @@
 //   sigmoid, renormalised  dl_j = (1 - s_j) w_j (dw_j - D / scale)      plain  (1 - s_j) w_j dw_j
 //   softmax, renormalised  dl_j = w_j (dw_j - D / scale)                plain  dl_e = [selected] w_e dw_e - s_e D
 //
-// One wavefront per token, lane l holding experts l, l + 64, ...; each of the k rounds takes the largest
-// remaining key, as in route_dev.h.  Keys are 64 bits wide: scores of different experts lie as near as
-// 2^-30 to each other in some row of a large batch, and which of them is selected is a result.
+// 16 lanes per token sort the experts in fp32 (route_scored_kernel); what fp32 cannot decide, scores that lie as
+// near as 2^-30 in some row of a large batch and rows with masked or non-finite logits, is decided in 64 bits,
+// since which expert is selected is a result: among the token's candidates, or by a wavefront over the whole row
+// (route_exact).
+//
+// Bound by its instructions, not by HBM: 8192 tokens of 256 experts in 8 groups take 10 us, without groups and
+// bias 5.4 (moe_route's wavefront per token 9.7), where their 8.9 MB take 2 us; one token 5 us. The gradient
+// writes all of dlogits and reads no more than k values per token, but for a softmax over all experts: 8192 x 256
+// 4.5 us and 5.9.
 #include "kernels.h"
 #include "rows_dev.h"
 
@@ -437,14 +443,15 @@ __global__ __launch_bounds__(64) void route_scored_kernel(const float* __restric
   const bool chosen = rank < k;
   float lj = logits[row + min(id, E - 1)];
   float s;
+  // (scores near fp32's smallest, whose last bits a factor or a renormalisation would bring out, by route_exact)
   if (p.score == kScoreSoftmax) {
     const float m = p.renorm ? max16(chosen ? lj : -kInf) : top;
     s = expf(lj - m) * (p.renorm ? 1.0f : inv);
-    unsure |= !(fabsf(m) < kInf);
+    unsure |= chosen && !(lj - m > -70.0f);
   } else {
     const float e = expf(-fabsf(lj));
     s = (lj > 0.f ? 1.0f : e) / (1.0f + e);
-    if (p.renorm) unsure |= !(max16(chosen ? lj : -kInf) > -60.0f);  // (sums of the smallest floats)
+    unsure |= chosen && !(lj > -70.0f);
   }
   if (p.renorm) s = s / reduce16(chosen ? s : 0.f, SumOp{});
   // (unsure is a group's, a token's: any of its lanes)

@@ -50,7 +50,7 @@ SHAPES = [  # T, E, k, groups, top_groups, group_top
     (1, 1, 1, 1, 1, 1), (1, 256, 8, 8, 4, 2), (3, 8, 2, 1, 1, 1), (5, 60, 4, 6, 3, 1), (7, 60, 4, 1, 1, 1), (77, 64, 8, 8, 3, 2),
     (130, 65, 5, 13, 7, 2), (64, 128, 8, 4, 1, 1), (33, 160, 6, 8, 3, 1), (300, 256, 8, 8, 4, 2),
     (257, 384, 8, 1, 1, 1), (9, 512, 8, 64, 8, 2), (11, 512, 8, 2, 2, 1), (4, 512, 1, 1, 1, 1), (6, 16, 8, 8, 4, 2),
-    (4, 7, 7, 7, 7, 1), (5, 320, 3, 5, 1, 2), (3, 511, 8, 1, 1, 2)]
+    (4, 7, 7, 7, 7, 1), (5, 320, 3, 5, 1, 2), (70, 96, 8, 12, 5, 2), (70, 192, 6, 3, 2, 2), (3, 511, 8, 1, 1, 2)]
 
 
 @pytest.mark.parametrize("T,E,k,groups,top,gt", SHAPES)
@@ -135,6 +135,43 @@ def test_route_scored_extreme_logits(moe):
     check(moe, l[:4], 4, sigmoid=False, tiny=2.0 ** -149)
     check(moe, l[:4], 4, sigmoid=False, renorm=False, tiny=2.0 ** -149)
     check(moe, l[:4], 4, _bias(32, 1, 1.0), sigmoid=False, tiny=2.0 ** -149)  # (scores of 1e-30 selected)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_scored_scores_near_fp32s_smallest(moe, sigmoid, renorm):
+    """Selected experts far below the first, whose scores fp32 holds in a few bits or none: a renormalisation or a
+    factor brings them back, with all their bits.  (2^-149: what a weight itself may be off by)"""
+    l = torch.full((6, 64), -200.0)
+    for i, low in enumerate((-60.0, -75.0, -88.0, -95.0, -100.0, -103.0)):
+        l[i, 3:9] = low - torch.arange(6) / 7.0
+        if not sigmoid:
+            l[i, 20] = 0.0  # (the softmax's largest)
+    check(moe, l, 6, sigmoid=sigmoid, renorm=renorm, scale=2.0 ** 100, tiny=2.0 ** -149)
+    check(moe, l, 6, sigmoid=sigmoid, renorm=renorm, scale=1.0, tiny=2.0 ** -149)
+
+
+@pytest.mark.parametrize("E,k,groups,top", [(256, 8, 8, 4), (256, 8, 1, 1), (64, 6, 1, 1), (384, 8, 1, 1)])
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_route_scored_of_any_address(moe, E, k, groups, top, sigmoid):
+    """Logits, bias and gradients that start at a multiple of 4 bytes, not of 16."""
+    T = 37
+    l, b = _logits(T, E, 3), _bias(E, 2, 0.05 if sigmoid else 0.004)
+
+    def moved(t):
+        return torch.cat([torch.zeros(1), t.flatten()]).cuda()[1:].view(t.shape)
+
+    for bias in (b, None):
+        kw = dict(groups=groups, top_groups=top, group_top=2, renorm=False)
+        want, ww = B.route_scored(f64(l), k, None if bias is None else f64(bias), sigmoid, **kw)
+        for ml in (moved, torch.Tensor.cuda):
+            for mb in (moved, torch.Tensor.cuda):
+                ids, w = moe.route_scored(ml(l), k, None if bias is None else mb(bias), score=SCORE[sigmoid], **kw)
+                assert np.array_equal(ids.cpu().numpy(), want) and (np.abs(f64(w) - ww) <= W * ww).all()
+        dw = torch.randn(T, k, generator=torch.Generator().manual_seed(1)).cuda()
+        got = [moe.route_scored_grad(m(l), ids, w, dw, SCORE[sigmoid], False) for m in (moved, torch.Tensor.cuda)]
+        ref, mag = B.route_scored_grad(f64(l), want, f64(w), f64(dw), sigmoid, renorm=False)
+        assert all((np.abs(f64(g) - ref) <= G * mag).all() for g in got)
 
 
 @pytest.mark.parametrize("sigmoid", [True, False])
