@@ -384,8 +384,9 @@ typedef struct moe_scoring {
  * logits, whose order the scores have.
  * An expert whose logit is -inf is masked: its score is 0 and it comes behind every expert with a finite c
  * or c = +inf, whatever its bias; where fewer than k others are left (a row may be masked whole) the lowest
- * masked ids fill up, with weight 0.  The lowest finite float is a number like others.  A NaN logit or bias, or
- * softmax over a +inf logit, leaves weights unspecified; the ids of a row are k different experts whatever it holds.
+ * masked ids fill up, with weight 0.  The lowest finite float is a number like others.  A NaN logit or bias,
+ * or softmax over a +inf logit, leaves weights unspecified; the ids of a row are k different experts whatever
+ * it holds.
  *   logits [T][E] fp32, bias [E] fp32 or NULL.  Outputs [T][k].
  *   1 <= k <= 8, E <= 512, groups <= 64 and a divisor of E, T < 2^25, else MOE_ERR_UNSUPPORTED. */
 int moe_route_scored(const float* logits, const float* bias, int T, int E, int k, const moe_scoring* scoring,
@@ -452,16 +453,16 @@ typedef struct moe_w4 {
 } moe_w4;
 
 /* Layout of 4-bit weights for moe_gemm_w4 (load time): src row-major -> codes, scales and zeros (NULL without
- * src->zeros) of the same sizes, overlapping neither src nor each other.  The layout is the library's: per 16 rows, codes in
- * 1 KB units of 128 columns, scales and zeros [K / group][16].  All pointers 16-byte aligned. */
+ * src->zeros) of the same sizes, overlapping neither src nor each other.  The layout is the library's, by
+ * units of 16 rows and 128 columns.  All pointers 16-byte aligned. */
 int moe_w4_tile(const moe_w4* src, void* codes, void* scales, uint8_t* zeros, hipStream_t stream);
 
 /* Product of bf16 rows with 4-bit weights: y[m][n] = bf16(sum_k x[m][k] * W[n][k]); with `up` (of w's N, K,
  * group and scale_dtype) the SwiGLU of the pair, bf16(SiLU(x Wt) * (x Upt)): a shared expert's gate and up
  * step, whose y moe_gemm_w4 takes back to d for moe_combine's shared_y.  Codes less zero points are exact in
  * the products, sums and scales are fp32, one rounding.
- *   x [M][K], y [M][N] bf16, not overlapping.  M * K < 2^31, N * K < 2^32, M * N < 2^37, else MOE_ERR_UNSUPPORTED; pointers
- *   16-byte aligned.  M = 0 is a no-op. */
+ *   x [M][K], y [M][N] bf16, not overlapping.  M * K < 2^31, N * K < 2^32, M * N < 2^37, else
+ *   MOE_ERR_UNSUPPORTED; pointers 16-byte aligned.  M = 0 is a no-op. */
 int moe_gemm_w4(const void* x, int M, const moe_w4* w, const moe_w4* up, void* y, hipStream_t stream);
 
 /* Static name of a status code. */

@@ -806,6 +806,7 @@ int moe_gemm_w4(const void* x, int M, const moe_w4* w, const moe_w4* up, void* y
   if ((int64_t)M * w->N >= (int64_t(1) << 37)) return MOE_ERR_UNSUPPORTED;  // (a launch's threads)
   if (M == 0) return MOE_OK;
   if (!x || !y || !aligned16(x) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if (overlap(x, (int64_t)M * w->K * 2, y, (int64_t)M * w->N * 2)) return MOE_ERR_INVALID_ARG;
   const int cus = device_cus();
   if (cus == 0) return MOE_ERR_HIP;
   W4Args a;

@@ -85,7 +85,7 @@ __device__ __forceinline__ float scale_f32(uint32_t bits, bool fp16) {
 // lies in LDS (few short rows): a wavefront then keeps nothing but weights in flight.
 // ------------------------------------------------------------------------------------------------
 constexpr int kXlBytes = 64 << 10;
-constexpr int xl_stride(int K) { return K * 2 + 64; }  // (rows start in different banks)
+constexpr int64_t xl_stride(int K) { return (int64_t)K * 2 + 64; }  // (rows start in different banks)
 
 template <int MQ, int NR, int GROUP, bool PAIR, bool ZERO, int W, bool XL, bool FP16>
 __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
@@ -107,7 +107,7 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
 #pragma unroll
   for (int q = 0; q < MQ; ++q) {  // (a row past the last re-reads it; never stored)
     const int r = min(q * 16 + r16, rows - 1);
-    xoff[q] = XL ? (uint32_t)(r * xl_stride(K) + kg * 16) : ((uint32_t)(m0 + r) * (uint32_t)K + kg * 8) * 2;
+    xoff[q] = XL ? (uint32_t)(r * (int)xl_stride(K) + kg * 16) : ((uint32_t)(m0 + r) * (uint32_t)K + kg * 8) * 2;
   }
   f32x4 tot[NR][MQ];
 #pragma unroll
@@ -199,7 +199,7 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
     // the first pieces of x, then both batches of weights behind them; the barrier waits for LDS alone
     constexpr int A = 2;
     const int per = K / 8, n = rows * per;  // 16-byte pieces of a row, of x
-    auto place = [&](int i) { return reinterpret_cast<uint4*>(xl + (i / per) * xl_stride(K) + (i % per) * 16); };
+    auto place = [&](int i) { return reinterpret_cast<uint4*>(xl + (i / per) * (int)xl_stride(K) + (i % per) * 16); };
     uint4 v[A];
 #pragma unroll
     for (int q = 0; q < A; ++q) v[q] = gload16(a.x, (uint32_t)min((int)threadIdx.x + q * 64 * W, n - 1) * 16);
@@ -376,7 +376,8 @@ __global__ __launch_bounds__(256, 2) void gemm_tile_w4(W4Args a) {
         const int zi = (j % C) * S + g;  // (row by row, its groups)
         const uint32_t z = ZERO ? zb[zi / 4][PAIR ? j >> 1 : 0] >> (8 * (zi % 4)) : 0u;
 #pragma unroll
-        for (int f = 0; f < F; ++f) wf[j][f] = decode8<ZERO>(c[g * F + f], ZERO ? zero_bytes(a.m[PAIR ? j >> 1 : 0].zero(z)) : 0u);
+        for (int f = 0; f < F; ++f)
+          wf[j][f] = decode8<ZERO>(c[g * F + f], ZERO ? zero_bytes(a.m[PAIR ? j >> 1 : 0].zero(z)) : 0u);
       }
       // (behind the last use of this chunk's; the loop's head waits for them)
       if (g == S - 1) load_scales(next);
@@ -462,7 +463,7 @@ hipError_t launch_stream(W4Args a, hipStream_t s) {
   constexpr int PC = PAIR ? 2 : 1, per = NR / PC;
   a.mtiles = (a.M + 16 * MQ - 1) / (16 * MQ);
   const unsigned grid = (unsigned)a.mtiles * ((a.N / 16 + per - 1) / per);
-  const int lds = MQ * NR * (W - 1) * 1024 + (XL ? a.M * xl_stride(a.K) : 0);
+  const int lds = MQ * NR * (W - 1) * 1024 + (XL ? a.M * (int)xl_stride(a.K) : 0);
   gemm_stream_w4<MQ, NR, GROUP, PAIR, ZERO, W, XL><<<grid, 64 * W, lds, s>>>(a);
   return hipGetLastError();
 }
@@ -496,7 +497,8 @@ hipError_t launch_tiles(W4Args a, int num_cus, hipStream_t s) {
 template <int GROUP>
 hipError_t launch_group(const W4Args& a, int cus, hipStream_t s) {
   const bool zero = a.m[0].zeros;  // (of either matrix, kernels.h)
-  if (a.m[1].codes) return zero ? launch_tiles<GROUP, true, true>(a, cus, s) : launch_tiles<GROUP, true, false>(a, cus, s);
+  if (a.m[1].codes)
+    return zero ? launch_tiles<GROUP, true, true>(a, cus, s) : launch_tiles<GROUP, true, false>(a, cus, s);
   return zero ? launch_tiles<GROUP, false, true>(a, cus, s) : launch_tiles<GROUP, false, false>(a, cus, s);
 }
 

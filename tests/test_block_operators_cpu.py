@@ -117,6 +117,8 @@ def test_gemm_w4_refusals(L):
         assert call(**{name: None}) == INV
     for name in ("x", "y", "codes", "scales", "zeros"):
         assert call(**{name: A + 8}) == INV
+    # y [2][16] ends in x [2][128], or begins in it
+    assert call(x=A, y=A) == INV and call(x=A, y=A - 48) == INV and call(x=A, y=A + 496) == INV
     for bad in (dict(N=32), dict(K=256), dict(group=64), dict(fmt=moe.SCALE_FP16), dict(codes=None),
                 dict(layout=moe.LAYOUT_ROW_MAJOR)):
         assert call(M=0, up=w4(**bad)) == INV
@@ -181,3 +183,68 @@ def test_binding_refusals():
     refused("GPU", moe.gemm_w4, torch.zeros(2, 128, dtype=bf), t)
     refused("x must have shape", moe.gemm_w4, x, t)
     assert t.struct().layout == moe.LAYOUT_TILED and ctypes.sizeof(t.struct()) == 48
+
+
+def test_binding_runs_on_the_tensors_gpu(monkeypatch):
+    """Tensors of a GPU that is not the current one: every call is made with that GPU current and on its stream,
+    and tensors of two GPUs are refused."""
+    import contextlib
+    current, calls = [0], []
+
+    @contextlib.contextmanager
+    def device(i):
+        was, current[0] = current[0], i
+        yield
+        current[0] = was
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: calls.append((name, current[0], args[-1])) or 0
+
+    class Gpu:
+        """A tensor by its shape and type."""
+        is_cuda = True
+
+        def __init__(self, shape, dtype, at=1):
+            self.shape, self.dtype, self.at, self.device = torch.Size(shape), dtype, at, torch.device("cuda", at)
+
+        def get_device(self):
+            return self.at
+
+        def dim(self):
+            return len(self.shape)
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return A
+
+        def new_empty(self, shape, dtype=None):
+            return Gpu((shape,) if isinstance(shape, int) else shape, dtype or self.dtype, self.at)
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    monkeypatch.setattr(moe, "_stream", lambda: 100 + current[0])
+    monkeypatch.setattr(moe, "lib", Lib)
+    monkeypatch.setattr(torch, "empty_like", lambda t, dtype=None: Gpu(t.shape, dtype or t.dtype, t.at))
+    bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    x, w, l = Gpu((4, 256), bf), Gpu((256,), bf), Gpu((4, 16), f32)
+    ids, dw = Gpu((4, 2), torch.int32), Gpu((4, 2), f32)
+    moe.route_scored(l, 2, Gpu((16,), f32))
+    moe.route_scored_grad(l, ids, dw, dw)
+    moe.block_norm(x, x, w, w, x)
+    moe.block_norm_grad(x, x, x, w, x, w, w)
+    t = moe.w4_tile(Gpu((16, 128), u8), Gpu((16, 2), bf), Gpu((16, 2), u8))
+    moe.gemm_w4(x, t, t)
+    names = ["moe_route_scored", "moe_route_scored_grad", "moe_block_norm", "moe_block_norm_grad", "moe_w4_tile",
+             "moe_gemm_w4"]
+    assert [c for c in calls if not c[0].endswith("bytes")] == [(n, 1, 101) for n in names] and current == [0]
+    other = Gpu((4, 256), bf, 0)
+    for f in (lambda: moe.block_norm(x, other, w), lambda: moe.block_norm_grad(x, x, other, w),
+              lambda: moe.gemm_w4(other, t), lambda: moe.route_scored(l, 2, Gpu((16,), f32, 0)),
+              lambda: moe.route_scored_grad(l, Gpu((4, 2), torch.int32, 0), dw, dw),
+              lambda: moe.w4_tile(Gpu((16, 128), u8), Gpu((16, 2), bf, 0))):
+        with pytest.raises(moe.MoEError, match="GPU"):
+            f()

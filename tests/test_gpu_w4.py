@@ -180,6 +180,88 @@ def test_gemm_w4_past_32_bit_offsets(moe):
         assert ((y.float() - want).abs() <= want.abs() * 2 * BF + 1).all()
 
 
+# Of a matrix of few columns so many weight rows (or rows of x) that the MFMA tiles take it: more than 24 tiles of
+# 16 weight rows by 32 rows of x per CU, of 256 CUs.
+TILES = [(999, 3216, 256), (1000, 4096, 128), (97, 24592, 128), (33, 49168, 128), (1025, 2992, 1152), (6145 * 32, 16, 128)]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("pair", [False, True])
+def test_gemm_w4_many_tiles(moe, M, N, K, group, zeros, pair):
+    assert (M + 31) // 32 * (N // 16) > 24 * 256
+    test_gemm_w4(moe, M, N, K, group, zeros, pair)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_gemm_w4_many_tiles_of_a_pair(moe, zeros, dtype):
+    """So few weight rows that only both matrices together are many tiles, the last of 80 rows; matrices with and
+    without zero points."""
+    M, N, K, group = 999, 1616, 256, 64
+    x, w, up = _bf16(M, K, seed=1), _w(N, K, group, zeros, 1, dtype), _w(N, K, group, True, 2, dtype)
+    check(x, moe.gemm_w4(x, moe.w4_tile(*w), moe.w4_tile(*up)), w, up, group)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_gemm_w4_many_tiles_every_code(moe, group, zeros):
+    """x a unit matrix: the product is the exact weights, rounded once."""
+    N, K = 24592, 128
+    codes, s, _ = _w(N, K, group, False, 3)
+    codes[:, :64] = torch.arange(N * 64, device="cuda").reshape(N, 64).to(torch.uint8)
+    z = torch.randint(0, 128, (N, K // group), generator=torch.Generator().manual_seed(1), dtype=torch.uint8)
+    w = (codes, s, z.cuda() if zeros else None)
+    want = torch.from_numpy(values(w, group)).to(torch.bfloat16).cuda()
+    y = moe.gemm_w4(torch.eye(K, dtype=torch.bfloat16, device="cuda"), moe.w4_tile(*w))
+    assert torch.equal(y, want.t())
+
+
+def test_gemm_w4_many_tiles_neighbours_and_non_finite_values(moe):
+    M, N, K = 999, 3216, 256
+    w = moe.w4_tile(*_w(N, K, 32, True, 1))
+    x = _bf16(M + 3, K, seed=3)
+    x[M:] = float("nan")
+    y = torch.full((M + 3, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    assert moe.lib().moe_gemm_w4(x.data_ptr(), M, w.struct(), None, y.data_ptr(), st) == 0
+    x = x[:M].contiguous()
+    clean = moe.gemm_w4(x, w)
+    assert torch.equal(y[:M], clean) and (y[M:] == 7).all()
+    x[500, 7], x[M - 1, 200] = float("nan"), float("inf")
+    y = moe.gemm_w4(x, w)
+    rest = [i for i in range(M) if i not in (500, M - 1)]
+    assert not y[[500, M - 1]].isfinite().any() and torch.equal(y[rest], clean[rest])
+    codes, s, z = _w(N, K, 128, True, 5)
+    w = (codes, (s.float() * 1e-30).to(torch.bfloat16), z)
+    x = (_bf16(M, K, seed=1).float() * 1e34).to(torch.bfloat16)
+    check(x, moe.gemm_w4(x, moe.w4_tile(*w)), w, None, 128)
+
+
+@pytest.mark.parametrize("M,K", [(16, 1920), (16, 2048), (4, 7936), (4, 8192), (1, 32640), (1, 32768)])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("pair", [False, True])
+def test_gemm_w4_as_long_as_lds_holds(moe, M, K, zeros, pair):
+    """Few rows that just fit on chip beside the weights, and that just do not."""
+    test_gemm_w4(moe, M, 48, K, 128, zeros, pair)
+
+
+def test_gemm_w4_of_the_longest_rows(moe):
+    """16 rows of 2^26 columns, 2^31 bytes: one value of each picks out a column of exact weights."""
+    N, K, M = 16, 2 ** 26, 16
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda")
+    s = (torch.rand(N, K // 128, device="cuda") * 0.02 + 0.001).to(torch.bfloat16)
+    at = torch.randint(0, K, (M,), generator=torch.Generator().manual_seed(1)).cuda()
+    at[0], at[1] = 0, K - 1
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[torch.arange(M), at] = 1
+    y = moe.gemm_w4(x, moe.w4_tile(codes, s))
+    c = codes[:, at // 2].int()
+    want = (torch.where(at % 2 == 1, c >> 4, c & 15) - 8).double() * s[:, at // 128].double()
+    assert torch.equal(y, want.t().to(torch.bfloat16))
+
+
 # ------------------------------------------------------------------------------------------------
 # a block's surroundings, run together
 # ------------------------------------------------------------------------------------------------
