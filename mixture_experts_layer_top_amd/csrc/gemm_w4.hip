@@ -91,7 +91,8 @@ template <int MQ, int NR, int GROUP, bool PAIR, bool ZERO, int W, bool XL, bool 
 __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
   constexpr int S = 128 / GROUP, F = GROUP / 32;  // groups per unit, MFMAs per group
   constexpr int U = MQ == 1 ? 2 : 1;              // units per batch (by registers)
-  constexpr int PC = PAIR ? 2 : 1;                // accumulators per output
+  constexpr bool HALF = PAIR && NR == 1;          // 8 rows of either matrix in one fragment, rows 8.. the second's
+  constexpr int PC = PAIR && !HALF ? 2 : 1;       // accumulators per output
   constexpr int P = MQ * NR / PC;                 // outputs (16 x 16) per wavefront
   float* const red = reinterpret_cast<float*>(lds);  // [P][W - 1][PC * 4][64]
   uint8_t* const xl = lds + P * (W - 1) * PC * 1024;
@@ -99,7 +100,9 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
   const int r16 = lane & 15, kg = lane >> 4;
   const int K = a.K, nkb = K / 128, nblk = a.N / 16;
   const int m0 = (blockIdx.x % a.mtiles) * (16 * MQ), rows = min(16 * MQ, a.M - m0);
-  const int b0 = (blockIdx.x / a.mtiles) * (NR / PC);  // first 16-row block
+  const int n0 = (blockIdx.x / a.mtiles) * (HALF ? 8 : 16 * NR / PC);  // first weight row
+  const int b0 = n0 / 16;                                             // and its 16-row block
+  const int hn = HALF ? n0 % 16 + (r16 & 7) : r16, hs = HALF ? n0 % 16 / 4 + (kg & 1) : kg;
   uint32_t unit0[NR], xoff[MQ];
 #pragma unroll
   for (int j = 0; j < NR; ++j)  // (a block past N re-reads the last one; never stored)
@@ -125,19 +128,21 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
       const uint32_t kb = (uint32_t)min(kw + W * (i + u), nkb - 1);
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
-        const W4Mat& m = a.m[PAIR ? j & 1 : 0];
+        // (of a fragment of both matrices lane by lane; a scale is its result's row's, the rest its operand's)
+        const int mc = HALF ? r16 >> 3 : PAIR ? j & 1 : 0, ms = HALF ? kg >> 1 : mc;
         const size_t unit = unit0[j] + kb;
-        const char* codes = static_cast<const char*>(m.codes) + unit * 1024;
-        bt.w[u][j] = a.mtiles == 1 ? gload16_nt(codes, lane * 16) : gload16(codes, lane * 16);
-        const char* sc = static_cast<const char*>(m.scales) + unit * (32 * S);
+        const char* codes = static_cast<const char*>(a.m[mc].codes) + unit * 1024;
+        const uint32_t at = kg * 256 + hn * 16;
+        bt.w[u][j] = a.mtiles == 1 ? gload16_nt(codes, at) : gload16(codes, at);
+        const char* sc = static_cast<const char*>(a.m[ms].scales) + unit * (32 * S);
         if (S == 1) {
-          const uint2 v = gload8(sc, kg * 8);
+          const uint2 v = gload8(sc, hs * 8);
           bt.s[u][j][0] = v.x;
           bt.s[u][j][1] = v.y;
         } else {
 #pragma unroll
           for (int g = 0; g < S / 2; ++g) {
-            const uint4 v = gload16(sc, kg * (8 * S) + g * 16);
+            const uint4 v = gload16(sc, hs * (8 * S) + g * 16);
             bt.s[u][j][4 * g] = v.x;
             bt.s[u][j][4 * g + 1] = v.y;
             bt.s[u][j][4 * g + 2] = v.z;
@@ -145,8 +150,8 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
           }
         }
         if (ZERO) {
-          const uint8_t* z = m.zeros + unit * (16 * S);
-          bt.z[ZERO ? u : 0][j] = S == 1 ? gload_u8(z, r16) : S == 2 ? gload_u16(z, r16 * 2) : gload4(z, r16 * 4);
+          const uint8_t* z = a.m[mc].zeros + unit * (16 * S);
+          bt.z[ZERO ? u : 0][j] = S == 1 ? gload_u8(z, hn) : S == 2 ? gload_u16(z, hn * 2) : gload4(z, hn * 4);
         }
       }
       if (!XL) {
@@ -167,7 +172,7 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
         const uint32_t c[4] = {bt.w[u][j].x, bt.w[u][j].y, bt.w[u][j].z, bt.w[u][j].w};
 #pragma unroll
         for (int g = 0; g < S; ++g) {
-          const uint32_t z = ZERO ? zero_bytes(a.m[PAIR ? j & 1 : 0].zero(bt.z[ZERO ? u : 0][j] >> (8 * g))) : 0u;
+          const uint32_t z = ZERO ? zero_bytes(a.m[HALF ? r16 >> 3 : PAIR ? j & 1 : 0].zero(bt.z[ZERO ? u : 0][j] >> (8 * g))) : 0u;
           float sc[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -249,12 +254,12 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
       }
     // lane holds weight rows 4 kg + r of row r16 of x
     const int r = p % MQ * 16 + r16, b = b0 + p / MQ;
-    if (r >= rows || b >= nblk) continue;
     if (PAIR) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[0][e] = swiglu(v[0][e], v[PC - 1][e]);
+      for (int e = 0; e < 4; ++e) v[0][e] = swiglu(v[0][e], HALF ? __shfl_xor(v[0][e], 32) : v[PC - 1][e]);
     }
-    gstore8(a.y, ((size_t)(m0 + r) * a.N + b * 16 + 4 * kg) * 2,
+    if (r >= rows || b >= nblk || (HALF && kg >= 2)) continue;
+    gstore8(a.y, ((size_t)(m0 + r) * a.N + b * 16 + 4 * hs) * 2,
             uint2{pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3])});
   }
 }
@@ -460,9 +465,9 @@ __global__ __launch_bounds__(64 * W) void gemm_stream_w4(W4Args a) {
 
 template <int MQ, int NR, int GROUP, bool PAIR, bool ZERO, int W, bool XL>
 hipError_t launch_stream(W4Args a, hipStream_t s) {
-  constexpr int PC = PAIR ? 2 : 1, per = NR / PC;
+  constexpr int rows = PAIR ? 8 * NR : 16 * NR;  // (of a matrix)
   a.mtiles = (a.M + 16 * MQ - 1) / (16 * MQ);
-  const unsigned grid = (unsigned)a.mtiles * ((a.N / 16 + per - 1) / per);
+  const unsigned grid = (unsigned)a.mtiles * ((a.N + rows - 1) / rows);
   const int lds = MQ * NR * (W - 1) * 1024 + (XL ? a.M * (int)xl_stride(a.K) : 0);
   gemm_stream_w4<MQ, NR, GROUP, PAIR, ZERO, W, XL><<<grid, 64 * W, lds, s>>>(a);
   return hipGetLastError();
@@ -483,9 +488,18 @@ hipError_t launch_tiles(W4Args a, int num_cus, hipStream_t s) {
     return hipGetLastError();
   }
   if (a.M <= 16) {
-    // x in LDS where it fits (1 x 7168 x 7168 11.2 us, 12.3 with x from L2; 16 rows of 7168 do not)
-    if (a.M * xl_stride(a.K) <= kXlBytes) return launch_stream<1, PAIR ? 2 : 1, GROUP, PAIR, ZERO, 8, true>(a, s);
-    return launch_stream<1, 2, GROUP, PAIR, ZERO, 8, false>(a, s);
+    // x in LDS where it fits (1 x 7168 x 7168 11.2 us, 12.3 with x from L2; 16 rows of 7168 do not).  16 weight rows
+    // a workgroup (of a pair 8 of either matrix) where that is no more than one per CU: pair 1 x 2048 x 7168 10.4 us,
+    // 12.7 with 32, 1 x 3200 x 7168 13.8 and 13.1; 16 x 2048 x 7168 10.8 and 12.8, 16 x 7168 x 7168 19.6 and 14.1.
+    const bool narrow = a.N / 16 * 2 <= num_cus;
+    if (a.M * xl_stride(a.K) <= kXlBytes) {
+      if constexpr (PAIR) {
+        if (!narrow) return launch_stream<1, 2, GROUP, PAIR, ZERO, 8, true>(a, s);
+      }
+      return launch_stream<1, 1, GROUP, PAIR, ZERO, 8, true>(a, s);
+    }
+    return narrow ? launch_stream<1, 1, GROUP, PAIR, ZERO, 8, false>(a, s)
+                  : launch_stream<1, 2, GROUP, PAIR, ZERO, 8, false>(a, s);
   }
   // 64 weight rows a workgroup halve what is read of x, where there are workgroups for half the CUs (64 x 7168 x
   // 7168 23 us, 33 with 32; 64 x 2048 x 2048 8.9 and 7.4).  Groups of 128 only: the registers hold no more scales.

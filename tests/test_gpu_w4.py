@@ -81,6 +81,9 @@ def test_gemm_w4_one_matrix_with_zeros(moe):
     a, b = _w(96, 512, 64, True, 1), _w(96, 512, 64, False, 2)
     check(x, moe.gemm_w4(x, moe.w4_tile(*a), moe.w4_tile(*b)), a, b, 64)
     check(x, moe.gemm_w4(x, moe.w4_tile(*b), moe.w4_tile(*a)), b, a, 64)
+    x = x[:3].contiguous()
+    check(x, moe.gemm_w4(x, moe.w4_tile(*a), moe.w4_tile(*b)), a, b, 64)
+    check(x, moe.gemm_w4(x, moe.w4_tile(*b), moe.w4_tile(*a)), b, a, 64)
 
 
 @pytest.mark.parametrize("M", [1, 40, 300])
@@ -237,6 +240,15 @@ def test_gemm_w4_many_tiles_neighbours_and_non_finite_values(moe):
     w = (codes, (s.float() * 1e-30).to(torch.bfloat16), z)
     x = (_bf16(M, K, seed=1).float() * 1e34).to(torch.bfloat16)
     check(x, moe.gemm_w4(x, moe.w4_tile(*w)), w, None, 128)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 2064, 512), (1, 2032, 512), (7, 2064, 1152), (16, 2064, 4096), (16, 2048, 4096)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("pair", [False, True])
+def test_gemm_w4_few_rows_by_more_or_fewer_weight_rows_than_cus_take(moe, M, N, K, group, zeros, pair):
+    """Either side of 16 weight rows per CU (of a pair in sum), with x on chip and not."""
+    test_gemm_w4(moe, M, N, K, group, zeros, pair)
 
 
 @pytest.mark.parametrize("M,K", [(16, 1920), (16, 2048), (4, 7936), (4, 8192), (1, 32640), (1, 32768)])
