@@ -82,7 +82,11 @@ __device__ __forceinline__ float scale_f32(uint32_t bits, bool fp16) {
 // wavefronts split K (interleaved units; the sums meet in LDS in a fixed order)
 //
 // Weights go straight from HBM into registers, 1 KB per load, are decoded there and multiplied.  XL: all of x
-// lies in LDS (few short rows): a wavefront then keeps nothing but weights in flight.
+// lies in LDS (few short rows): a wavefront then keeps nothing but weights in flight.  Bound by the latency of two or
+// three loads in a row per wavefront and a launch, then by HBM: group 128, 1 x 7168 x 7168 10.7 us (2.6 TB/s),
+// 1 x 14336 x 4096 10.8 (2.8); 64 x 7168 x 7168 22 us; more rows by L2, which gives x anew to every 64 weight rows.
+// (16 wavefronts along K, or four units a batch instead of two: 12.9 and 10.3 us for 1 x 7168 x 7168, but group 32,
+// 1 x 14336 x 4096 16.4 and 18.5 instead of 13.5.)
 // ------------------------------------------------------------------------------------------------
 constexpr int kXlBytes = 64 << 10;
 constexpr int64_t xl_stride(int K) { return (int64_t)K * 2 + 64; }  // (rows start in different banks)
@@ -271,7 +275,10 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
 // from registers, once for 128 rows, and only x goes through LDS as operands (global_load_lds, two stages of
 // 128 columns).  A group's sums are four chained MFMAs from zero (one per 32 columns); the scale takes them to
 // the totals while the next ones run.  Here x is the MFMA's first operand: a lane then holds one weight row per
-// fragment, and one scale.
+// fragment, and one scale.  Bound by the SIMDs' issue: 4096 x 14336 x 4096, group 128, 395 to 433 us by the clock
+// (1.1 to 1.2 PFLOP/s; the library's bf16 product of this size 406), MFMAs in 0.53 of the cycles and decoding and
+// scaling in 0.53; group 32, whose scales are four times as many, 552.  Wave priorities and a stagger of the
+// wavefronts gave nothing.
 // ------------------------------------------------------------------------------------------------
 constexpr int kTileM = 128;
 constexpr int kXStage = kTileM * 256;  // bytes: rows of 16 pieces of 16 bytes, swizzled by the row

@@ -16,10 +16,11 @@
 // since which expert is selected is a result: among the token's candidates, or by a wavefront over the whole row
 // (route_exact).
 //
-// Bound by its instructions, not by HBM: 8192 tokens of 256 experts in 8 groups take 10 us, without groups and
-// bias 5.4 (moe_route's wavefront per token 9.7), where their 8.9 MB take 2 us; one token 5 us. The gradient
-// writes all of dlogits and reads no more than k values per token, but for a softmax over all experts: 8192 x 256
-// 4.5 us and 5.9.
+// Bound by one token's chain of some thousand dependent instructions, which two wavefronts per SIMD (8192 tokens)
+// do not hide, not by HBM: 8192 tokens of 256 experts in 8 groups take 9.5 us, without groups and bias 5.4
+// (moe_route's wavefront per token 9.7), where their 8.9 MB take 2 us; 32768 of 384 19 us (2.8 TB/s), one token 4.9.
+// The gradient writes all of dlogits and reads no more than k values per token, but for a softmax over all
+// experts: 8192 x 256 4.5 us and 5.9.
 #include "kernels.h"
 #include "rows_dev.h"
 
