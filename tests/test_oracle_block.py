@@ -79,3 +79,12 @@ def test_w4_values_by_hand():
     assert B.gemm_w4([[3.0, 1.0]], w)[0].tolist() == [[1.0]]
     y, _ = B.gemm_w4([[3.0, 1.0]], w, 2 * w)
     assert np.allclose(y, 1 / (1 + np.exp(-1.0)) * 2)
+
+
+def test_block_norm_by_hand():
+    # mean squares of 1 and 4: x / 1 * post, then the gate, both scales and the residual; h / 2 * pre
+    x, r = [[1.0, -1.0]], [[6.0, 4.0]]
+    h, mag, y = B.block_norm(x, r, [2.0, 4.0], [0.5, -1.0], [3.0, 10.0], 0.5, -1.0, 0.0)
+    assert h.tolist() == [[2.0, -2.0]] and mag.tolist() == [[4.0, 6.0]] and y(h).tolist() == [[3.0, -10.0]]
+    h, _, y = B.block_norm(x, r, None, None, [1.0, 1.0], 1.0, 1.0, 2.0)
+    assert h.tolist() == [[7.0, 3.0]] and np.allclose(y(h), h / np.sqrt(31.0))
