@@ -269,6 +269,199 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
 }
 
 // ------------------------------------------------------------------------------------------------
+// middling rows: 128 weight rows (PAIR: 64 of either matrix) by 64 rows of x per workgroup
+//
+// 8 wavefronts: two halves of K, each with its own units and its own ring of x in LDS, by four of 32 weight rows.  A
+// stage is two units of either half; loads run one stage ahead, x by global_load_lds, weights into registers as in
+// the streaming tiles.
+// ------------------------------------------------------------------------------------------------
+constexpr int kMidM = 64, kMidUnit = kMidM * 256;
+
+template <int GROUP, bool PAIR, bool ZERO, bool FP16>
+__device__ __forceinline__ void mid_w4(const W4Args& a, int nblocks, uint8_t* ring) {
+  constexpr int S = 128 / GROUP, F = GROUP / 32;
+  constexpr int NR = 2, WK = 2, WN = 4, U = 2, PC = PAIR ? 2 : 1, MQ = kMidM / 16;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wk = wv / WN, wn = wv % WN;
+  const int r16 = lane & 15, kg = lane >> 4;
+  const int K = a.K, nkb = K / 128, nblk = a.N / 16, steps = (nkb + 3) / 4;
+  // (a weight block's tiles run on one XCD, whose L2 then reads it once)
+  const int turn = blockIdx.x >> 3, nb = turn / a.mtiles * 8 + (blockIdx.x & 7);
+  if (nb >= nblocks) return;
+  const int m0 = turn % a.mtiles * kMidM, b0 = nb * (8 / PC) + wn * (NR / PC);
+  uint32_t unit0[NR];
+#pragma unroll
+  for (int j = 0; j < NR; ++j)  // (a block past N re-reads the last one; never stored)
+    unit0[j] = (uint32_t)min(b0 + j / PC, nblk - 1) * (uint32_t)nkb;
+  f32x4 tot[NR][MQ];
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int t = 0; t < MQ; ++t) tot[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Batch {
+    uint4 w[U][NR];
+    uint32_t s[U][NR][2 * S], z[ZERO ? U : 1][NR];
+  };
+  auto load_x = [&](int i, int stage) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int l = wn * 8 + q, u = l / 16;
+      const int kb = min(i * 4 + wk * U + u, nkb - 1);
+      const int row = 4 * (l % 16) + (tid_here() >> 4 & 3), piece = (tid_here() & 15) ^ (row & 15);
+      const uint32_t off = (uint32_t)min(m0 + row, a.M - 1) * (uint32_t)(K * 2) + piece * 16;
+      dma16(static_cast<const char*>(a.x) + (size_t)kb * 256, off,
+            (lds_void*)(ring + ((wk * 2 + stage) * U + u) * kMidUnit + l % 16 * 1024));
+    }
+  };
+  auto load = [&](Batch& bt, int i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t kb = (uint32_t)min(i * 4 + wk * U + u, nkb - 1);
+#pragma unroll
+      for (int j = 0; j < NR; ++j) {
+        const W4Mat& m = a.m[PAIR ? j & 1 : 0];
+        const size_t unit = unit0[j] + kb;
+        bt.w[u][j] = gload16(static_cast<const char*>(m.codes) + unit * 1024, lane * 16);
+        const char* sc = static_cast<const char*>(m.scales) + unit * (32 * S);
+        if (S == 1) {
+          const uint2 v = gload8(sc, kg * 8);
+          bt.s[u][j][0] = v.x;
+          bt.s[u][j][1] = v.y;
+        } else {
+#pragma unroll
+          for (int g = 0; g < S / 2; ++g) {
+            const uint4 v = gload16(sc, kg * (8 * S) + g * 16);
+            bt.s[u][j][4 * g] = v.x;
+            bt.s[u][j][4 * g + 1] = v.y;
+            bt.s[u][j][4 * g + 2] = v.z;
+            bt.s[u][j][4 * g + 3] = v.w;
+          }
+        }
+        if (ZERO) {
+          const uint8_t* z = m.zeros + unit * (16 * S);
+          bt.z[ZERO ? u : 0][j] = S == 1 ? gload_u8(z, r16) : S == 2 ? gload_u16(z, r16 * 2) : gload4(z, r16 * 4);
+        }
+      }
+    }
+  };
+  auto landed = [&](Batch& bt) {  // (a wait for registers behind the next stage's loads would wait for those too)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NR; ++j) {
+        uint4& w = bt.w[u][j];
+        asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
+#pragma unroll
+        for (int g = 0; g < 2 * S; ++g) asm volatile("" : "+v"(bt.s[u][j][g]));
+        if (ZERO) asm volatile("" : "+v"(bt.z[ZERO ? u : 0][j]));
+      }
+  };
+  auto compute = [&](const Batch& bt, int i, int stage) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i * 4 + wk * U + u >= nkb) break;
+      uint32_t xa = ((wk * 2 + stage) * U + u) * kMidUnit + r16 * 256 + (kg ^ (r16 & 3)) * 16 + (r16 >> 2) * 64;
+      asm volatile("" : "+v"(xa));
+#pragma unroll
+      for (int g = 0; g < S; ++g) {
+        f32x4 acc[NR][MQ];
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+          for (int t = 0; t < MQ; ++t) acc[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          bf16x8 xf[MQ];
+#pragma unroll
+          for (int t = 0; t < MQ; ++t)
+            xf[t] = as_bf16x8(*reinterpret_cast<const uint4*>(ring + ((xa ^ ((g * F + f) * 64)) + t * 4096)));
+#pragma unroll
+          for (int j = 0; j < NR; ++j) {
+            const uint32_t c[4] = {bt.w[u][j].x, bt.w[u][j].y, bt.w[u][j].z, bt.w[u][j].w};
+            const uint32_t z = ZERO ? zero_bytes(a.m[PAIR ? j & 1 : 0].zero(bt.z[ZERO ? u : 0][j] >> (8 * g))) : 0u;
+            const bf16x8 wf = decode8<ZERO>(c[g * F + f], z);
+#pragma unroll
+            for (int t = 0; t < MQ; ++t) acc[j][t] = mfma16(wf, xf[t], acc[j][t]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float sc = scale_f32(bt.s[u][j][2 * g + (r >> 1)] >> (16 * (r & 1)) & 0xFFFF, FP16) *
+                             (ZERO ? 1.0f : kSymScale);
+#pragma unroll
+            for (int t = 0; t < MQ; ++t) tot[j][t][r] = fmaf(sc, acc[j][t][r], tot[j][t][r]);
+          }
+      }
+    }
+  };
+  Batch c0, c1;
+  auto step = [&](Batch& now, Batch& next, int i, int stage) {
+    MOE_WAITCNT(0, 15);  // this stage has landed
+    landed(now);
+    __syncthreads();  // for every wavefront; and all have read the other one
+    load_x(min(i + 1, steps - 1), stage ^ 1);
+    load(next, min(i + 1, steps - 1));
+    compute(now, i, stage);
+  };
+  load_x(0, 0);
+  load(c0, 0);
+  for (int i = 0; i < steps; i += 2) {
+    step(c0, c1, i, 0);
+    if (i + 1 < steps) step(c1, c0, i + 1, 1);
+  }
+  MOE_WAITCNT(0, 15);
+  __syncthreads();
+  // every wavefront parks its sums but those of the tiles it finishes itself: tile t goes to wavefront t % WK
+  auto slot = [&](int t, int from, int j) {
+    const int at = (t * (WK - 1) + (from < t % WK ? from : from - 1)) * NR + j;
+    return reinterpret_cast<f32x4*>(ring) + (wn * (MQ * (WK - 1) * NR) + at) * 64 + lane;
+  };
+#pragma unroll
+  for (int t = 0; t < MQ; ++t)
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+      if (t % WK != wk) *slot(t, wk, j) = tot[j][t];
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < MQ; ++t) {
+    if (t % WK != wk) continue;
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int w = 0; w < WK; ++w)
+        if (w != t % WK) tot[j][t] += *slot(t, w, j);
+    // lane holds weight rows 4 kg + r of row r16 of x
+    const int r = m0 + t * 16 + r16;
+#pragma unroll
+    for (int j = 0; j < NR; j += PC) {
+      f32x4 v = tot[j][t];
+      if (PAIR) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = swiglu(v[e], tot[j + PC - 1][t][e]);
+      }
+      const int b = b0 + j / PC;
+      if (r < a.M && b < nblk)
+        gstore8(a.y, ((size_t)r * a.N + b * 16 + 4 * kg) * 2, uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+    }
+  }
+}
+template <int GROUP, bool PAIR, bool ZERO>
+__global__ __launch_bounds__(512) void gemm_mid_w4(W4Args a, int nblocks) {
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[8 * kMidUnit];
+  if (a.fp16) mid_w4<GROUP, PAIR, ZERO, true>(a, nblocks, ring);
+  else mid_w4<GROUP, PAIR, ZERO, false>(a, nblocks, ring);
+}
+template <int GROUP, bool PAIR, bool ZERO>
+hipError_t launch_mid(W4Args a, hipStream_t s) {
+  a.mtiles = (a.M + kMidM - 1) / kMidM;
+  const int nblocks = (a.N / 16 + (PAIR ? 3 : 7)) / (PAIR ? 4 : 8);
+  gemm_mid_w4<GROUP, PAIR, ZERO><<<(unsigned)a.mtiles * ((nblocks + 7) / 8 * 8), 512, 0, s>>>(a, nblocks);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------------------
 // many rows: 256 weight rows (PAIR: 128 of either matrix) by 128 rows of x per workgroup
 //
 // Each of the 4 wavefronts holds 64 weight rows and all 128 rows of x: a weight is decoded by one wavefront,
@@ -479,21 +672,24 @@ hipError_t launch_stream(W4Args a, hipStream_t s) {
   gemm_stream_w4<MQ, NR, GROUP, PAIR, ZERO, W, XL><<<grid, 64 * W, lds, s>>>(a);
   return hipGetLastError();
 }
-// The streaming tiles, unless there are so many (16 weight rows by 32 rows of x each, a unit of work per 128
-// columns) that the MFMA tiles, which need as long for one as for 128 rows, take less.  Microseconds, streaming and
-// MFMA tiles, at rows x weight rows x columns (tiles per CU): group 128, 256 x 7168 x 7168 (14) 79 and 122, 512
-// (28) 135 and 123, 1024 x 2048 x 2048 (16) 31 and 38, 2048 (32) 59 and 39; group 32 pair, 512 x 2048 x 7168
-// (16) 135 and 193, 1024 (32) 266 and 193.
-constexpr int kStreamTilesPerCu = 24;
+// More than 32 rows of x: the streaming tiles where the middling ones would not be enough workgroups, the latter for up
+// to two of them per CU, the MFMA tiles beyond.  Microseconds, streaming and middling tiles, at rows x weight rows x columns
+// (workgroups of the latter per CU): group 128, 128 x 7168 x 7168 (0.4) 41 and 45, 192 x 6144 x 4096 (0.6) 40 and
+// 27, 256 x 7168 x 7168 (0.9) 79 and 46; group 64, 256 x 3584 x 4096 (0.4) 41 and 29; group 32 pair, 256 x 2048 x
+// 7168 (0.5) 70 and 57.  MFMA and middling tiles: group 128, 512 x 7168 x 7168 (1.75) 123 and 89, 2048 x
+// 2048 x 2048 (2) 39 and 38, 2200 (2.2) 39 and 48; group 32 pair, 1024 x 2048 x 7168 (2) 213 and 122, 2048 (4) 213
+// and 243.  Up to 32 rows half of a middling tile or more would be idle: 24 x 28672 x 4096 (0.9) 27 and 31.
 template <int GROUP, bool PAIR, bool ZERO>
 hipError_t launch_tiles(W4Args a, int num_cus, hipStream_t s) {
   const int64_t blocks = a.N / 16 * (PAIR ? 2 : 1), mtiles = (a.M + 31) / 32;
-  if (a.M > 32 && mtiles * blocks > (int64_t)kStreamTilesPerCu * num_cus) {
+  const int64_t mid = (int64_t)((a.M + kMidM - 1) / kMidM) * ((blocks + 7) / 8);
+  if (a.M > 32 && mid > 2 * num_cus) {
     a.mtiles = (a.M + kTileM - 1) / kTileM;
     const int64_t grid = (int64_t)a.mtiles * ((a.N + (PAIR ? 127 : 255)) / (PAIR ? 128 : 256));
     gemm_tile_w4<GROUP, PAIR, ZERO><<<(unsigned)grid, 256, 0, s>>>(a);
     return hipGetLastError();
   }
+  if (a.M > 32 && mid > (GROUP == 128 ? num_cus / 2 : num_cus / 8 * 3)) return launch_mid<GROUP, PAIR, ZERO>(a, s);
   if (a.M <= 16) {
     // x in LDS where it fits (1 x 7168 x 7168 11.2 us, 12.3 with x from L2; 16 rows of 7168 do not).  16 weight rows
     // a workgroup (of a pair 8 of either matrix) where that is no more than one per CU: pair 1 x 2048 x 7168 10.4 us,

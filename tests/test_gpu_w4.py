@@ -183,9 +183,11 @@ def test_gemm_w4_past_32_bit_offsets(moe):
         assert ((y.float() - want).abs() <= want.abs() * 2 * BF + 1).all()
 
 
-# Of a matrix of few columns so many weight rows (or rows of x) that the MFMA tiles take it: more than 24 tiles of
-# 16 weight rows by 32 rows of x per CU, of 256 CUs.
-TILES = [(999, 3216, 256), (1000, 4096, 128), (97, 24592, 128), (33, 49168, 128), (1025, 2992, 1152), (6145 * 32, 16, 128)]
+# Of a matrix of few columns so many weight rows (or rows of x) that the middling or the MFMA tiles take it: by tiles of
+# 128 weight rows and 64 rows of x, more than half of 256 CUs, or two per CU.
+TILES = [(999, 3216, 256), (1000, 4096, 128), (97, 24592, 128), (33, 49168, 128), (1025, 2992, 1152), (6145 * 32, 16, 128),
+         (250, 4224, 128), (130, 5520, 256), (70, 8336, 384), (64, 16400, 640), (33, 17000 // 16 * 16, 1152), (2000, 528, 512),
+         (999, 8208, 256), (129, 22288, 128), (65, 33360, 384), (2100, 2080, 1280), (5000, 1040, 128)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
@@ -193,25 +195,26 @@ TILES = [(999, 3216, 256), (1000, 4096, 128), (97, 24592, 128), (33, 49168, 128)
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("pair", [False, True])
 def test_gemm_w4_many_tiles(moe, M, N, K, group, zeros, pair):
-    assert (M + 31) // 32 * (N // 16) > 24 * 256
+    assert (M + 63) // 64 * ((N + 127) // 128) > 128
     test_gemm_w4(moe, M, N, K, group, zeros, pair)
 
 
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_gemm_w4_many_tiles_of_a_pair(moe, zeros, dtype):
-    """So few weight rows that only both matrices together are many tiles, the last of 80 rows; matrices with and
-    without zero points."""
-    M, N, K, group = 999, 1616, 256, 64
-    x, w, up = _bf16(M, K, seed=1), _w(N, K, group, zeros, 1, dtype), _w(N, K, group, True, 2, dtype)
-    check(x, moe.gemm_w4(x, moe.w4_tile(*w), moe.w4_tile(*up)), w, up, group)
+    """So few weight rows that only both matrices together are many tiles, the last of 16 or 80 rows; matrices with
+    and without zero points."""
+    for M, N, K, group in ((999, 1616, 256, 64), (600, 1040, 384, 32), (2100, 1168, 128, 128)):
+        x, w, up = _bf16(M, K, seed=1), _w(N, K, group, zeros, 1, dtype), _w(N, K, group, True, 2, dtype)
+        check(x, moe.gemm_w4(x, moe.w4_tile(*w), moe.w4_tile(*up)), w, up, group)
 
 
+@pytest.mark.parametrize("N", [24592, 33360])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("zeros", [False, True])
-def test_gemm_w4_many_tiles_every_code(moe, group, zeros):
+def test_gemm_w4_many_tiles_every_code(moe, N, group, zeros):
     """x a unit matrix: the product is the exact weights, rounded once."""
-    N, K = 24592, 128
+    K = 128
     codes, s, _ = _w(N, K, group, False, 3)
     codes[:, :64] = torch.arange(N * 64, device="cuda").reshape(N, 64).to(torch.uint8)
     z = torch.randint(0, 128, (N, K // group), generator=torch.Generator().manual_seed(1), dtype=torch.uint8)
@@ -221,8 +224,9 @@ def test_gemm_w4_many_tiles_every_code(moe, group, zeros):
     assert torch.equal(y, want.t())
 
 
-def test_gemm_w4_many_tiles_neighbours_and_non_finite_values(moe):
-    M, N, K = 999, 3216, 256
+@pytest.mark.parametrize("N", [3216, 8208])
+def test_gemm_w4_many_tiles_neighbours_and_non_finite_values(moe, N):
+    M, K = 999, 256
     w = moe.w4_tile(*_w(N, K, 32, True, 1))
     x = _bf16(M + 3, K, seed=3)
     x[M:] = float("nan")
