@@ -84,7 +84,7 @@ __device__ __forceinline__ float scale_f32(uint32_t bits, bool fp16) {
 // Weights go straight from HBM into registers, 1 KB per load, are decoded there and multiplied.  XL: all of x
 // lies in LDS (few short rows): a wavefront then keeps nothing but weights in flight.  Bound by the latency of two or
 // three loads in a row per wavefront and a launch, then by HBM: group 128, 1 x 7168 x 7168 10.7 us (2.6 TB/s),
-// 1 x 14336 x 4096 10.8 (2.8); 64 x 7168 x 7168 22 us; more rows by L2, which gives x anew to every 64 weight rows.
+// 1 x 14336 x 4096 10.8 (2.8); 64 x 7168 x 7168 23 us, 128 41: by L2, which gives x anew to every 64 weight rows.
 // (16 wavefronts along K, or four units a batch instead of two: 12.9 and 10.3 us for 1 x 7168 x 7168, but group 32,
 // 1 x 14336 x 4096 16.4 and 18.5 instead of 13.5.)
 // ------------------------------------------------------------------------------------------------
@@ -273,7 +273,10 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
 //
 // 8 wavefronts: two halves of K, each with its own units and its own ring of x in LDS, by four of 32 weight rows.  A
 // stage is two units of either half; loads run one stage ahead, x by global_load_lds, weights into registers as in
-// the streaming tiles.
+// the streaming tiles.  256 x 7168 x 7168, group 128, 46 us (0.57 PFLOP/s): bound by issue, decoding for only 64 rows
+// of x at a time, and by L2, one after the other where they do not overlap (without the loads 37 us, without the
+// products 29, 10.6 TB/s).  Reading and decoding a piece ahead and interleaving it with the MFMAs gained 1 to 4%
+// and spilled registers with groups of 32; four parts of K with 64 weight rows each gained 3% and spilled alike.
 // ------------------------------------------------------------------------------------------------
 constexpr int kMidM = 64, kMidUnit = kMidM * 256;
 
