@@ -176,7 +176,8 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
         const uint32_t c[4] = {bt.w[u][j].x, bt.w[u][j].y, bt.w[u][j].z, bt.w[u][j].w};
 #pragma unroll
         for (int g = 0; g < S; ++g) {
-          const uint32_t z = ZERO ? zero_bytes(a.m[HALF ? r16 >> 3 : PAIR ? j & 1 : 0].zero(bt.z[ZERO ? u : 0][j] >> (8 * g))) : 0u;
+          const W4Mat& m = a.m[HALF ? r16 >> 3 : PAIR ? j & 1 : 0];
+          const uint32_t z = ZERO ? zero_bytes(m.zero(bt.z[ZERO ? u : 0][j] >> (8 * g))) : 0u;
           float sc[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -675,13 +676,13 @@ hipError_t launch_stream(W4Args a, hipStream_t s) {
   gemm_stream_w4<MQ, NR, GROUP, PAIR, ZERO, W, XL><<<grid, 64 * W, lds, s>>>(a);
   return hipGetLastError();
 }
-// More than 32 rows of x: the streaming tiles where the middling ones would not be enough workgroups, the latter for up
-// to two of them per CU, the MFMA tiles beyond.  Microseconds, streaming and middling tiles, at rows x weight rows x columns
-// (workgroups of the latter per CU): group 128, 128 x 7168 x 7168 (0.4) 41 and 45, 192 x 6144 x 4096 (0.6) 40 and
-// 27, 256 x 7168 x 7168 (0.9) 79 and 46; group 64, 256 x 3584 x 4096 (0.4) 41 and 29; group 32 pair, 256 x 2048 x
-// 7168 (0.5) 70 and 57.  MFMA and middling tiles: group 128, 512 x 7168 x 7168 (1.75) 123 and 89, 2048 x
-// 2048 x 2048 (2) 39 and 38, 2200 (2.2) 39 and 48; group 32 pair, 1024 x 2048 x 7168 (2) 213 and 122, 2048 (4) 213
-// and 243.  Up to 32 rows half of a middling tile or more would be idle: 24 x 28672 x 4096 (0.9) 27 and 31.
+// More than 32 rows of x: the streaming tiles where the middling ones would not be enough workgroups, the latter for
+// up to two of them per CU, the MFMA tiles beyond.  Microseconds, streaming and middling tiles, at rows x weight rows x
+// columns (workgroups of the latter per CU): group 128, 128 x 7168 x 7168 (0.4) 41 and 45, 192 x 6144 x 4096 (0.6)
+// 40 and 27, 256 x 7168 x 7168 (0.9) 79 and 46; group 64, 256 x 3584 x 4096 (0.4) 41 and 29; group 32 pair, 256 x
+// 2048 x 7168 (0.5) 70 and 57.  MFMA and middling tiles: group 128, 512 x 7168 x 7168 (1.75) 123 and 89, 2048 x 2048 x
+// 2048 (2) 39 and 38, 2200 (2.2) 39 and 48; group 32 pair, 1024 x 2048 x 7168 (2) 213 and 122, 2048 (4) 213 and 243.
+// Up to 32 rows half of a middling tile or more would be idle: 24 x 28672 x 4096 (0.9) 27 and 31.
 template <int GROUP, bool PAIR, bool ZERO>
 hipError_t launch_tiles(W4Args a, int num_cus, hipStream_t s) {
   const int64_t blocks = a.N / 16 * (PAIR ? 2 : 1), mtiles = (a.M + 31) / 32;

@@ -246,6 +246,33 @@ def test_gemm_w4_many_tiles_neighbours_and_non_finite_values(moe, N):
     check(x, moe.gemm_w4(x, moe.w4_tile(*w)), w, None, 128)
 
 
+@pytest.mark.parametrize("N", [3216, 8208])
+def test_gemm_w4_many_tiles_captured_and_on_two_streams(moe, N):
+    """A captured call replayed with new inputs, and two at once, give the eager call's bits."""
+    M, K = 999, 640
+    w, up = moe.w4_tile(*_w(N, K, 64, True, 1)), moe.w4_tile(*_w(N, K, 64, False, 2))
+    x, other = _bf16(M, K, seed=3), _bf16(M, K, seed=4)
+    want = {0: moe.gemm_w4(x, w, up), 1: moe.gemm_w4(other, w, up)}
+    a = x.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = moe.gemm_w4(a, w, up)
+    for i in (0, 1, 0, 1):
+        a.copy_(other if i else x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append((i, moe.gemm_w4(other if i else x, w, up)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(v, want[i]) for i, v in got)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 2064, 512), (1, 2032, 512), (7, 2064, 1152), (16, 2064, 4096), (16, 2048, 4096)])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("zeros", [False, True])
