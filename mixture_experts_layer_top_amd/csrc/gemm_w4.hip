@@ -270,29 +270,31 @@ __device__ __forceinline__ void stream_w4(const W4Args& a, uint8_t* lds) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// middling rows: 128 weight rows (PAIR: 64 of either matrix) by 64 rows of x per workgroup
+// middling rows: 128 weight rows (PAIR: 64 of either matrix) by 16 * MQ = 64 or 128 rows of x per workgroup
 //
 // 8 wavefronts: two halves of K, each with its own units and its own ring of x in LDS, by four of 32 weight rows.  A
-// stage is two units of either half; loads run one stage ahead, x by global_load_lds, weights into registers as in
-// the streaming tiles.  256 x 7168 x 7168, group 128, 46 us (0.57 PFLOP/s): bound by issue, decoding for only 64 rows
-// of x at a time, and by L2, one after the other where they do not overlap (without the loads 37 us, without the
-// products 29, 10.6 TB/s).  Reading and decoding a piece ahead and interleaving it with the MFMAs gained 1 to 4%
-// and spilled registers with groups of 32; four parts of K with 64 weight rows each gained 3% and spilled alike.
+// stage is two units of either half (128 rows of x: one); loads run one stage ahead, x by global_load_lds, weights
+// into registers as in the streaming tiles.  Group 128, 256 x 7168 x 7168 46 us, 512 71 us (0.57 and 0.74 PFLOP/s):
+// bound by issue, decoding for 64 or 128 rows of x at a time, and by L2, one after the other where they do not
+// overlap (256 rows without the loads 37 us, without the products 29, 10.6 TB/s).  Reading and decoding a piece ahead
+// and interleaving it with the MFMAs gained 1 to 4% and spilled registers with groups of 32; four parts of K with 64
+// weight rows each gained 3% and spilled alike.
 // ------------------------------------------------------------------------------------------------
-constexpr int kMidM = 64, kMidUnit = kMidM * 256;
+constexpr int kMidRing = 128 << 10;
 
-template <int GROUP, bool PAIR, bool ZERO, bool FP16>
+template <int GROUP, bool PAIR, bool ZERO, int MQ, bool FP16>
 __device__ __forceinline__ void mid_w4(const W4Args& a, int nblocks, uint8_t* ring) {
   constexpr int S = 128 / GROUP, F = GROUP / 32;
-  constexpr int NR = 2, WK = 2, WN = 4, U = 2, PC = PAIR ? 2 : 1, MQ = kMidM / 16;
+  constexpr int NR = 2, WK = 2, WN = 4, PC = PAIR ? 2 : 1, M = 16 * MQ;
+  constexpr int kUnit = M * 256, U = kMidRing / (2 * WK * kUnit);  // bytes of x, units of a stage and half
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = wv / WN, wn = wv % WN;
   const int r16 = lane & 15, kg = lane >> 4;
-  const int K = a.K, nkb = K / 128, nblk = a.N / 16, steps = (nkb + 3) / 4;
+  const int K = a.K, nkb = K / 128, nblk = a.N / 16, steps = (nkb + WK * U - 1) / (WK * U);
   // (a weight block's tiles run on one XCD, whose L2 then reads it once)
   const int turn = blockIdx.x >> 3, nb = turn / a.mtiles * 8 + (blockIdx.x & 7);
   if (nb >= nblocks) return;
-  const int m0 = turn % a.mtiles * kMidM, b0 = nb * (8 / PC) + wn * (NR / PC);
+  const int m0 = turn % a.mtiles * M, b0 = nb * (8 / PC) + wn * (NR / PC);
   uint32_t unit0[NR];
 #pragma unroll
   for (int j = 0; j < NR; ++j)  // (a block past N re-reads the last one; never stored)
@@ -309,18 +311,18 @@ __device__ __forceinline__ void mid_w4(const W4Args& a, int nblocks, uint8_t* ri
   auto load_x = [&](int i, int stage) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int l = wn * 8 + q, u = l / 16;
-      const int kb = min(i * 4 + wk * U + u, nkb - 1);
-      const int row = 4 * (l % 16) + (tid_here() >> 4 & 3), piece = (tid_here() & 15) ^ (row & 15);
+      const int l = wn * 8 + q, u = l / (M / 4), r4 = l % (M / 4);
+      const int kb = min((i * WK + wk) * U + u, nkb - 1);
+      const int row = 4 * r4 + (tid_here() >> 4 & 3), piece = (tid_here() & 15) ^ (row & 15);
       const uint32_t off = (uint32_t)min(m0 + row, a.M - 1) * (uint32_t)(K * 2) + piece * 16;
       dma16(static_cast<const char*>(a.x) + (size_t)kb * 256, off,
-            (lds_void*)(ring + ((wk * 2 + stage) * U + u) * kMidUnit + l % 16 * 1024));
+            (lds_void*)(ring + ((wk * 2 + stage) * U + u) * kUnit + r4 * 1024));
     }
   };
   auto load = [&](Batch& bt, int i) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t kb = (uint32_t)min(i * 4 + wk * U + u, nkb - 1);
+      const uint32_t kb = (uint32_t)min((i * WK + wk) * U + u, nkb - 1);
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
         const W4Mat& m = a.m[PAIR ? j & 1 : 0];
@@ -363,40 +365,49 @@ __device__ __forceinline__ void mid_w4(const W4Args& a, int nblocks, uint8_t* ri
   auto compute = [&](const Batch& bt, int i, int stage) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i * 4 + wk * U + u >= nkb) break;
-      uint32_t xa = ((wk * 2 + stage) * U + u) * kMidUnit + r16 * 256 + (kg ^ (r16 & 3)) * 16 + (r16 >> 2) * 64;
+      if ((i * WK + wk) * U + u >= nkb) break;
+      uint32_t xa = ((wk * 2 + stage) * U + u) * kUnit + r16 * 256 + (kg ^ (r16 & 3)) * 16 + (r16 >> 2) * 64;
       asm volatile("" : "+v"(xa));
 #pragma unroll
       for (int g = 0; g < S; ++g) {
-        f32x4 acc[NR][MQ];
+        bf16x8 wf[NR][F];
+        float sc[NR][4];
 #pragma unroll
-        for (int j = 0; j < NR; ++j)
+        for (int j = 0; j < NR; ++j) {
+          const uint32_t c[4] = {bt.w[u][j].x, bt.w[u][j].y, bt.w[u][j].z, bt.w[u][j].w};
+          const uint32_t z = ZERO ? zero_bytes(a.m[PAIR ? j & 1 : 0].zero(bt.z[ZERO ? u : 0][j] >> (8 * g))) : 0u;
 #pragma unroll
-          for (int t = 0; t < MQ; ++t) acc[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int f = 0; f < F; ++f) wf[j][f] = decode8<ZERO>(c[g * F + f], z);
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-          bf16x8 xf[MQ];
-#pragma unroll
-          for (int t = 0; t < MQ; ++t)
-            xf[t] = as_bf16x8(*reinterpret_cast<const uint4*>(ring + ((xa ^ ((g * F + f) * 64)) + t * 4096)));
-#pragma unroll
-          for (int j = 0; j < NR; ++j) {
-            const uint32_t c[4] = {bt.w[u][j].x, bt.w[u][j].y, bt.w[u][j].z, bt.w[u][j].w};
-            const uint32_t z = ZERO ? zero_bytes(a.m[PAIR ? j & 1 : 0].zero(bt.z[ZERO ? u : 0][j] >> (8 * g))) : 0u;
-            const bf16x8 wf = decode8<ZERO>(c[g * F + f], z);
-#pragma unroll
-            for (int t = 0; t < MQ; ++t) acc[j][t] = mfma16(wf, xf[t], acc[j][t]);
-          }
+          for (int r = 0; r < 4; ++r)
+            sc[j][r] = scale_f32(bt.s[u][j][2 * g + (r >> 1)] >> (16 * (r & 1)) & 0xFFFF, FP16) *
+                       (ZERO ? 1.0f : kSymScale);
         }
+        // (64 rows of x at a time: twice as many accumulators would not fit the registers beside the totals)
 #pragma unroll
-        for (int j = 0; j < NR; ++j)
+        for (int h = 0; h < MQ; h += 4) {
+          f32x4 acc[NR][4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float sc = scale_f32(bt.s[u][j][2 * g + (r >> 1)] >> (16 * (r & 1)) & 0xFFFF, FP16) *
-                             (ZERO ? 1.0f : kSymScale);
+          for (int j = 0; j < NR; ++j)
 #pragma unroll
-            for (int t = 0; t < MQ; ++t) tot[j][t][r] = fmaf(sc, acc[j][t][r], tot[j][t][r]);
-          }
+            for (int t = 0; t < 4; ++t) acc[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int f = 0; f < F; ++f)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const bf16x8 xf = as_bf16x8(
+                  *reinterpret_cast<const uint4*>(ring + ((xa ^ ((g * F + f) * 64)) + (h + t) * 4096)));
+#pragma unroll
+              for (int j = 0; j < NR; ++j) acc[j][t] = mfma16(wf[j][f], xf, acc[j][t]);
+            }
+#pragma unroll
+          for (int j = 0; j < NR; ++j)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) tot[j][h + t][r] = fmaf(sc[j][r], acc[j][t][r], tot[j][h + t][r]);
+          if (MQ > 4) __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   };
@@ -451,17 +462,17 @@ __device__ __forceinline__ void mid_w4(const W4Args& a, int nblocks, uint8_t* ri
     }
   }
 }
-template <int GROUP, bool PAIR, bool ZERO>
+template <int GROUP, bool PAIR, bool ZERO, int MQ>
 __global__ __launch_bounds__(512) void gemm_mid_w4(W4Args a, int nblocks) {
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[8 * kMidUnit];
-  if (a.fp16) mid_w4<GROUP, PAIR, ZERO, true>(a, nblocks, ring);
-  else mid_w4<GROUP, PAIR, ZERO, false>(a, nblocks, ring);
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kMidRing];
+  if (a.fp16) mid_w4<GROUP, PAIR, ZERO, MQ, true>(a, nblocks, ring);
+  else mid_w4<GROUP, PAIR, ZERO, MQ, false>(a, nblocks, ring);
 }
-template <int GROUP, bool PAIR, bool ZERO>
+template <int GROUP, bool PAIR, bool ZERO, int MQ>
 hipError_t launch_mid(W4Args a, hipStream_t s) {
-  a.mtiles = (a.M + kMidM - 1) / kMidM;
+  a.mtiles = (a.M + 16 * MQ - 1) / (16 * MQ);
   const int nblocks = (a.N / 16 + (PAIR ? 3 : 7)) / (PAIR ? 4 : 8);
-  gemm_mid_w4<GROUP, PAIR, ZERO><<<(unsigned)a.mtiles * ((nblocks + 7) / 8 * 8), 512, 0, s>>>(a, nblocks);
+  gemm_mid_w4<GROUP, PAIR, ZERO, MQ><<<(unsigned)a.mtiles * ((nblocks + 7) / 8 * 8), 512, 0, s>>>(a, nblocks);
   return hipGetLastError();
 }
 
@@ -676,24 +687,27 @@ hipError_t launch_stream(W4Args a, hipStream_t s) {
   gemm_stream_w4<MQ, NR, GROUP, PAIR, ZERO, W, XL><<<grid, 64 * W, lds, s>>>(a);
   return hipGetLastError();
 }
-// More than 32 rows of x: the streaming tiles where the middling ones would not be enough workgroups, the latter for
-// up to two of them per CU, the MFMA tiles beyond.  Microseconds, streaming and middling tiles, at rows x weight rows x
-// columns (workgroups of the latter per CU): group 128, 128 x 7168 x 7168 (0.4) 41 and 45, 192 x 6144 x 4096 (0.6)
-// 40 and 27, 256 x 7168 x 7168 (0.9) 79 and 46; group 64, 256 x 3584 x 4096 (0.4) 41 and 29; group 32 pair, 256 x
-// 2048 x 7168 (0.5) 70 and 57.  MFMA and middling tiles: group 128, 512 x 7168 x 7168 (1.75) 123 and 89, 2048 x 2048 x
-// 2048 (2) 39 and 38, 2200 (2.2) 39 and 48; group 32 pair, 1024 x 2048 x 7168 (2) 213 and 122, 2048 (4) 213 and 243.
-// Up to 32 rows half of a middling tile or more would be idle: 24 x 28672 x 4096 (0.9) 27 and 31.
+// More than 32 rows of x: the streaming tiles where the middling ones would not be enough workgroups; these with 64
+// rows of x for up to one workgroup per CU, with 128 where that is no more than one (groups of 32: two), with 64 up to
+// two; the MFMA tiles beyond.  Microseconds at rows x weight rows x columns (workgroups with 64 rows of x per CU): streaming
+// and 64 rows, group 128, 128 x 7168 x 7168 (0.4) 41 and 45, 192 x 6144 x 4096 (0.6) 40 and 27, 256 x 7168 x 7168 (0.9)
+// 79 and 46; group 64, 256 x 3584 x 4096 (0.4) 41 and 29; group 32 pair, 256 x 2048 x 7168 (0.5) 70 and 57.  64 rows,
+// 128 and MFMA tiles, group 128, 256 x 7168 x 7168 (0.9) 47, 68 and 121, 512 (1.75) 88, 71 and 122, 1024 (3.5) 178,
+// 135 and 124, 2048 x 2048 x 2048 (2) 38, 27 and 39; group 32 pair, 1024 x 2048 x 7168 (2) 118, 90 and 193, 2048 (4)
+// 247, 187 and 213.  Up to 32 rows half of a middling tile or more would be idle: 24 x 28672 x 4096 (0.9) 27 and 31.
 template <int GROUP, bool PAIR, bool ZERO>
 hipError_t launch_tiles(W4Args a, int num_cus, hipStream_t s) {
   const int64_t blocks = a.N / 16 * (PAIR ? 2 : 1), mtiles = (a.M + 31) / 32;
-  const int64_t mid = (int64_t)((a.M + kMidM - 1) / kMidM) * ((blocks + 7) / 8);
-  if (a.M > 32 && mid > 2 * num_cus) {
+  const int64_t mid64 = (mtiles + 1) / 2 * ((blocks + 7) / 8), mid128 = (mtiles + 3) / 4 * ((blocks + 7) / 8);
+  if (a.M > 32 && mid64 > (GROUP == 128 ? num_cus / 2 : num_cus / 8 * 3)) {
+    if (mid64 > num_cus && mid128 <= num_cus) return launch_mid<GROUP, PAIR, ZERO, 8>(a, s);
+    if (mid64 <= 2 * num_cus) return launch_mid<GROUP, PAIR, ZERO, 4>(a, s);
+    if (GROUP == 32 && mid128 <= 2 * num_cus) return launch_mid<GROUP, PAIR, ZERO, 8>(a, s);
     a.mtiles = (a.M + kTileM - 1) / kTileM;
     const int64_t grid = (int64_t)a.mtiles * ((a.N + (PAIR ? 127 : 255)) / (PAIR ? 128 : 256));
     gemm_tile_w4<GROUP, PAIR, ZERO><<<(unsigned)grid, 256, 0, s>>>(a);
     return hipGetLastError();
   }
-  if (a.M > 32 && mid > (GROUP == 128 ? num_cus / 2 : num_cus / 8 * 3)) return launch_mid<GROUP, PAIR, ZERO>(a, s);
   if (a.M <= 16) {
     // x in LDS where it fits (1 x 7168 x 7168 11.2 us, 12.3 with x from L2; 16 rows of 7168 do not).  16 weight rows
     // a workgroup (of a pair 8 of either matrix) where that is no more than one per CU: pair 1 x 2048 x 7168 10.4 us,

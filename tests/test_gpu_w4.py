@@ -183,11 +183,11 @@ def test_gemm_w4_past_32_bit_offsets(moe):
         assert ((y.float() - want).abs() <= want.abs() * 2 * BF + 1).all()
 
 
-# Of a matrix of few columns so many weight rows (or rows of x) that the middling or the MFMA tiles take it: by tiles of
-# 128 weight rows and 64 rows of x, more than half of 256 CUs, or two per CU.
+# Of a matrix of few columns so many weight rows (or rows of x) that the middling or the MFMA tiles take it: tiles of 128
+# weight rows by 64 rows of x (more than half of 256 CUs), by 128 rows of x, and of 256 by 128 rows.
 TILES = [(999, 3216, 256), (1000, 4096, 128), (97, 24592, 128), (33, 49168, 128), (1025, 2992, 1152), (6145 * 32, 16, 128),
          (250, 4224, 128), (130, 5520, 256), (70, 8336, 384), (64, 16400, 640), (33, 17000 // 16 * 16, 1152), (2000, 528, 512),
-         (999, 8208, 256), (129, 22288, 128), (65, 33360, 384), (2100, 2080, 1280), (5000, 1040, 128)]
+         (999, 8208, 256), (129, 22288, 128), (65, 33360, 384), (2100, 2080, 1280), (5000, 1040, 128), (300, 7152, 384), (120, 18416, 256)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
@@ -209,7 +209,7 @@ def test_gemm_w4_many_tiles_of_a_pair(moe, zeros, dtype):
         check(x, moe.gemm_w4(x, moe.w4_tile(*w), moe.w4_tile(*up)), w, up, group)
 
 
-@pytest.mark.parametrize("N", [24592, 33360])
+@pytest.mark.parametrize("N", [8976, 24592, 33360, 65552])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("zeros", [False, True])
 def test_gemm_w4_many_tiles_every_code(moe, N, group, zeros):
@@ -224,7 +224,7 @@ def test_gemm_w4_many_tiles_every_code(moe, N, group, zeros):
     assert torch.equal(y, want.t())
 
 
-@pytest.mark.parametrize("N", [3216, 8208])
+@pytest.mark.parametrize("N", [1616, 3216, 8208])
 def test_gemm_w4_many_tiles_neighbours_and_non_finite_values(moe, N):
     M, K = 999, 256
     w = moe.w4_tile(*_w(N, K, 32, True, 1))
@@ -246,7 +246,7 @@ def test_gemm_w4_many_tiles_neighbours_and_non_finite_values(moe, N):
     check(x, moe.gemm_w4(x, moe.w4_tile(*w)), w, None, 128)
 
 
-@pytest.mark.parametrize("N", [3216, 8208])
+@pytest.mark.parametrize("N", [1616, 3216, 8208])
 def test_gemm_w4_many_tiles_captured_and_on_two_streams(moe, N):
     """A captured call replayed with new inputs, and two at once, give the eager call's bits."""
     M, K = 999, 640
