@@ -291,10 +291,11 @@ __device__ __forceinline__ void mid_w4(const W4Args& a, int nblocks, uint8_t* ri
   const int wk = wv / WN, wn = wv % WN;
   const int r16 = lane & 15, kg = lane >> 4;
   const int K = a.K, nkb = K / 128, nblk = a.N / 16, steps = (nkb + WK * U - 1) / (WK * U);
-  // (a weight block's tiles run on one XCD, whose L2 then reads it once)
-  const int turn = blockIdx.x >> 3, nb = turn / a.mtiles * 8 + (blockIdx.x & 7);
-  if (nb >= nblocks) return;
-  const int m0 = turn % a.mtiles * M, b0 = nb * (8 / PC) + wn * (NR / PC);
+  // (every XCD takes an eighth of the tiles in a row, those of a weight block one behind the other: its L2 then
+  // reads the block once)
+  const int tile = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  if (tile >= nblocks * a.mtiles) return;
+  const int m0 = tile % a.mtiles * M, b0 = tile / a.mtiles * (8 / PC) + wn * (NR / PC);
   uint32_t unit0[NR];
 #pragma unroll
   for (int j = 0; j < NR; ++j)  // (a block past N re-reads the last one; never stored)
@@ -472,7 +473,7 @@ template <int GROUP, bool PAIR, bool ZERO, int MQ>
 hipError_t launch_mid(W4Args a, hipStream_t s) {
   a.mtiles = (a.M + 16 * MQ - 1) / (16 * MQ);
   const int nblocks = (a.N / 16 + (PAIR ? 3 : 7)) / (PAIR ? 4 : 8);
-  gemm_mid_w4<GROUP, PAIR, ZERO, MQ><<<(unsigned)a.mtiles * ((nblocks + 7) / 8 * 8), 512, 0, s>>>(a, nblocks);
+  gemm_mid_w4<GROUP, PAIR, ZERO, MQ><<<(unsigned)(a.mtiles * nblocks + 7) / 8 * 8, 512, 0, s>>>(a, nblocks);
   return hipGetLastError();
 }
 

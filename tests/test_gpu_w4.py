@@ -187,7 +187,8 @@ def test_gemm_w4_past_32_bit_offsets(moe):
 # weight rows by 64 rows of x (more than half of 256 CUs), by 128 rows of x, and of 256 by 128 rows.
 TILES = [(999, 3216, 256), (1000, 4096, 128), (97, 24592, 128), (33, 49168, 128), (1025, 2992, 1152), (6145 * 32, 16, 128),
          (250, 4224, 128), (130, 5520, 256), (70, 8336, 384), (64, 16400, 640), (33, 17000 // 16 * 16, 1152), (2000, 528, 512),
-         (999, 8208, 256), (129, 22288, 128), (65, 33360, 384), (2100, 2080, 1280), (5000, 1040, 128), (300, 7152, 384), (120, 18416, 256)]
+         (999, 8208, 256), (129, 22288, 128), (65, 33360, 384), (2100, 2080, 1280), (5000, 1040, 128), (300, 7152, 384), (120, 18416, 256),
+         (8321, 128, 256), (17000, 48, 384), (9000, 144, 128)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
