@@ -197,8 +197,8 @@ __global__ __launch_bounds__(64) void route_exact_kernel(const float* __restrict
 // 16 lanes per token
 //
 // Lane i of a token holds experts i v .. i v + v - 1 (v = ceil(E / 16)) and their c in fp32.  A key is c's
-// place below the row's largest, in 23 bits, above the expert's complement in 9: unsigned order is c's order
-// and ties go to the lower id, so one register carries an expert through the sort.  Each lane keeps its eight
+// place below the row's largest, 1 to 2^23 - 1, above the expert's complement, 511 - e, in 9 bits: unsigned order is
+// c's order and ties go to the lower id, so one register carries an expert through the sort, and 0 is no expert.  Each lane keeps its eight
 // largest keys in order (one med3 per place and key), then four exchanges with other lanes merge the lists
 // (the larger of each with the other's reversed, and a bitonic sort of eight).
 //
@@ -363,8 +363,9 @@ __global__ __launch_bounds__(64) void route_scored_kernel(const float* __restric
 #pragma unroll
   for (int i = 0; i < V; ++i) high = fmaxf(high, c[i]);
   high = max16(kept ? high : -kInf);
-  // (values further below the largest than the span have place 0.  A place is off by half a step of c - base,
-  // its rounding down and the id's carry into it: 3 between two without errors of their own)
+  // (values further below the largest than the span have place 1.  Far from 0 base is rounded, by more than what
+  // it is above high - span: the largest ones then share the last place.  A place is off by half a step of c - base
+  // and its rounding down: 3 between two without errors of their own are more than enough)
   const float span = bias ? 2.0f : 16.0f, scale = kPlaces / span, base = high - span * (1.0f - 0x1p-20f);
   const int apart = 2 + (int)fminf((bias ? 2.0f * tol_s + fabsf(high) * 0x1p-22f : 0.f) * scale + 1.0f, 1e6f);
   uint32_t best[8];
@@ -374,8 +375,8 @@ __global__ __launch_bounds__(64) void route_scored_kernel(const float* __restric
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = e0 + i;
-    const uint32_t place = (uint32_t)fminf(fmaxf((c[i] - base) * scale, 0.0f), kPlaces - 1.0f);  // (NaN: 0)
-    key[i] = kept && (VEC || (i < v && e < E)) ? (place << 9) + (uint32_t)(512 - e) : 0u;
+    const uint32_t place = (uint32_t)fminf(fmaxf((c[i] - base) * scale, 1.0f), kPlaces - 1.0f);  // (NaN: 1)
+    key[i] = kept && (VEC || (i < v && e < E)) ? (place << 9) + (uint32_t)(511 - e) : 0u;
 #pragma unroll
     for (int j = 7; j > 0; --j)
       if (j <= i) best[j] = med3(key[i], best[j - 1], best[j]);
@@ -400,13 +401,13 @@ __global__ __launch_bounds__(64) void route_scored_kernel(const float* __restric
     const uint32_t after = j < 7 ? best[j + 1] : next;
     const bool apart_here = after == 0u || (int)(best[j] >> 9) - (int)(after >> 9) >= apart;
     if (j < k) {
-      unsure |= best[j] < 2u << 9;  // (place 0: clamped, masked or NaN)
+      unsure |= best[j] < 2u << 9;  // (place 1: clamped, masked or NaN)
       close |= !apart_here;
     }
     if (j >= k - 1) gap |= apart_here;
     if (j == li) mine = best[j];
   }
-  int id = (mine & 511u) ? 512 - (int)(mine & 511u) : 0, rank = li < 8 ? li : 16;
+  int id = mine ? 511 - (int)(mine & 511u) : 0, rank = li < 8 ? li : 16;
   if (__ballot(close)) {
     // candidates again, in 64 bits: right among them if a gap divides them from the rest
     uint32_t last = 0u;

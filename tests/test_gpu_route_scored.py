@@ -270,6 +270,44 @@ def test_route_scored_grad_against_differences(moe, sigmoid, renorm):
     assert abs(num - (dl * v).sum()) <= (mag * np.abs(v)).sum() * (G + W) + 1e-8
 
 
+SIZES = [(64, 8, 4, 2), (128, 4, 2, 1), (256, 8, 4, 2), (384, 16, 5, 2), (512, 2, 1, 2), (8, 2, 1, 1), (60, 6, 2, 2),
+         (320, 4, 2, 2), (511, 7, 3, 1)]  # E, groups, top_groups, group_top
+
+
+def _places(E):
+    """Experts at the ends of the row, of its sixteenths and of its middle."""
+    v = (E + 15) // 16
+    return sorted({e for e in (0, 1, v - 1, v, 2 * v - 1, E // 2 - 1, E // 2, E - v, E - 2, E - 1) if 0 <= e < E})
+
+
+@pytest.mark.parametrize("E,groups,top,gt", SIZES)
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_route_scored_every_expert_first_in_far_rows(moe, E, groups, top, gt, sigmoid):
+    """Rows of neighbouring logits that lie far from 0, each expert of interest the largest of its row: without a
+    bias the order is the logits', wherever they lie."""
+    down = torch.stack([(torch.arange(E) - e) % E for e in _places(E)]).float()
+    k = min(8, E // groups * top)
+    for step in (1.0 / 8, 1.0):
+        rows = [off - step * down for off in (0.0, 20.0, 255.0, 272.5, 300.0, 500.0, 600.0, 1e3, 5e3, 1e4, 2.0 ** 20)]
+        l = torch.cat(rows + [r - 2 * r[:, :1].max() for r in rows])
+        for kw in (dict(), dict(groups=groups, top_groups=top, group_top=gt)):
+            check(moe, l, k, sigmoid=sigmoid, tiny=2.0 ** -149, **kw)
+
+
+@pytest.mark.parametrize("E,groups,top,gt", SIZES)
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_route_scored_every_expert_first_by_far_biases(moe, E, groups, top, gt, sigmoid):
+    """The same of biases, which order the experts and lie far from 0."""
+    k = min(8, E // groups * top)
+    l = _logits(3, E, 7, 0.01)
+    for off in (0.0, 20.0, 33.0, 34.0, 40.0, 64.0, 100.0, 1e3, -31.0, -40.0, -100.0, -1e3):
+        for e in _places(E):
+            bias = off - ((torch.arange(E) - e) % E).float() / 16
+            for kw in (dict(), dict(groups=groups, top_groups=top, group_top=gt)):
+                ids, _ = check(moe, l, k, bias, sigmoid, **kw)
+                assert (ids[:, 0] == e).all() or kw
+
+
 def test_route_scored_past_32_bit_offsets(moe):
     """More than 2^32 bytes of logits: every fourth row is the same row."""
     E, k = 512, 8
