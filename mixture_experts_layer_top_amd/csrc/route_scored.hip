@@ -367,7 +367,9 @@ __global__ __launch_bounds__(64) void route_scored_kernel(const float* __restric
   // it is above high - span: the largest ones then share the last place.  A place is off by half a step of c - base
   // and its rounding down: 3 between two without errors of their own are more than enough)
   const float span = bias ? 2.0f : 16.0f, scale = kPlaces / span, base = high - span * (1.0f - 0x1p-20f);
-  const int apart = 2 + (int)fminf((bias ? 2.0f * tol_s + fabsf(high) * 0x1p-22f : 0.f) * scale + 1.0f, 1e6f);
+  // (up to all places: sums past 2^21 lie more than a million apart, and still may be out of order)
+  const float off = (bias ? 2.0f * tol_s + fabsf(high) * 0x1p-22f : 0.f) * scale;
+  const int apart = 2 + (int)fminf(off + 1.0f, kPlaces);
   uint32_t best[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) best[j] = 0u;

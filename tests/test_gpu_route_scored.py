@@ -308,6 +308,27 @@ def test_route_scored_every_expert_first_by_far_biases(moe, E, groups, top, gt, 
                 assert (ids[:, 0] == e).all() or kw
 
 
+def _at_a_border(rng, T, E, c, step):
+    """Logits [T, E] and biases [E], on fp32's grid of width `step` there, whose sums all lie within some 2^-24 of
+    c + step / 2, half a step: fp32's scores, off by less, put them a whole step apart."""
+    m = rng.integers(int(0.1 / step), int(0.9 / step) + 1, E)
+    s = step / 2 + step * m
+    l = np.log(s / (1 - s)).astype(np.float32)
+    l = l + rng.integers(-1, 2, (T, E)) * np.spacing(l)
+    return torch.from_numpy(l.astype(np.float32)), torch.from_numpy((c - step * m).astype(np.float32))
+
+
+@pytest.mark.parametrize("E,k", [(8, 4), (16, 8), (14, 6), (64, 8), (60, 8)])
+@pytest.mark.parametrize("c", [2.0 ** 6, 2.0 ** 16, 2.0 ** 20, 2.0 ** 21, 2.0 ** 22, 3.0 * 2 ** 20])
+def test_route_scored_at_a_border_of_far_sums(moe, E, k, c):
+    """Scores and biases whose sums fp32 rounds to either side, far from 0: compared in 64 bits."""
+    l, b = _at_a_border(np.random.default_rng(E), 200, E, c, float(np.spacing(np.float32(c))))
+    b[16:] -= 4.0  # (16 or fewer are near: in some rows as many are above the border as are selected)
+    check(moe, l, k, b)
+    if E % 4 == 0:
+        check(moe, l, 4, b, groups=4, top_groups=2, group_top=2 if E > 4 else 1)
+
+
 def test_route_scored_past_32_bit_offsets(moe):
     """More than 2^32 bytes of logits: every fourth row is the same row."""
     E, k = 512, 8
