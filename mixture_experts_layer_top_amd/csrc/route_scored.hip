@@ -403,7 +403,7 @@ __global__ __launch_bounds__(64) void route_scored_kernel(const float* __restric
     const uint32_t after = j < 7 ? best[j + 1] : next;
     const bool apart_here = after == 0u || (int)(best[j] >> 9) - (int)(after >> 9) >= apart;
     if (j < k) {
-      unsure |= best[j] < 2u << 9;  // (place 1: clamped, masked or NaN)
+      unsure |= (int)(best[j] >> 9) <= apart;  // (place 1: clamped, masked or NaN, or too near to what is)
       close |= !apart_here;
     }
     if (j >= k - 1) gap |= apart_here;

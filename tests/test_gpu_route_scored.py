@@ -329,6 +329,19 @@ def test_route_scored_at_a_border_of_far_sums(moe, E, k, c):
         check(moe, l, 4, b, groups=4, top_groups=2, group_top=2 if E > 4 else 1)
 
 
+@pytest.mark.parametrize("E,k", [(8, 2), (16, 4), (14, 3), (64, 2), (60, 6)])
+@pytest.mark.parametrize("top", [100.0, 50.0, 1000.0, -100.0])
+def test_route_scored_at_the_end_of_the_span(moe, E, k, top):
+    """One expert as far above the others as the fast comparison reaches, and the others at a border of fp32 there:
+    its nearest places, and what lies below them."""
+    step = float(np.spacing(np.float32(abs(top) + 1.0)))
+    for off in range(-2, 3):
+        l, b = _at_a_border(np.random.default_rng(E + off), 200, E, top - 2.0 + off * step, step)
+        l[:, E // 2], b[E // 2] = 0.0, top - 0.5
+        b[16:] -= 4.0
+        check(moe, l, k, b)
+
+
 def test_route_scored_past_32_bit_offsets(moe):
     """More than 2^32 bytes of logits: every fourth row is the same row."""
     E, k = 512, 8
