@@ -284,6 +284,7 @@ __global__ __launch_bounds__(64) void route_scored_kernel(const float* __restric
   }
   // scores, and a softmax's largest logit and 1 / sum
   float top = -kInf, inv = 1.0f;
+  double inv64 = 1.0;
   if (p.score == kScoreSoftmax) {
 #pragma unroll
     for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
@@ -296,8 +297,9 @@ __global__ __launch_bounds__(64) void route_scored_kernel(const float* __restric
     } else {
       double sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += (double)expf(l[i] - top);
-      inv = 1.0f / (float)reduce16(sum, SumOp{});
+      for (int i = 0; i < V; ++i) sum += exp((double)l[i] - (double)top);  // (-inf past E)
+      inv64 = 1.0 / reduce16(sum, SumOp{});
+      inv = (float)inv64;
     }
   }
   const bool scored = bias || (p.groups > 1 && p.group_top > 1);
@@ -445,25 +447,25 @@ __global__ __launch_bounds__(64) void route_scored_kernel(const float* __restric
     if (close) rank = above;
   }
   const bool chosen = rank < k;
-  float lj = logits[row + min(id, E - 1)];
-  float s;
-  // (scores near fp32's smallest, whose last bits a factor or a renormalisation would bring out, by route_exact)
+  // scores, their renormalisation and scale in 64 bits; what even they do not hold, by route_exact
+  const float lj = logits[row + min(id, E - 1)];
+  double s;
   if (p.score == kScoreSoftmax) {
-    const float m = p.renorm ? max16(chosen ? lj : -kInf) : top;
-    s = expf(lj - m) * (p.renorm ? 1.0f : inv);
-    unsure |= chosen && !(lj - m > -70.0f);
+    const double x = (double)lj - (double)(p.renorm ? max16(chosen ? lj : -kInf) : top);
+    s = exp(x) * inv64;
+    unsure |= chosen && !(x > -700.0);
   } else {
-    const float e = expf(-fabsf(lj));
-    s = (lj > 0.f ? 1.0f : e) / (1.0f + e);
-    unsure |= chosen && !(lj > -70.0f);
+    const double e = exp(-fabs((double)lj));
+    s = (lj > 0.f ? 1.0 : e) / (1.0 + e);
+    unsure |= chosen && !(lj > -700.0f);
   }
-  if (p.renorm) s = s / reduce16(chosen ? s : 0.f, SumOp{});
+  if (p.renorm) s = s / reduce16(chosen ? s : 0.0, SumOp{});
   // (unsure is a group's, a token's: any of its lanes)
   const uint64_t ask = __ballot(unsure);
   const bool redo = (ask >> (lane & 48)) & 0xFFFF;
   if (tok < T && chosen && !redo) {
     ids[(size_t)t * k + rank] = id;
-    w[(size_t)t * k + rank] = s * p.scale;
+    w[(size_t)t * k + rank] = float(s * (double)p.scale);
   }
   if (ask) {
     for (int q = 0; q < 4; ++q)

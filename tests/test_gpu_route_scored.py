@@ -342,6 +342,21 @@ def test_route_scored_at_the_end_of_the_span(moe, E, k, top):
         check(moe, l, k, b)
 
 
+@pytest.mark.parametrize("E,k,groups,top", [(256, 8, 8, 4), (384, 8, 1, 1), (60, 4, 6, 3), (100, 1, 1, 1)])
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("renorm,scale", [(True, 2.5), (False, 1.0)])
+def test_route_scored_weights_are_rounded_once(moe, E, k, groups, top, sigmoid, renorm, scale):
+    """Scores, their sum, quotient and scale in 64 bits: with an exponential of 2 u64, E additions and 4 more
+    roundings, u64 = 2^-53, an fp32 weight is within half a step, 2^-24, and 2^-42 of it more."""
+    l = _logits(1500, E, E)
+    l[::7] *= 20.0  # (scores near 0 and 1 too)
+    kw = dict(groups=groups, top_groups=top, group_top=2, renorm=renorm, scale=scale)
+    for bias in (None, _bias(E, E, 0.05 if sigmoid else 1.0 / E)):
+        ids, w = check(moe, l, k, bias, sigmoid, tiny=2.0 ** -149, **kw)
+        ww = B.route_scored(f64(l), k, None if bias is None else f64(bias), sigmoid, **kw)[1]
+        assert (np.abs(f64(w) - ww) <= (2.0 ** -24 + 2.0 ** -42) * np.abs(ww) + 2.0 ** -150).all()
+
+
 def test_route_scored_past_32_bit_offsets(moe):
     """More than 2^32 bytes of logits: every fourth row is the same row."""
     E, k = 512, 8
