@@ -566,15 +566,18 @@ hipError_t launch_route_scored(const float* logits, const float* bias, int T, in
     kernel<<<(unsigned)T, 64, 0, s>>>(logits, bias, E, k, p, ids, w);
     return hipGetLastError();
   }
+  // Whole vectors wherever a lane's experts are some of them (8192 tokens, with and
+  // without: 192 experts 6.0 us and 8.5, 320 8.0 and 13.8, 448 9.5 and 17.3).
+  using Kernel = decltype(&route_scored_kernel<4, true>);
+  static constexpr Kernel kVec[] = {
+      &route_scored_kernel<4, true>,  &route_scored_kernel<8, true>,  &route_scored_kernel<12, true>,
+      &route_scored_kernel<16, true>, &route_scored_kernel<20, true>, &route_scored_kernel<24, true>,
+      &route_scored_kernel<28, true>, &route_scored_kernel<32, true>};
   const bool vec = E % 64 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
-  auto* kernel = vec && E == 64    ? &route_scored_kernel<4, true>
-                 : vec && E == 128 ? &route_scored_kernel<8, true>
-                 : vec && E == 256 ? &route_scored_kernel<16, true>
-                 : vec && E == 384 ? &route_scored_kernel<24, true>
-                 : vec && E == 512 ? &route_scored_kernel<32, true>
-                 : E <= 64         ? &route_scored_kernel<4, false>
-                 : E <= 128        ? &route_scored_kernel<8, false>
-                 : E <= 256        ? &route_scored_kernel<16, false> : &route_scored_kernel<32, false>;
+  const Kernel kernel = vec        ? kVec[E / 64 - 1]
+                        : E <= 64  ? &route_scored_kernel<4, false>
+                        : E <= 128 ? &route_scored_kernel<8, false>
+                        : E <= 256 ? &route_scored_kernel<16, false> : &route_scored_kernel<32, false>;
   kernel<<<((unsigned)T + 3) / 4, 64, 0, s>>>(logits, bias, T, E, k, p, ids, w);
   return hipGetLastError();
 }

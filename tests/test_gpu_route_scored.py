@@ -357,6 +357,20 @@ def test_route_scored_weights_are_rounded_once(moe, E, k, groups, top, sigmoid, 
         assert (np.abs(f64(w) - ww) <= (2.0 ** -24 + 2.0 ** -42) * np.abs(ww) + 2.0 ** -150).all()
 
 
+@pytest.mark.parametrize("E", [64 * i for i in range(1, 9)])
+def test_route_scored_of_whole_vectors_and_not(moe, E):
+    """Every E of whole 16-byte vectors per lane, and the same rows at an address that allows none (a softmax's sum
+    then has another order: a last bit)."""
+    T = 70
+    l, b = _logits(T, E, E).cuda(), _bias(E, E).cuda()
+    moved = torch.cat([torch.zeros(1, device="cuda"), l.flatten()])[1:].view(T, E)
+    for kw in (dict(), dict(groups=8, top_groups=4, group_top=2), dict(score=0, renorm=False)):
+        for bias in (b, None):
+            (i0, w0), (i1, w1) = moe.route_scored(l, 8, bias, **kw), moe.route_scored(moved, 8, bias, **kw)
+            assert torch.equal(i0, i1) and (w0 - w1).abs().max() <= 2.0 ** -24
+    check(moe, l.cpu(), 8, b.cpu(), groups=8, top_groups=4, group_top=2)
+
+
 def test_route_scored_past_32_bit_offsets(moe):
     """More than 2^32 bytes of logits: every fourth row is the same row."""
     E, k = 512, 8
