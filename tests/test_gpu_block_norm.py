@@ -290,6 +290,22 @@ def test_block_norm_grad_of_non_finite_rows(moe):
     assert dp[4103].isnan() and dq[5].isnan()
 
 
+@pytest.mark.parametrize("d", [512, 1024, 2048, 4096, 8192, 16384])
+def test_block_norm_grad_row_sums_past_24_bits(moe, d):
+    """Whole numbers, whose squares sum to more than fp32 holds: eight at a time they are exact in fp32, and a
+    row's are in fp64, so that both roots are those of the exact mean, bit for bit."""
+    rng = np.random.default_rng(d)
+    one, zero = torch.ones(1, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, d, dtype=torch.bfloat16, device="cuda")
+    for _ in range(24):
+        v = rng.integers(-256, 257, (1, d)).astype(np.float32)
+        t = torch.from_numpy(v).to(torch.bfloat16).cuda()
+        n = v * (np.float32(1) / np.sqrt(np.float32((v.astype(np.float64) ** 2).sum() / d)))
+        # dpre = dy n2; with dy = 0 H is dh, and dpost = H n1
+        dpre = moe.block_norm_grad(one, one, t, one[0], eps=0.0)[2]
+        dpost = moe.block_norm_grad(zero, t, one, one[0], one, one[0], eps=0.0)[3]
+        assert np.array_equal(dpre.cpu().numpy(), n[0]) and np.array_equal(dpost.cpu().numpy(), n[0])
+
+
 def test_block_norm_past_32_bit_offsets(moe):
     """More than 2^32 bytes per tensor: every fourth row is the same row."""
     d = 7168
