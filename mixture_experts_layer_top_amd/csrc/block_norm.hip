@@ -87,7 +87,8 @@ __device__ __forceinline__ float squares(const uint4& v) {
 
 // A row's sums in fp64, the same in every thread and in a fixed order: row_reduce's, but that all rows of 16
 // lanes pass theirs on through LDS, where the r-th row of each wavefront joins those of value r: one exchange among lanes
-// for all values (4096 x 2048 33.6 us; with row_reduce in fp64 37.0, in fp32 32.9).  red: NA * R / 16 values of its own for every call.
+// for all values (4096 x 2048 33.6 us; with row_reduce in fp64 37.0, in fp32 32.9).  red: NA * R / 16 values of its
+// own for every call.
 template <int R, int NA>
 __device__ __forceinline__ void row_sums(double (&v)[NA], double* red) {
   static_assert(NA <= 4, "a row of lanes per value");
@@ -282,25 +283,10 @@ __global__ __launch_bounds__(R, 4) void block_grad_kernel(BlockGrad a, double in
   }
 }
 
-// The workgroups' sums [nb][2][d] in a fixed order: 32 columns per workgroup, as dw_reduce_kernel in
-// norm.hip, then the factors that all rows share.
+// The workgroups' sums [nb][2][d] in a fixed order (norm_dev.h), then the factors that all rows share.
 __global__ __launch_bounds__(256) void block_grad_sum_kernel(BlockGrad a, int nb, int d) {
   __shared__ float red[32][33];
-  const int c = threadIdx.x & 7, r = threadIdx.x >> 3, col = blockIdx.x * 32 + c * 4;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  if (col < 2 * d) {  // (d % 8 == 0)
-#pragma unroll 4
-    for (int b = r; b < nb; b += 32) {
-      const uint4 v = ld16(a.part, ((size_t)b * 2 * d + col) / 4);
-      s[0] += __uint_as_float(v.x);
-      s[1] += __uint_as_float(v.y);
-      s[2] += __uint_as_float(v.z);
-      s[3] += __uint_as_float(v.w);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) red[r][c * 4 + j] = s[j];
-  __syncthreads();
+  sum_parts(a.part, nb, 2 * d, red);
   const int at = blockIdx.x * 32 + threadIdx.x;
   if (threadIdx.x >= 32 || at >= 2 * d) return;
   float v = 0.f;

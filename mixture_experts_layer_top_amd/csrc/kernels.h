@@ -268,7 +268,8 @@ hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float e
                           int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s,
                           const BlockIn* b = nullptr);
 constexpr int kNormGradBlocks = 512;
-constexpr int kNormGradRows = 3;  // per workgroup, until there are that many
+constexpr int kNormGradRows = 3;      // per workgroup, until there are that many
+constexpr int kNormGradChain = 128;   // and no more than these: more workgroups then
 int rmsnorm_grad_parts(int T);
 hipError_t launch_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* w,
                                float eps, int T, int d, void* dx, float* dw, float* part,

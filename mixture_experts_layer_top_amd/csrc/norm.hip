@@ -404,26 +404,11 @@ __global__ __launch_bounds__(R) void rmsnorm_grad_kernel(
   }
 }
 
-// dw[c] = sum_b part[b][c]: 32 columns per workgroup (whole 128-byte lines), its 32 groups of 8 threads
-// take every 32nd partial, then the groups' sums in order.
+// dw[c] = sum_b part[b][c] (norm_dev.h).
 __global__ __launch_bounds__(256) void dw_reduce_kernel(const float* __restrict__ part, int nb, int d,
                                                         float* __restrict__ dw) {
   __shared__ float red[32][33];
-  const int c = threadIdx.x & 7, r = threadIdx.x >> 3, col = blockIdx.x * 32 + c * 4;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  if (col < d) {  // (d % 8 == 0)
-#pragma unroll 4
-    for (int b = r; b < nb; b += 32) {
-      const uint4 v = ld16(part, ((size_t)b * d + col) / 4);
-      s[0] += __uint_as_float(v.x);
-      s[1] += __uint_as_float(v.y);
-      s[2] += __uint_as_float(v.z);
-      s[3] += __uint_as_float(v.w);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) red[r][c * 4 + j] = s[j];
-  __syncthreads();
+  sum_parts(part, nb, d, red);
   if (threadIdx.x < 32 && blockIdx.x * 32 + (int)threadIdx.x < d) {
     float v = 0.f;
     for (int b = 0; b < 32; ++b) v += red[b][threadIdx.x];
@@ -470,9 +455,12 @@ hipError_t launch_quant_i8(const void* x, bool f32, int T, int d, uint8_t* q, fl
 
 // Partial sums of dw: one per workgroup, each 8 d bytes of traffic beside a row's 6 or 8 d.  At 1, 3 and
 // 6 rows per workgroup: 777 x 4096 13.4, 12.3, 13.4 us; 333 x 4096 9.8, 9.9, 12.5; 1500 x 2048 11.1,
-// 11.9, 12.4.
+// 11.9, 12.4.  A workgroup adds its rows one behind another in fp32, each addition off by up to 2^-24 of what there
+// is: never more than kNormGradChain rows, so that 2^25 rows are no further off than 2^16 (with 512
+// workgroups for all up to 2^-10 of the sum; and short rows in too few wavefronts: 131072 x 1024 217 us, 360 then).
 int rmsnorm_grad_parts(int T) {
-  return T <= 64 ? T : std::min(kNormGradBlocks, std::max(64, (T + kNormGradRows - 1) / kNormGradRows));
+  const int few = std::min(kNormGradBlocks, std::max(64, (T + kNormGradRows - 1) / kNormGradRows));
+  return T <= 64 ? T : std::max(few, (T + kNormGradChain - 1) / kNormGradChain);
 }
 
 hipError_t launch_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* w,

@@ -70,4 +70,30 @@ __device__ __forceinline__ uint4 enlarged(uint4 h) {
   return h;
 }
 
+// Column sums of part [nb][d] by workgroups of 256 threads: 32 columns each (whole 128-byte lines), its 32 groups of
+// 8 threads take every 32nd partial, 16 in fp32 at a time and those in fp64 (one time for up to 512 partials).
+// red[g][c]: group g's sum of the workgroup's column c, 0 past d (d % 4 == 0), behind a barrier.
+__device__ __forceinline__ void sum_parts(const float* __restrict__ part, int nb, int d, float (*red)[33]) {
+  const int c = threadIdx.x & 7, r = threadIdx.x >> 3, col = blockIdx.x * 32 + c * 4;
+  double t[4] = {0.0, 0.0, 0.0, 0.0};
+  if (col < d) {
+    for (int b0 = r; b0 < nb; b0 += 16 * 32) {
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int b = b0; b < min(b0 + 16 * 32, nb); b += 32) {
+        const uint4 v = ld16(part, ((size_t)b * d + col) / 4);
+        s[0] += __uint_as_float(v.x);
+        s[1] += __uint_as_float(v.y);
+        s[2] += __uint_as_float(v.z);
+        s[3] += __uint_as_float(v.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[j] += (double)s[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) red[r][c * 4 + j] = (float)t[j];
+  __syncthreads();
+}
+
 }  // namespace moe

@@ -306,6 +306,38 @@ def test_block_norm_grad_row_sums_past_24_bits(moe, d):
         assert np.array_equal(dpre.cpu().numpy(), n[0]) and np.array_equal(dpost.cpu().numpy(), n[0])
 
 
+@pytest.mark.parametrize("T", [8192, 65536, 65537, 300000, 2 ** 21 + 5, 2 ** 25 - 1])
+@pytest.mark.parametrize("token", [False, True])
+def test_block_norm_grad_sums_over_long_columns(moe, T, token):
+    """Equal rows: a column is T times one fp32 product (whole numbers, eps 0: test_..._past_24_bits), whose
+    additions a chain of fp32 would round the same way each.  At most 128 rows of a workgroup one behind another, 16
+    and then 32 sums: 176 u, and a gate's and the output's roundings."""
+    d, v = 8, np.array([[3.0, 7.0, -11.0, 13.0, 1.0, -5.0, 2.0, 9.0]], np.float32)
+    row = torch.from_numpy(v).to(torch.bfloat16).cuda()
+    n = (v * (np.float32(1) / np.sqrt(np.float32((v.astype(np.float64) ** 2).sum() / d)))).astype(np.float64)[0]
+    one, pre = torch.ones(1, d, dtype=torch.bfloat16, device="cuda").expand(T, d).contiguous(), row.new_ones(d)
+    rows = row.expand(T, d).contiguous()
+    gate = 2 * one if token else 2 * pre
+    _, _, dpre, _, _ = moe.block_norm_grad(one, one, rows, pre, eps=0.0)
+    _, _, _, dpost, dgate = moe.block_norm_grad(torch.zeros_like(one), rows, one, pre, one, pre, gate, eps=0.0)
+    got = [(dpre, 1), (dpost, 2)] + ([] if token else [(dgate, 1)])
+    for g, f in got:
+        assert (np.abs(f64(g) - f * T * n) <= (128 + 16 + 32 + 2) * 2.0 ** -24 * f * T * np.abs(n)).all()
+
+
+@pytest.mark.parametrize("T,d", [(8192, 264), (70001, 40), (300000, 16)])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+def test_block_norm_grad_of_many_rows(moe, T, d, gate):
+    """Products of one sign, so that nothing cancels on the way."""
+    x, h, dy, dh = (_bf16(T, d, seed=i, mean=2.0, std=0.3) for i in range(4))
+    pre, post, gate = _bf16(d, seed=5, mean=1.0, std=0.1), _bf16(d, seed=6, mean=1.0, std=0.1), _gate(gate, T, d)
+    out = moe.block_norm_grad(dy, x, h, pre, dh, post, gate, 0.5, 0.25)
+    ref = B.block_norm_grad(f64(dy), f64(dh), f64(x), f64(h), f64(post), f64(gate), f64(pre), 0.5, 0.25, EPS)
+    for name, g in zip(("dpre", "dpost", "dgate"), out[2:]):
+        if ref[name].ndim == 1:
+            assert (np.abs(f64(g) - ref[name]) <= ref["e_" + name] * (G + 178 * 2.0 ** -24)).all(), name
+
+
 def test_block_norm_past_32_bit_offsets(moe):
     """More than 2^32 bytes per tensor: every fourth row is the same row."""
     d = 7168

@@ -459,3 +459,15 @@ def test_rmsnorm_grad_of_products_below_fp32(moe, d, dy_size, h_size):
     terms = r * (np.abs(g) + np.abs(n) * np.abs(g * n).mean(-1, keepdims=True) + 2.0 ** -149)
     assert (np.abs(f64(dx) - ref) <= np.abs(ref) * 2.0 ** -8 + terms * 2 * Y + r * 2.0 ** -148).all()
     assert not dx[1].any()
+
+
+@pytest.mark.parametrize("T", [8192, 65536, 65537, 300000, 2 ** 21 + 5, 2 ** 25 - 1])
+def test_rmsnorm_grad_sums_over_long_columns(moe, T):
+    """Equal rows of whole numbers, without eps: a column is T times one fp32 product, whose additions a chain of
+    fp32 would round the same way each.  At most 128 rows of a workgroup one behind another, 16 and then 32 sums."""
+    d, v = 8, np.array([[3.0, 7.0, -11.0, 13.0, 1.0, -5.0, 2.0, 9.0]], np.float32)
+    n = (v * (np.float32(1) / np.sqrt(np.float32((v.astype(np.float64) ** 2).sum() / d)))).astype(np.float64)[0]
+    row = torch.from_numpy(v).to(torch.bfloat16).cuda()
+    one = torch.ones_like(row)
+    dw = moe.rmsnorm_grad(one.expand(T, d).contiguous(), row.expand(T, d).contiguous(), one[0], None, 0.0)[1]
+    assert (np.abs(f64(dw) - T * n) <= (128 + 16 + 32 + 2) * 2.0 ** -24 * T * np.abs(n)).all()
