@@ -712,8 +712,9 @@ hipError_t launch_tiles(W4Args a, int num_cus, hipStream_t s) {
   if (a.M <= 16) {
     // x in LDS where it fits (1 x 7168 x 7168 11.2 us, 12.3 with x from L2; 16 rows of 7168 do not).  16 weight rows
     // a workgroup (of a pair 8 of either matrix) where that is no more than one per CU: pair 1 x 2048 x 7168 10.4 us,
-    // 12.7 with 32, 1 x 3200 x 7168 13.8 and 13.1; 16 x 2048 x 7168 10.8 and 12.8, 16 x 7168 x 7168 19.6 and 14.1.
-    const bool narrow = a.N / 16 * 2 <= num_cus;
+    // 12.7 with 32, 1 x 3200 x 7168 13.8 and 13.1; one matrix, 16 x 2048 x 7168 10.8 and 12.8, 16 x 4096 x 7168 11.7
+    // and 13.6, with groups of 32 12.4 and 15.0, 16 x 7168 x 7168 19.6 and 14.1.
+    const bool narrow = blocks <= num_cus;
     if (a.M * xl_stride(a.K) <= kXlBytes) {
       if constexpr (PAIR) {
         if (!narrow) return launch_stream<1, 2, GROUP, PAIR, ZERO, 8, true>(a, s);

@@ -283,6 +283,22 @@ def test_gemm_w4_few_rows_by_more_or_fewer_weight_rows_than_cus_take(moe, M, N, 
     test_gemm_w4(moe, M, N, K, group, zeros, pair)
 
 
+@pytest.mark.parametrize("M,K", [(9, 4096), (16, 2048), (16, 7168)])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("pair", [False, True])
+def test_gemm_w4_a_workgroup_per_cu_and_one_more(moe, M, K, group, zeros, pair):
+    """As many blocks of 16 weight rows as there are CUs, of both matrices in sum, and more: x beside 16 and 32 weight
+    rows gives the same bits."""
+    N = 16 * torch.cuda.get_device_properties(0).multi_processor_count // (2 if pair else 1)
+    big = [_w(N + 16, K, group, zeros, i) for i in range(2 if pair else 1)]
+    few = [tuple(None if t is None else t[:N].contiguous() for t in w) for w in big]
+    x = _bf16(M, K, seed=M)
+    y = moe.gemm_w4(x, *(moe.w4_tile(*w) for w in big))
+    check(x, y, big[0], big[1] if pair else None, group)
+    assert torch.equal(moe.gemm_w4(x, *(moe.w4_tile(*w) for w in few)), y[:, :N])
+
+
 @pytest.mark.parametrize("M,K", [(16, 1920), (16, 2048), (4, 7936), (4, 8192), (1, 32640), (1, 32768)])
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("pair", [False, True])
