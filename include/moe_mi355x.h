@@ -460,7 +460,8 @@ int moe_w4_tile(const moe_w4* src, void* codes, void* scales, uint8_t* zeros, hi
 /* Product of bf16 rows with 4-bit weights: y[m][n] = bf16(sum_k x[m][k] * W[n][k]); with `up` (of w's N, K,
  * group and scale_dtype) the SwiGLU of the pair, bf16(SiLU(x Wt) * (x Upt)): a shared expert's gate and up
  * step, whose y moe_gemm_w4 takes back to d for moe_combine's shared_y.  Codes less zero points are exact in
- * the products, sums and scales are fp32, one rounding.
+ * the products, sums and scales are fp32, one rounding.  A group's sum of x * (code - zero) has to stay in fp32's
+ * range ahead of its scale, and without zeros 16 times that sum: it does for |x| < 2^114, whatever the codes.
  *   x [M][K], y [M][N] bf16, not overlapping.  M * K < 2^31, N * K < 2^32, M * N < 2^37, else
  *   MOE_ERR_UNSUPPORTED; pointers 16-byte aligned.  M = 0 is a no-op. */
 int moe_gemm_w4(const void* x, int M, const moe_w4* w, const moe_w4* up, void* y, hipStream_t stream);

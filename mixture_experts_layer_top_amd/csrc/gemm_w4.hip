@@ -50,7 +50,8 @@ __device__ __forceinline__ uint32_t zero_bytes(uint32_t z) { return 0x80808080u 
 
 // Eight codes -> bf16 of code - z, in K order, exactly.  Without zero points (z = 8) the sign sits in the
 // nibble's own top bit: the high half of a byte then is 16 (code - 8), and the 16 is left to the scale
-// (kSymScale).  Either way a signed byte converts in one instruction and a pair packs in another.
+// (kSymScale): the group's sum is 16 times as large, as far as fp32 goes as one with zero points of 127.  Either
+// way a signed byte converts in one instruction and a pair packs in another.
 constexpr float kSymScale = 0.0625f;
 __device__ __forceinline__ float byte_f32(uint32_t w, int b) { return (float)(int8_t)(w >> (8 * b)); }
 template <bool ZERO>

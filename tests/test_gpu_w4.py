@@ -131,6 +131,21 @@ def test_gemm_w4_large_and_non_finite_values(moe, M):
     assert not moe.gemm_w4(x, t).any()
 
 
+@pytest.mark.parametrize("M", [1, 16, 33, 64, 128, 300])
+@pytest.mark.parametrize("N", [128, 4096])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zero", [None, 8, 127])
+def test_gemm_w4_of_the_largest_x(moe, M, N, group, zero):
+    """x just below 2^114, of one sign, by codes of 0: the largest sums of a group that are promised, 2^14 times x
+    at most, are finite, and its scale brings them back."""
+    K = 256
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    s = torch.full((N, K // group), 2.0 ** -115, dtype=torch.bfloat16, device="cuda")
+    w = (codes, s, None if zero is None else torch.full((N, K // group), zero, dtype=torch.uint8, device="cuda"))
+    x = torch.full((M, K), 2.0 ** 114 * (1 - 2.0 ** -8), dtype=torch.bfloat16, device="cuda")
+    check(x, moe.gemm_w4(x, moe.w4_tile(*w)), w, None, group)
+
+
 @pytest.mark.parametrize("M", [1, 5, 16, 40, 70, 150, 300])
 @pytest.mark.parametrize("pair", [False, True])
 def test_gemm_w4_neighbours_and_repeat(moe, M, pair):
