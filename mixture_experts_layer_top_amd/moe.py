@@ -638,6 +638,14 @@ class W4Weights:
     K: int
     group: int
 
+    def __post_init__(self):
+        # (the library goes by N, K and group: smaller tensors would be read past their ends)
+        dev, shape = self.codes.get_device(), (self.N, self.K // self.group if self.group > 0 else 0)
+        _arg(self.codes, "codes", (self.N, self.K // 2), (torch.uint8,), dev)
+        _arg(self.scales, "scales", shape, (torch.bfloat16, torch.float16), dev)
+        if self.zeros is not None:
+            _arg(self.zeros, "zeros", shape, (torch.uint8,), dev)
+
     def struct(self, layout: int = LAYOUT_TILED) -> W4:
         fmt = SCALE_FP16 if self.scales.dtype == torch.float16 else SCALE_BF16
         return W4(_ptr(self.codes), _ptr(self.scales), _ptr(self.zeros), self.N, self.K, self.group, fmt, layout)

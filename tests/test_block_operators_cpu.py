@@ -185,6 +185,19 @@ def test_binding_refusals():
     assert t.struct().layout == moe.LAYOUT_TILED and ctypes.sizeof(t.struct()) == 48
 
 
+def test_w4_weights_of_other_sizes_are_refused():
+    """Weights made by hand: the library reads N, K and group's worth of them."""
+    q, s, z = torch.zeros(16, 64, dtype=torch.uint8), torch.zeros(16, 4, dtype=torch.float16), None
+    moe.W4Weights(q, s, z, 16, 128, 32)
+    moe.W4Weights(q, s, q[:, :4].contiguous(), 16, 128, 32)
+    for bad in (dict(N=32), dict(N=0), dict(K=256), dict(K=64), dict(group=16), dict(group=64), dict(group=0),
+                dict(codes=q[:8]), dict(codes=q.to(torch.int8)), dict(codes=q.t().contiguous().t()),
+                dict(scales=s[:, :2]), dict(scales=s.float()), dict(zeros=q[:, :2]), dict(zeros=q[:, :4]),
+                dict(zeros=s)):
+        with pytest.raises(moe.MoEError):
+            moe.W4Weights(**dict(dict(codes=q, scales=s, zeros=z, N=16, K=128, group=32), **bad))
+
+
 def test_binding_runs_on_the_tensors_gpu(monkeypatch):
     """Tensors of a GPU that is not the current one: every call is made with that GPU current and on its stream,
     and tensors of two GPUs are refused."""
