@@ -302,7 +302,11 @@ __global__ __launch_bounds__(256) void block_grad_sum_kernel(BlockGrad a, int nb
 
 }  // namespace
 
-int block_grad_parts(int T) { return rmsnorm_grad_parts(T); }
+// A row takes two reductions one behind the other, and a workgroup's sums 16 d bytes beside its 12 or 16 d: at 1, 2, 3
+// and 4 rows per workgroup, 200 x 4096 12.5, 13.0, 14.6, 16.8 us; 333 x 4096 with a gate per token 15.5, 14.9, 17.7,
+// 20.2; 777 x 7168 31.7, 29.8, 31.2, 29.6; 777 x 4096 with a gate per token 22.3, 21.0, 22.8, 23.8.  (Up to 1024
+// workgroups for long batches: 2048 x 7168 57 us, 50 with 512.)
+int block_grad_parts(int T) { return norm_grad_parts(T, kBlockGradRows); }
 
 hipError_t launch_block_grad(BlockGrad a, int d, hipStream_t s) {
   // Outputs pass the caches by when a call's rows are more than the 256 MB last-level cache holds (8192 x 7168 154

@@ -270,6 +270,7 @@ hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float e
 constexpr int kNormGradBlocks = 512;
 constexpr int kNormGradRows = 3;      // per workgroup, until there are that many
 constexpr int kNormGradChain = 128;   // and no more than these: more workgroups then
+int norm_grad_parts(int T, int rows);
 int rmsnorm_grad_parts(int T);
 hipError_t launch_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* w,
                                float eps, int T, int d, void* dx, float* dw, float* part,
@@ -295,6 +296,7 @@ struct BlockGrad {
   float* part;
   int once;  // (the launch's)
 };
+constexpr int kBlockGradRows = 2;  // as kNormGradRows
 int block_grad_parts(int T);
 hipError_t launch_block_grad(BlockGrad a, int d, hipStream_t s);
 

@@ -455,11 +455,14 @@ hipError_t launch_quant_i8(const void* x, bool f32, int T, int d, uint8_t* q, fl
 
 // Partial sums of dw: one per workgroup, each 8 d bytes of traffic beside a row's 6 or 8 d.  At 1, 3 and
 // 6 rows per workgroup: 777 x 4096 13.4, 12.3, 13.4 us; 333 x 4096 9.8, 9.9, 12.5; 1500 x 2048 11.1,
-// 11.9, 12.4.  A workgroup adds its rows one behind another in fp32, each addition off by up to 2^-24 of what there
-// is: never more than kNormGradChain rows, so that 2^25 rows are no further off than 2^16 (with 512
-// workgroups for all up to 2^-10 of the sum; and short rows in too few wavefronts: 131072 x 1024 217 us, 360 then).
-int rmsnorm_grad_parts(int T) {
-  const int few = std::min(kNormGradBlocks, std::max(64, (T + kNormGradRows - 1) / kNormGradRows));
+// 11.9, 12.4.
+int rmsnorm_grad_parts(int T) { return norm_grad_parts(T, kNormGradRows); }
+
+// A workgroup adds its rows one behind another in fp32, each addition off by up to 2^-24 of what there is: never more
+// than kNormGradChain rows, so that 2^25 rows are no further off than 2^16 (with 512 workgroups for all up to 2^-10
+// of the sum; and short rows in too few wavefronts: 131072 x 1024 217 us, 360 then).
+int norm_grad_parts(int T, int rows) {
+  const int few = std::min(kNormGradBlocks, std::max(64, (T + rows - 1) / rows));
   return T <= 64 ? T : std::max(few, (T + kNormGradChain - 1) / kNormGradChain);
 }
 

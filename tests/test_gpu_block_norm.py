@@ -306,6 +306,19 @@ def test_block_norm_grad_row_sums_past_24_bits(moe, d):
         assert np.array_equal(dpre.cpu().numpy(), n[0]) and np.array_equal(dpost.cpu().numpy(), n[0])
 
 
+@pytest.mark.parametrize("T", [63, 64, 65, 127, 128, 129, 130, 1023, 1024, 1025, 1026])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+def test_block_norm_grad_row_shares(moe, T, gate):
+    """As many workgroups as rows, one with two, and full ones beside one that is not."""
+    d = 72
+    x, h, dy, dh = (_bf16(T, d, seed=i) for i in range(4))
+    pre, post, gate = _bf16(d, seed=5), _bf16(d, seed=6), _gate(gate, T, d)
+    a = (dy, x, h, pre, dh, post, gate, 0.5, 0.25)
+    out = moe.block_norm_grad(*a)
+    check_grad(dy, dh, x, h, pre, post, gate, 0.5, 0.25, out)
+    assert moe.lib().moe_block_norm_grad_workspace_bytes(T, d) >= 8 * d * min(T, 64)
+
+
 @pytest.mark.parametrize("T", [8192, 65536, 65537, 300000, 2 ** 21 + 5, 2 ** 25 - 1])
 @pytest.mark.parametrize("token", [False, True])
 def test_block_norm_grad_sums_over_long_columns(moe, T, token):
