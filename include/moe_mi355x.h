@@ -380,8 +380,8 @@ typedef struct moe_scoring {
 /* Route by scores: c_e = s_e + bias_e (bias, for balance, takes part in the selection only); topk_ids[t] =
  * the k experts with the largest c among the top_groups best groups, descending, ties to the lower id (of
  * groups: to the lower group); topk_w[t][j] = scale * s_j, renormalised scale * s_j / sum_i s_i (0 where that
- * sum is 0).  The selection is that of scores in 64 bits; without a bias experts are compared by their
- * logits, whose order the scores have.
+ * sum is 0).  Scores are worked out in 64 bits, for the selection as for the weights, which are rounded once;
+ * without a bias experts are compared by their logits, whose order the scores have.
  * An expert whose logit is -inf is masked: its score is 0 and it comes behind every expert with a finite c
  * or c = +inf, whatever its bias; where fewer than k others are left (a row may be masked whole) the lowest
  * masked ids fill up, with weight 0.  The lowest finite float is a number like others.  A NaN logit or bias,

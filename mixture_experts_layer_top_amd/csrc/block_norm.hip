@@ -11,7 +11,7 @@
 // Bound by HBM: x, h, dy and dh are read once and dx, dr written once, 12 bytes a value; H stays in fp32
 // registers between the two norms. 8192 x 7168 takes 156 us (4.5 TB/s; a copy runs at 5.1), with a gate per token
 // 190 us (16 bytes a value, 4.9 TB/s). Few rows are bound by their chain of loads and two reductions instead:
-// 7.6 us for one row of 7168. Loading the next row ahead, loads past the caches and more or fewer workgroups than
+// 8.1 us for one row of 7168. Loading the next row ahead, loads past the caches and more or fewer workgroups than
 // four wavefronts per SIMD gave nothing.
 #include <algorithm>
 #include <type_traits>

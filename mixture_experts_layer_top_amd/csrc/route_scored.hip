@@ -14,11 +14,13 @@
 // 16 lanes per token sort the experts in fp32 (route_scored_kernel); what fp32 cannot decide, scores that lie as
 // near as 2^-30 in some row of a large batch and rows with masked or non-finite logits, is decided in 64 bits,
 // since which expert is selected is a result: among the token's candidates, or by a wavefront over the whole row
-// (route_exact).
+// (route_exact).  Weights are worked out in 64 bits and rounded once.
 //
 // Bound by one token's chain of some thousand dependent instructions, which two wavefronts per SIMD (8192 tokens)
-// do not hide, not by HBM: 8192 tokens of 256 experts in 8 groups take 9.5 us, without groups and bias 5.4
-// (moe_route's wavefront per token 9.7), where their 8.9 MB take 2 us; 32768 of 384 19 us (2.8 TB/s), one token 4.9.
+// do not hide, not by HBM: 8192 tokens of 256 experts in 8 groups take 8.4 to 11.3 us, by how many need 64 bits, without
+// groups and bias 5.5 (moe_route's wavefront per token 9.7), where their 8.9 MB take 2 us; 32768 of 384 21 us (2.5
+// TB/s), one token 5.0.  Groups that 16 lanes do not share out go to route_exact at once: 60 experts in 6 groups 12
+// us, 380 in 2, whose groups two lanes of 64 walk, 92.
 // The gradient writes all of dlogits and reads no more than k values per token, but for a softmax over all
 // experts: 8192 x 256 4.5 us and 5.9.
 #include "kernels.h"
@@ -198,9 +200,9 @@ __global__ __launch_bounds__(64) void route_exact_kernel(const float* __restrict
 //
 // Lane i of a token holds experts i v .. i v + v - 1 (v = ceil(E / 16)) and their c in fp32.  A key is c's
 // place below the row's largest, 1 to 2^23 - 1, above the expert's complement, 511 - e, in 9 bits: unsigned order is
-// c's order and ties go to the lower id, so one register carries an expert through the sort, and 0 is no expert.  Each lane keeps its eight
-// largest keys in order (one med3 per place and key), then four exchanges with other lanes merge the lists
-// (the larger of each with the other's reversed, and a bitonic sort of eight).
+// c's order and ties go to the lower id, so one register carries an expert through the sort, and 0 is no expert.
+// Each lane keeps its eight largest keys in order (one med3 per place and key), then four exchanges with other lanes
+// merge the lists (the larger of each with the other's reversed, and a bitonic sort of eight).
 //
 // fp32 and 23 bits do not decide everything.  Where two of the first k + 1 keys are nearer than their errors (a row
 // in some hundred), the first nine are compared again in 64 bits, a lane each.  Where that cannot help (the
