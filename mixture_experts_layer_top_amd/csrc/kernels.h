@@ -254,8 +254,6 @@ hipError_t launch_gemm_i8(const void* xq, const float* xs, int M, const void* wq
 hipError_t launch_quant_i8(const void* x, bool f32, int T, int d, uint8_t* q, float* qs,
                            hipStream_t s);
 
-// RMS norm (fmt: 0 bf16 only, 1 e4m3 per 128, 2 e4m3 with E8M0 per 32, 3 int8 rows) and its gradient
-// (part: rmsnorm_grad_parts(T) rows of d partial sums, unused when dw is null).
 // What a block's output passes before the residual is added (null pointers: no such step).
 struct BlockIn {
   const void* post;  // weight of the norm behind the block, [d]
@@ -263,13 +261,14 @@ struct BlockIn {
   int gate_rows;
   float rs, bs;
 };
-// b: a block norm (x is the block's output, res the residual, which it needs), else null.
+// RMS norm (fmt: 0 bf16 only, 1 e4m3 per 128, 2 e4m3 with E8M0 per 32, 3 int8 rows) and its gradient
+// (part: rmsnorm_grad_parts(T) rows of d partial sums, unused when dw is null).  b: a block norm (x is the block's output, res the residual, which it needs), else null.
 hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float eps, int T, int d,
                           int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s,
                           const BlockIn* b = nullptr);
 constexpr int kNormGradBlocks = 512;
-constexpr int kNormGradRows = 3;      // per workgroup, until there are that many
-constexpr int kNormGradChain = 128;   // and no more than these: more workgroups then
+constexpr int kNormGradRows = 3;     // per workgroup, until there are that many
+constexpr int kNormGradChain = 128;  // and no more than these: more workgroups then
 int norm_grad_parts(int T, int rows);
 int rmsnorm_grad_parts(int T);
 hipError_t launch_rmsnorm_grad(const void* dy, const void* dh, const void* h, const void* w,

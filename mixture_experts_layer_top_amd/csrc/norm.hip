@@ -25,7 +25,8 @@ namespace moe {
 
 namespace {
 
-// hv: the block's output x in, the new residual stream h out; rv: the residual.
+// hv: the block's output x in, the new residual stream h out; rv: the residual.  fp32, with a root that is rounded
+// once.  (All of it in fp64 took 5.1 us for one row of 7168, 4.3 as it is, and 92 us for 8192, 87 as it is.)
 template <int R, int V>
 __device__ __forceinline__ void block_stream(uint4 (&hv)[V], const uint4 (&rv)[V], const BlockIn& b, float eps,
                                              double inv_d, int i, int nvec, size_t base,
@@ -50,7 +51,7 @@ __device__ __forceinline__ void block_stream(uint4 (&hv)[V], const uint4 (&rv)[V
       if (i + R * s < nvec) sum[0] += (double)p;
     }
     row_reduce<R>(sum, red[0], SumOp{});
-    rstd = row_rstd(sum[0], inv_d, eps);
+    rstd = row_rstd_once(sum[0], inv_d, eps);
     if (!row_in_range(sum[0], inv_d, eps)) {  // (the same in all threads of the row)
       sum[0] = 0.0;
 #pragma unroll

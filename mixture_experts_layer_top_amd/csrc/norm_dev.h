@@ -32,6 +32,11 @@ __device__ __forceinline__ bool row_in_range(double sum, double inv_d, float eps
 __device__ __forceinline__ float row_rstd(double sum, double inv_d, float eps) {
   return 1.0f / sqrtf(float(sum * inv_d) + eps);
 }
+// The same rounded once instead of four times: the instruction's root, and a Newton step in fp64.
+__device__ __forceinline__ float row_rstd_once(double sum, double inv_d, float eps) {
+  const double m = fma(sum, inv_d, (double)eps), r = (double)__builtin_amdgcn_rsqf((float)m);
+  return (float)fma(0.5 * r, fma(-m * r, r, 1.0), r);
+}
 // The same of any row, from squares summed in fp64 (which bf16's never leave): for a small row the value
 // over 2^32, which kSmallRow times the row's values make good; NaN for a row that holds an infinity or
 // NaN, so that the whole row shows it (and for a zero row without eps, 0 / 0).

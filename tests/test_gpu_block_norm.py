@@ -351,6 +351,23 @@ def test_block_norm_grad_of_many_rows(moe, T, d, gate):
             assert (np.abs(f64(g) - ref[name]) <= ref["e_" + name] * (G + 178 * 2.0 ** -24)).all(), name
 
 
+@pytest.mark.parametrize("T,d", [(1000, 256), (30000, 64), (1100, 7168)])
+def test_block_norm_root_is_rounded_once(moe, T, d):
+    """Whole numbers without eps, whose mean squares are exact where d is a power of two: h = bf16(fp32(x root)), bit
+    for bit, with the one fp32 number that is nearest to the root (rows where that is a close call, 2^-40, aside)."""
+    rng = np.random.default_rng(d)
+    v = rng.integers(-200, 201, (T, d))
+    x = torch.from_numpy(v.astype(np.float32)).to(torch.bfloat16).cuda()
+    one, zero = torch.ones(d, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(x)
+    h = moe.block_norm(x, zero, one, one, None, 0.0, 1.0, 0.0)[0]
+    root = 1 / np.sqrt((v ** 2).sum(1, keepdims=True) / np.float64(d))
+    near = root.astype(np.float32)
+    gap = np.abs(np.abs(root - near) / np.spacing(near) - 0.5)  # (from a half step)
+    sure = (gap > 2.0 ** -16)[:, 0]
+    want = torch.from_numpy(v.astype(np.float32) * near).to(torch.bfloat16)
+    assert sure.mean() > 0.99 and torch.equal(h.cpu()[sure], want[sure])
+
+
 def test_block_norm_past_32_bit_offsets(moe):
     """More than 2^32 bytes per tensor: every fourth row is the same row."""
     d = 7168
