@@ -17,7 +17,7 @@
 // (route_exact).  Weights are worked out in 64 bits and rounded once.
 //
 // Bound by one token's chain of some thousand dependent instructions, which two wavefronts per SIMD (8192 tokens)
-// do not hide, not by HBM: 8192 tokens of 256 experts in 8 groups take 8.4 to 11.3 us, by how many need 64 bits, without
+// do not hide, not by HBM: 8192 tokens of 256 experts in 8 groups take 8.3 to 12.9 us, by how many need 64 bits, without
 // groups and bias 5.5 (moe_route's wavefront per token 9.7), where their 8.9 MB take 2 us; 32768 of 384 21 us (2.5
 // TB/s), one token 5.0.  Groups that 16 lanes do not share out go to route_exact at once: 60 experts in 6 groups 12
 // us, 380 in 2, whose groups two lanes of 64 walk, 92.
