@@ -86,9 +86,9 @@ __device__ __forceinline__ float squares(const uint4& v) {
 }
 
 // A row's sums in fp64, the same in every thread and in a fixed order: row_reduce's, but that all rows of 16
-// lanes pass theirs on through LDS, where the r-th row of each wavefront joins those of value r: one exchange among lanes
-// for all values (4096 x 2048 33.6 us; with row_reduce in fp64 37.0, in fp32 32.9).  red: NA * R / 16 values of its
-// own for every call.
+// lanes pass theirs on through LDS, and the r-th row of each wavefront joins those of value r: one exchange among
+// lanes for all values (4096 x 2048 33.6 us; with row_reduce in fp64 37.0, in fp32 32.9).  red: NA * R / 16 values
+// of its own for every call.
 template <int R, int NA>
 __device__ __forceinline__ void row_sums(double (&v)[NA], double* red) {
   static_assert(NA <= 4, "a row of lanes per value");

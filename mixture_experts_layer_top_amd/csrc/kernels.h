@@ -262,7 +262,8 @@ struct BlockIn {
   float rs, bs;
 };
 // RMS norm (fmt: 0 bf16 only, 1 e4m3 per 128, 2 e4m3 with E8M0 per 32, 3 int8 rows) and its gradient
-// (part: rmsnorm_grad_parts(T) rows of d partial sums, unused when dw is null).  b: a block norm (x is the block's output, res the residual, which it needs), else null.
+// (part: rmsnorm_grad_parts(T) rows of d partial sums, unused when dw is null).
+// b: a block norm (x is the block's output, res the residual, which it needs), else null.
 hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float eps, int T, int d,
                           int fmt, void* h_out, void* y, void* q, void* qs, hipStream_t s,
                           const BlockIn* b = nullptr);

@@ -568,8 +568,8 @@ hipError_t launch_route_scored(const float* logits, const float* bias, int T, in
     kernel<<<(unsigned)T, 64, 0, s>>>(logits, bias, E, k, p, ids, w);
     return hipGetLastError();
   }
-  // Whole vectors wherever a lane's experts are some of them (8192 tokens, with and
-  // without: 192 experts 6.0 us and 8.5, 320 8.0 and 13.8, 448 9.5 and 17.3).
+  // Whole vectors wherever a lane's experts are some of them (8192 tokens, with and without: 192 experts 6.0 us and 8.5,
+  // 320 8.0 and 13.8, 448 9.5 and 17.3).
   using Kernel = decltype(&route_scored_kernel<4, true>);
   static constexpr Kernel kVec[] = {
       &route_scored_kernel<4, true>,  &route_scored_kernel<8, true>,  &route_scored_kernel<12, true>,
